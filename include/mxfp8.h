@@ -703,6 +703,120 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
                                          void* stream);
 
 /*
+ * The few tokens of a decoding step. The calls below read every weight once
+ * for a handful of rows; the activations stay bf16 and only the weights are
+ * block-scaled, so each weight is expanded exactly (an E2M1 or E4M3 element
+ * times its scale fits bf16) and products are summed in fp32.
+ *
+ * mx_gemv_fp4 / mx_gemv_nvfp4 -- y[m, n] = x[m, k] . W[n, k]^T with W in the
+ * rowwise layout of mx_quantize_fp4 (one E8M0 scale per 32 values) or
+ * mx_quantize_nvfp4 (one E4M3 scale per 16 values and the tensor's amax): the
+ * products with 4-bit weights of "TransformerEngine-accelerated Llama 3
+ * training with native PyTorch training loop" (Quantized Training), for one
+ * row or a few. mx_gemm_fp4 / mx_gemm_nvfp4 take 4-bit rows x as well and are
+ * the calls for many rows; these two are made for m up to 64 and read W again
+ * for every further 64 rows.
+ *   x        bf16 [m, k], consecutive rows ldx elements apart (ldx >= k where
+ *            m > 1, ldx % 8 == 0), 16-byte aligned.
+ *   w, w_s   codes [n, k/2], scales [n, k/32] (E8M0, codes 0 .. 254) or
+ *            [n, k/16] (E4M3); w 16-byte, NVFP4 scales 2-byte aligned.
+ *   w_amax   device fp32, the weight's amax from mx_quantize_nvfp4.
+ *   y        [m, n] row-major, bf16 (rounded once, to nearest even) or fp32.
+ * Rows of x do not mix: an infinity or NaN in one row stays in that row. Sums
+ * have one order for a given shape, so results repeat bit for bit. m or n zero
+ * is a no-op. Errors: MX_EINVAL (null pointers, y_dtype), MX_ESHAPE (negative
+ * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EUNSUPPORTED
+ * (m > 65536, n > 2^30, k > 2^24), MX_EHIP.
+ */
+MX_API mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
+                             int64_t k, void* y, mx_dtype y_dtype, void* stream);
+MX_API mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s,
+                               const float* w_amax, int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype,
+                               void* stream);
+
+/*
+ * grouped_mlp_decode -- the whole MoE MLP of a few tokens, from the router's
+ * choices to the summed output: dispatch, GroupedLinear -> ScaledSwiGLU ->
+ * GroupedLinear and combine (article items 1 and 3) without split_sizes, row
+ * copies or host work. With e = topk_idx[t, j] and w = topk_w[t, j]:
+ *     [g | u] = W1_e x_t;  A = w * silu(g) * u;  y[t] = sum over j of W2_e A
+ * g, u and the sums are fp32; A enters the second product as the sum of two
+ * bf16 numbers (16 significant bits); y is rounded once. The tokens stay bf16
+ * (grouped_mlp_fwd casts them to the weights' format instead).
+ *   dims       num_experts, rows = TOKENS (not routed rows), hidden, ffn.
+ *   topk       choices per token; rows * topk <= MX_DECODE_MAX_ENTRIES.
+ *   w_format   MX_W_BF16: w1 [E, 2F, H], w2 [E, H, F] bf16, scales NULL.
+ *              MX_W_MXFP8 / MX_W_MXFP4: rowwise codes of the same matrices
+ *              (mx_quantize / mx_quantize_fp4 of [E * 2F, H] and [E * H, F])
+ *              and their scales [E, 2F, H/32] and [E, H, F/32].
+ *   x          bf16 [tokens, H];  y bf16 [tokens, H], not overlapping x.
+ *   topk_idx   int32 [tokens, topk]; an entry outside [0, num_experts) is
+ *              dropped. A token whose entries are all dropped gets zeros. An
+ *              expert named twice by one token counts with the sum of its
+ *              weights.
+ *   topk_w     f32 [tokens, topk] or NULL (all 1).
+ *   workspace  grouped_mlp_decode_sizes bytes, 256-byte aligned.
+ * Requires H % 32 == 0 and F % 32 == 0. Only weights of experts that a token
+ * names are read. Results repeat bit for bit. tokens == 0 is a no-op.
+ * Errors: MX_EINVAL, MX_ESHAPE, MX_EALIGN (x, w1, w2, y 16-byte, topk_idx and
+ * topk_w 4-byte, workspace 256-byte), MX_EWORKSPACE, MX_EUNSUPPORTED (more
+ * than MX_MAX_GROUPS experts, too many entries, H or F above 2^24), MX_EHIP.
+ */
+typedef enum mx_weight_format { MX_W_BF16 = 0, MX_W_MXFP8 = 1, MX_W_MXFP4 = 2 } mx_weight_format;
+#define MX_DECODE_MAX_ENTRIES 1024
+MX_API mx_status grouped_mlp_decode_sizes(const mx_mlp_dims* dims, int32_t topk, size_t* workspace);
+MX_API mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_weight_format w_format, const void* x,
+                                    const int32_t* topk_idx, const float* topk_w, const void* w1,
+                                    const uint8_t* w1_s, const void* w2, const uint8_t* w2_s, void* y,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mx_moe_route -- the router's choice: the topk experts of each token and
+ * their routing weights, as mx_moe_dispatch and grouped_mlp_decode take them
+ * (each token activates a few experts: the article's Dense vs. MoE scaling).
+ *   logits       bf16 or f32 (logits_dtype) [tokens, num_experts].
+ *   bias         f32 [num_experts] added to the logits for the choice only
+ *                (load balancing), or NULL.
+ *   renormalize  1: weights are the softmax over the chosen logits; 0: the
+ *                softmax over all experts, at the chosen ones.
+ *   topk_idx     int32 [tokens, topk], by key = logit + bias (fp32) from the
+ *                largest; equal keys go to the lower expert. An expert whose
+ *                key is -inf or NaN is shut: never chosen, and no part of any
+ *                softmax. Where fewer than topk are open the rest is -1 (which
+ *                the dispatch drops) with weight 0.
+ *   topk_w       f32 [tokens, topk].
+ *   lse          f32 [tokens]: log of the sum of exp(logit) over the open
+ *                experts (-inf if none), for the backward and for a z-loss.
+ * Logits of +inf are outside the contract (weights are then unspecified, the
+ * choices are not).
+ *
+ * mx_moe_route_bwd -- gradient of the weights with respect to the logits:
+ *     dlogits[t, e] = p_e ([e chosen as j] dw[t, j] - sum_i w[t, i] dw[t, i])
+ * with p the softmax the weights came from. bias gets no gradient.
+ *   dw       f32 [tokens, topk] with perm NULL; or, with perm int32 [tokens,
+ *            topk] from mx_moe_dispatch, f32 [dw_rows] per routed row (the
+ *            dprobs of grouped_mlp_bwd): dw[t, j] is then dw[perm[t, j]], and 0
+ *            where perm lies outside [0, dw_rows). dw_rows is the number of
+ *            elements of dw in both cases.
+ *   topk_idx, topk_w, lse   from the forward (lse is read with renormalize 0
+ *            only, and may be NULL otherwise).
+ *   dlogits  [tokens, num_experts] of logits_dtype, all of it written; logits
+ *            may be NULL with renormalize 1.
+ * Both: tokens == 0 is a no-op. Errors: MX_EINVAL (null pointers, dtype),
+ * MX_ESHAPE (negative sizes, topk outside 1 .. num_experts, dw_rows not
+ * tokens * topk without perm), MX_EALIGN, MX_EUNSUPPORTED (num_experts >
+ * MX_MAX_GROUPS, topk > MX_ROUTE_MAX_TOPK, tokens > 2^27), MX_EHIP.
+ */
+#define MX_ROUTE_MAX_TOPK 16
+MX_API mx_status mx_moe_route(const void* logits, mx_dtype logits_dtype, const float* bias, int64_t tokens,
+                              int32_t num_experts, int32_t topk, int32_t renormalize, int32_t* topk_idx,
+                              float* topk_w, float* lse, void* stream);
+MX_API mx_status mx_moe_route_bwd(const void* logits, mx_dtype logits_dtype, const float* bias,
+                                  const int32_t* topk_idx, const float* topk_w, const float* lse, const float* dw,
+                                  int64_t dw_rows, const int32_t* perm, int64_t tokens, int32_t num_experts,
+                                  int32_t topk, int32_t renormalize, void* dlogits, void* stream);
+
+/*
  * mx_set_stage_events -- optional per-stage timing of the fused MLP calls
  * (observability only; the results are the same). While events are set, the
  * fused MLP calls run every stage on the caller's stream in order, without

@@ -23,6 +23,8 @@ __all__ = [
     "MAX_GROUPS", "padded_sizes", "quantize", "grouped_gemm", "mlp_sizes",
     "grouped_mlp_fwd", "grouped_mlp_bwd", "GroupedMLP", "MLPState", "MLPRunner",
     "set_stage_events", "FWD_STAGES", "BWD_STAGES", "mx_quantize_fp4", "mx_gemm_fp4", "mx_grouped_gemm_fp4",
+    "mx_gemv_fp4", "mx_gemv_nvfp4", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
+    "mx_moe_route", "mx_moe_route_bwd", "MoERoute",
 ]
 
 FWD_STAGES = ("quantize_x", "quantize_w1", "quantize_w2", "gemm1_swiglu", "gemm2")
@@ -153,6 +155,18 @@ def load() -> ctypes.CDLL:
     L.mx_gemm_nvfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
     L.mx_grouped_gemm_nvfp4.restype = ctypes.c_int
     L.mx_grouped_gemm_nvfp4.argtypes = [vp, vp, vp, vp, vp, vp, p64, i32, i64, i64, vp, i32, vp]
+    L.mx_gemv_fp4.restype = ctypes.c_int
+    L.mx_gemv_fp4.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.mx_gemv_nvfp4.restype = ctypes.c_int
+    L.mx_gemv_nvfp4.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.grouped_mlp_decode_sizes.restype = ctypes.c_int
+    L.grouped_mlp_decode_sizes.argtypes = [ctypes.POINTER(_Dims), i32, ctypes.POINTER(sz)]
+    L.grouped_mlp_decode.restype = ctypes.c_int
+    L.grouped_mlp_decode.argtypes = [ctypes.POINTER(_Dims), i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.mx_moe_route.restype = ctypes.c_int
+    L.mx_moe_route.argtypes = [vp, i32, vp, i64, i32, i32, i32, vp, vp, vp, vp]
+    L.mx_moe_route_bwd.restype = ctypes.c_int
+    L.mx_moe_route_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, vp, i64, i32, i32, i32, vp, vp]
     L.mx_device_copy.restype = ctypes.c_int
     L.mx_device_copy.argtypes = [vp, vp, i64, vp]
     L.mx_set_stage_events.restype = ctypes.c_int
@@ -919,6 +933,189 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
     return y
 
 
+# ---- the few tokens of a decoding step, and the router around the experts
+
+MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
+
+
+def _expect_on(who, dev, items):
+    """items: (tensor or None, shape, dtype, name, optional), as _expect_all,
+    and all on the device `dev` (one pass, for calls of a few microseconds)."""
+    for t, shape, dtype, name, optional in items:
+        if t is None:
+            if not optional:
+                raise ValueError(f"{who}: {name} is required")
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape:
+            raise ValueError(f"{who}: {name} must be a {dtype} tensor of shape {shape}, got "
+                             + (f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else str(type(t))))
+        if not t.is_contiguous() or not t.is_cuda or t.device != dev:
+            raise ValueError(f"{who}: {name} must be contiguous and on the device of the first argument ({dev})")
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current: its current stream,
+    or the given one."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+
+
+def _gemv(who, fn, group, x, w_q, w_s, amax, out_dtype, out, stream):
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{who}: x must be a 2-D bfloat16 CUDA tensor")
+    if not isinstance(w_q, torch.Tensor) or w_q.dim() != 2:
+        raise ValueError(f"{who}: w_q must be [n, k/2]")
+    m, k = x.shape
+    n = w_q.shape[0]
+    if k > 1 and m > 0 and x.stride(1) != 1:
+        raise ValueError(f"{who}: the elements of a row of x must be consecutive")
+    if out is not None:
+        out_dtype = out.dtype if isinstance(out, torch.Tensor) else None
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{who}: the output is bfloat16 or float32")
+    dev = x.device
+    items = [(w_q, (n, k // 2), torch.uint8, "w_q", False), (w_s, (n, k // group), torch.uint8, "w_s", False)]
+    if group == 16:
+        items.append((amax, (1,), torch.float32, "w_amax", False))
+    if out is not None:
+        items.append((out, (m, n), out_dtype, "out", False))
+    _expect_on(who, dev, items)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    weight = (w_q.data_ptr(), w_s.data_ptr()) if group == 32 else (w_q.data_ptr(), w_s.data_ptr(), amax.data_ptr())
+    _call(fn, dev, stream, x.data_ptr(), x.stride(0) if m > 1 else (k + 7) // 8 * 8, *weight, m, n, k, out.data_ptr(),
+          MX_F32 if out_dtype == torch.float32 else MX_BF16)
+    return out
+
+
+def mx_gemv_fp4(x, w_q, w_s, out_dtype=torch.bfloat16, out=None, stream=None):
+    """y [m, n] = x . W^T (mx_gemv_fp4): x bf16 [m, k] (its rows may be apart,
+    by a multiple of 8 elements), W rowwise MXFP4 as mx_quantize_fp4 makes it
+    (w_q [n, k/2], w_s [n, k/32]). Made for m up to 64; bf16 or fp32."""
+    return _gemv("mx_gemv_fp4", load().mx_gemv_fp4, 32, x, w_q, w_s, None, out_dtype, out, stream)
+
+
+def mx_gemv_nvfp4(x, w_q, w_s, w_amax, out_dtype=torch.bfloat16, out=None, stream=None):
+    """mx_gemv_fp4 on NVFP4 weights as mx_quantize_nvfp4 makes them (w_q
+    [n, k/2], w_s [n, k/16], w_amax [1]); k a multiple of 32."""
+    return _gemv("mx_gemv_nvfp4", load().mx_gemv_nvfp4, 16, x, w_q, w_s, w_amax, out_dtype, out, stream)
+
+
+def mlp_decode_workspace_bytes(E: int, T: int, H: int, F: int, topk: int) -> int:
+    """Bytes of the workspace of grouped_mlp_decode."""
+    n = ctypes.c_size_t()
+    _check(load().grouped_mlp_decode_sizes(ctypes.byref(_dims(E, T, H, F)), topk, ctypes.byref(n)))
+    return n.value
+
+
+def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out=None, workspace=None, stream=None):
+    """The MoE MLP of a few tokens, from the router's choices to the summed
+    output (grouped_mlp_decode): x bf16 [T, H], topk_idx int32 [T, k], topk_w
+    fp32 [T, k] or None (all 1) -> y bf16 [T, H]. Weights: bf16 w1 [E, 2F, H]
+    and w2 [E, H, F]; or rowwise codes with scales w1_s [E, 2F, H/32] and w2_s
+    [E, H, F/32]: uint8 w1 [E, 2F, H], w2 [E, H, F] (MXFP8) or w1 [E, 2F, H/2],
+    w2 [E, H, F/2] (MXFP4). T * k <= 1024."""
+    who = "grouped_mlp_decode"
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{who}: x must be a [T, H] CUDA tensor")
+    if not all(isinstance(t, torch.Tensor) and t.dim() == d for t, d in ((topk_idx, 2), (w1, 3), (w2, 3))):
+        raise ValueError(f"{who}: topk_idx must be [T, k], w1 and w2 [E, rows, cols] tensors")
+    T, H = x.shape
+    k = topk_idx.shape[1]
+    E, F2, cols = w1.shape
+    F = F2 // 2
+    if w1.dtype == torch.bfloat16:
+        fmt, pack = MX_W_BF16, 1
+    elif cols == H:
+        fmt, pack = MX_W_MXFP8, 1
+    else:
+        fmt, pack = MX_W_MXFP4, 2
+    wt = torch.bfloat16 if fmt == MX_W_BF16 else torch.uint8
+    dev = x.device
+    items = [(x, (T, H), torch.bfloat16, "x", False), (topk_idx, (T, k), torch.int32, "topk_idx", False),
+             (topk_w, (T, k), torch.float32, "topk_w", True), (w1, (E, 2 * F, H // pack), wt, "w1", False),
+             (w2, (E, H, F // pack), wt, "w2", False), (out, (T, H), torch.bfloat16, "out", True)]
+    if fmt == MX_W_BF16:
+        if w1_s is not None or w2_s is not None:
+            raise ValueError(f"{who}: bf16 weights have no scales")
+    else:
+        items += [(w1_s, (E, 2 * F, H // 32), torch.uint8, "w1_s", False),
+                  (w2_s, (E, H, F // 32), torch.uint8, "w2_s", False)]
+    _expect_on(who, dev, items)
+    L = load()
+    dims = ctypes.byref(_Dims(E, T, H, F))
+    need = ctypes.c_size_t()
+    _check(L.grouped_mlp_decode_sizes(dims, k, ctypes.byref(need)))
+    if workspace is None:
+        workspace = _byte_buffer(need.value, dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.device != dev \
+            or not workspace.is_contiguous():
+        raise ValueError(f"{who}: workspace must be a contiguous uint8 tensor on {dev}")
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _call(L.grouped_mlp_decode, dev, stream, dims, k, fmt, x.data_ptr(), topk_idx.data_ptr(), _address(topk_w),
+          w1.data_ptr(), _address(w1_s), w2.data_ptr(), _address(w2_s), out.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return out
+
+
+def _logits_dtype(who, logits):
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or not logits.is_cuda or not logits.is_contiguous() \
+            or logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{who}: logits must be a contiguous [T, E] bfloat16 or float32 CUDA tensor")
+    return MX_F32 if logits.dtype == torch.float32 else MX_BF16
+
+
+def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=None):
+    """The router's choice (mx_moe_route): logits [T, E] bf16 or fp32, bias
+    fp32 [E] (for the choice only) or None -> (topk_idx int32 [T, topk],
+    topk_w fp32 [T, topk], lse fp32 [T]), as mx_moe_dispatch and
+    grouped_mlp_decode take them."""
+    dt = _logits_dtype("mx_moe_route", logits)
+    T, E = logits.shape
+    dev = logits.device
+    if bias is not None:
+        _expect_on("mx_moe_route", dev, [(bias, (E,), torch.float32, "bias", False)])
+    idx = torch.empty((T, max(int(topk), 0)), dtype=torch.int32, device=dev)
+    w = torch.empty(idx.shape, dtype=torch.float32, device=dev)
+    lse = torch.empty((T,), dtype=torch.float32, device=dev)
+    _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, _address(bias), T, E, topk, int(bool(renormalize)),
+          idx.data_ptr(), w.data_ptr(), lse.data_ptr())
+    return idx, w, lse
+
+
+def mx_moe_route_bwd(logits, topk_idx, topk_w, lse, dw, perm=None, bias=None, renormalize: bool = True, stream=None):
+    """Gradient of mx_moe_route's weights with respect to the logits
+    (mx_moe_route_bwd): dw fp32 [T, k], or with perm (of mx_moe_dispatch) the
+    dprobs fp32 [rows] of the grouped MLP's backward -> dlogits [T, E] of the
+    logits' dtype. renormalize and bias as in the forward."""
+    who = "mx_moe_route_bwd"
+    dt = _logits_dtype(who, logits)
+    T, E = logits.shape
+    dev = logits.device
+    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
+        raise ValueError(f"{who}: topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    if perm is not None and (not isinstance(dw, torch.Tensor) or dw.dim() != 1):
+        raise ValueError(f"{who}: with perm, dw holds one value per routed row")
+    _expect_on(who, dev, [(topk_idx, (T, k), torch.int32, "topk_idx", False),
+                          (topk_w, (T, k), torch.float32, "topk_w", False), (lse, (T,), torch.float32, "lse", False),
+                          (perm, (T, k), torch.int32, "perm", True), (bias, (E,), torch.float32, "bias", True),
+                          (dw, (T, k) if perm is None else tuple(dw.shape), torch.float32, "dw", False)])
+    dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, _address(bias), topk_idx.data_ptr(),
+          topk_w.data_ptr(), lse.data_ptr(), dw.data_ptr(), dw.numel(), _address(perm), T, E, k,
+          int(bool(renormalize)), dlogits.data_ptr())
+    return dlogits
+
+
 _event_arrays = []   # keeps the handle arrays alive while the library holds them
 
 
@@ -1119,3 +1316,22 @@ class GroupedMLP(torch.autograd.Function):
         dx, dprobs, dw1, dw2 = grouped_mlp_bwd(dy.contiguous(), probs, ctx.state,
                                                want_dprobs=probs is not None)
         return dx, dprobs, dw1, dw2, None
+
+
+class MoERoute(torch.autograd.Function):
+    """topk_idx, topk_w = MoERoute.apply(logits, topk, bias, renormalize): the
+    router's choice with the gradient of the weights for the logits."""
+
+    @staticmethod
+    def forward(ctx, logits, topk, bias=None, renormalize=True):
+        logits = logits.contiguous()
+        idx, w, lse = mx_moe_route(logits, topk, bias=bias, renormalize=renormalize)
+        ctx.save_for_backward(logits, bias, idx, w, lse)
+        ctx.renormalize = renormalize
+        ctx.mark_non_differentiable(idx)
+        return idx, w
+
+    @staticmethod
+    def backward(ctx, _, dw):
+        logits, bias, idx, w, lse = ctx.saved_tensors
+        return mx_moe_route_bwd(logits, idx, w, lse, dw.contiguous(), bias=bias, renormalize=ctx.renormalize), None, None, None

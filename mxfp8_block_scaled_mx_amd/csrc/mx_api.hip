@@ -1830,3 +1830,169 @@ mx_status grouped_mlp_bwd_fp4_cached(const mx_mlp_dims* dims, const int64_t* spl
 }
 
 }  // extern "C"
+
+namespace {
+
+mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s,
+                    const float* w_amax, int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* stream) {
+  if (y_dtype != MX_BF16 && y_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad output dtype %d", who, (int)y_dtype);
+  if (m < 0 || n < 0 || k <= 0 || k % 32)
+    return fail(MX_ESHAPE, "%s: need m, n >= 0 and k a positive multiple of 32", who);
+  if (ldx % 8 || (m > 1 && ldx < k)) return fail(MX_ESHAPE, "%s: ldx %lld must be a multiple of 8 and at least k", who, (long long)ldx);
+  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30 and k <= 2^24", who);
+  if (m == 0 || n == 0) return MX_OK;
+  const bool nv = fmt == mx::WF_NVFP4;
+  if (!x || !w || !w_s || !y || (nv && !w_amax)) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(x, 16) || !aligned(w, 16) || (nv && (!aligned(w_s, 2) || !aligned(w_amax, 4))) ||
+      !aligned(y, y_dtype == MX_F32 ? 4 : 2))
+    return fail(MX_EALIGN, "%s: x and w must be 16-byte aligned, NVFP4 scales 2-byte, y by its element", who);
+  mx::GemvArgs a;
+  a.x = x; a.ldx = ldx; a.w = w; a.ws = w_s; a.amax = w_amax;
+  a.m = m; a.n = n; a.k = k; a.y = y; a.y_f32 = y_dtype == MX_F32;
+  hipError_t e = mx::launch_gemv(fmt, a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+// Sizes of a decode call: MX_OK and the byte offsets of its workspace.
+struct DecodeLayout {
+  size_t act_hi, act_lo, total;
+};
+mx_status decode_layout(const mx_mlp_dims* d, int32_t topk, DecodeLayout* L, const char* who) {
+  if (!d) return fail(MX_EINVAL, "%s: null dims", who);
+  if (d->num_experts < 1) return fail(MX_EINVAL, "%s: need at least one expert", who);
+  if (d->num_experts > mx::kMaxGroups)
+    return fail(MX_EUNSUPPORTED, "%s: %d experts exceeds the maximum %d", who, d->num_experts, mx::kMaxGroups);
+  if (d->rows < 0 || d->hidden <= 0 || d->hidden % 32 || d->ffn <= 0 || d->ffn % 32)
+    return fail(MX_ESHAPE, "%s: need tokens >= 0, hidden and ffn positive multiples of 32", who);
+  if (topk < 1) return fail(MX_ESHAPE, "%s: topk must be at least 1", who);
+  if (d->rows > MX_DECODE_MAX_ENTRIES || d->rows * topk > MX_DECODE_MAX_ENTRIES)
+    return fail(MX_EUNSUPPORTED, "%s: %lld tokens x top-%d is above %d entries (use mx_moe_dispatch and grouped_mlp_fwd)",
+                who, (long long)d->rows, topk, MX_DECODE_MAX_ENTRIES);
+  if (d->hidden > ((int64_t)1 << 24) || d->ffn > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: hidden or ffn above 2^24", who);
+  size_t cur = 0;
+  L->act_hi = take(cur, (size_t)(d->rows * topk * d->ffn * 2));
+  L->act_lo = take(cur, (size_t)(d->rows * topk * d->ffn * 2));
+  L->total = cur;
+  return MX_OK;
+}
+
+mx_status route_checks(const char* who, mx_dtype dt, int64_t tokens, int32_t E, int32_t topk) {
+  if (dt != MX_BF16 && dt != MX_F32) return fail(MX_EINVAL, "%s: bad logits dtype %d", who, (int)dt);
+  if (tokens < 0) return fail(MX_ESHAPE, "%s: need tokens >= 0", who);
+  if (E < 1 || topk < 1 || topk > E) return fail(MX_ESHAPE, "%s: need 1 <= topk <= num_experts", who);
+  if (E > mx::kMaxGroups) return fail(MX_EUNSUPPORTED, "%s: %d experts exceeds the maximum %d", who, E, mx::kMaxGroups);
+  if (topk > MX_ROUTE_MAX_TOPK) return fail(MX_EUNSUPPORTED, "%s: topk %d exceeds the maximum %d", who, topk, MX_ROUTE_MAX_TOPK);
+  if (tokens > ((int64_t)1 << 27)) return fail(MX_EUNSUPPORTED, "%s: more than 2^27 tokens", who);
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
+                      int64_t k, void* y, mx_dtype y_dtype, void* stream) {
+  g_err[0] = 0;
+  return gemv_impl("mx_gemv_fp4", mx::WF_MXFP4, x, ldx, w, w_s, nullptr, m, n, k, y, y_dtype, stream);
+}
+
+mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, const float* w_amax,
+                        int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* stream) {
+  g_err[0] = 0;
+  return gemv_impl("mx_gemv_nvfp4", mx::WF_NVFP4, x, ldx, w, w_s, w_amax, m, n, k, y, y_dtype, stream);
+}
+
+mx_status grouped_mlp_decode_sizes(const mx_mlp_dims* dims, int32_t topk, size_t* workspace) {
+  g_err[0] = 0;
+  DecodeLayout L;
+  mx_status st = decode_layout(dims, topk, &L, "grouped_mlp_decode_sizes");
+  if (st != MX_OK) return st;
+  if (workspace) *workspace = L.total;
+  return MX_OK;
+}
+
+mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_weight_format w_format, const void* x,
+                             const int32_t* topk_idx, const float* topk_w, const void* w1, const uint8_t* w1_s,
+                             const void* w2, const uint8_t* w2_s, void* y, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  g_err[0] = 0;
+  const char* who = "grouped_mlp_decode";
+  DecodeLayout L;
+  mx_status st = decode_layout(dims, topk, &L, who);
+  if (st != MX_OK) return st;
+  if (w_format != MX_W_BF16 && w_format != MX_W_MXFP8 && w_format != MX_W_MXFP4)
+    return fail(MX_EINVAL, "%s: bad weight format %d", who, (int)w_format);
+  if (dims->rows == 0) return MX_OK;
+  if (!x || !topk_idx || !w1 || !w2 || !y || !workspace) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if ((w_format == MX_W_BF16) != (w1_s == nullptr) || (w_format == MX_W_BF16) != (w2_s == nullptr))
+    return fail(MX_EINVAL, "%s: w1_s and w2_s go with block-scaled weights, and only with them", who);
+  if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4) || !aligned(workspace, 256))
+    return fail(MX_EALIGN, "%s: x, w1, w2 and y must be 16-byte, topk_idx and topk_w 4-byte, workspace 256-byte aligned", who);
+  if (workspace_bytes < L.total)
+    return fail(MX_EWORKSPACE, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, L.total);
+  mx::DecodeArgs a;
+  a.x = reinterpret_cast<const uint8_t*>(x);
+  a.topk_idx = topk_idx; a.topk_w = topk_w;
+  a.w1 = reinterpret_cast<const uint8_t*>(w1); a.w1_s = w1_s;
+  a.w2 = reinterpret_cast<const uint8_t*>(w2); a.w2_s = w2_s;
+  a.act_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act_hi);
+  a.act_lo = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act_lo);
+  a.y = y;
+  a.tokens = (int32_t)dims->rows; a.topk = topk; a.experts = dims->num_experts;
+  a.hidden = (int32_t)dims->hidden; a.ffn = (int32_t)dims->ffn;
+  hipError_t e = mx::launch_decode((int)w_format, a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+mx_status mx_moe_route(const void* logits, mx_dtype logits_dtype, const float* bias, int64_t tokens,
+                       int32_t num_experts, int32_t topk, int32_t renormalize, int32_t* topk_idx, float* topk_w,
+                       float* lse, void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_moe_route";
+  mx_status st = route_checks(who, logits_dtype, tokens, num_experts, topk);
+  if (st != MX_OK) return st;
+  if (tokens == 0) return MX_OK;
+  if (!logits || !topk_idx || !topk_w || !lse) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(logits, logits_dtype == MX_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4) || !aligned(lse, 4))
+    return fail(MX_EALIGN, "%s: arrays must be aligned to their elements", who);
+  mx::RouteArgs a;
+  a.logits = logits; a.f32 = logits_dtype == MX_F32; a.bias = bias; a.tokens = tokens; a.experts = num_experts;
+  a.topk = topk; a.renorm = renormalize != 0; a.topk_idx = topk_idx; a.topk_w = topk_w; a.lse = lse;
+  hipError_t e = mx::launch_route(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+mx_status mx_moe_route_bwd(const void* logits, mx_dtype logits_dtype, const float* bias, const int32_t* topk_idx,
+                           const float* topk_w, const float* lse, const float* dw, int64_t dw_rows,
+                           const int32_t* perm, int64_t tokens, int32_t num_experts, int32_t topk,
+                           int32_t renormalize, void* dlogits, void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_moe_route_bwd";
+  mx_status st = route_checks(who, logits_dtype, tokens, num_experts, topk);
+  if (st != MX_OK) return st;
+  if (dw_rows < 0 || (perm == nullptr && dw_rows != tokens * topk))
+    return fail(MX_ESHAPE, "%s: dw has %lld elements, expected tokens * topk without perm", who, (long long)dw_rows);
+  if (tokens == 0) return MX_OK;
+  if (!topk_idx || !topk_w || (dw_rows > 0 && !dw) || !dlogits || (!renormalize && (!logits || !lse)))
+    return fail(MX_EINVAL, "%s: null pointer argument", who);
+  const int el = logits_dtype == MX_F32 ? 4 : 2;
+  if (!aligned(logits, el) || !aligned(dlogits, el) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(topk_w, 4) || !aligned(lse, 4) || !aligned(dw, 4) || !aligned(perm, 4))
+    return fail(MX_EALIGN, "%s: arrays must be aligned to their elements", who);
+  mx::RouteBwdArgs a;
+  a.logits = logits; a.f32 = logits_dtype == MX_F32; a.bias = bias; a.topk_idx = topk_idx; a.topk_w = topk_w;
+  a.lse = lse; a.dw = dw; a.perm = perm; a.dw_rows = dw_rows; a.tokens = tokens; a.experts = num_experts;
+  a.topk = topk; a.renorm = renormalize != 0; a.dlogits = dlogits;
+  hipError_t e = mx::launch_route_bwd(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+}  // extern "C"

@@ -146,6 +146,13 @@ __device__ __forceinline__ int xcd_remap(int bid, int total) {
   return (local / CHUNK) * round + xcd * CHUNK + local % CHUNK;
 }
 
+// The scale S of an NVFP4 tensor with largest magnitude amax: 448 * 6 / amax,
+// 1 for amax = 0, at most 2^64.
+__device__ __forceinline__ float nvfp4_tensor_scale(float amax) {
+  if (!(amax > 0.0f)) return 1.0f;
+  return fminf(2688.0f / amax, 18446744073709551616.0f);   // cap 2^64
+}
+
 // Compile-time loop: fn(std::integral_constant<int, i>) for i in [I, N). Keeps
 // register-array indices constant however large the body is.
 template <int I, int N, typename Fn>

@@ -480,11 +480,6 @@ hipError_t launch_swiglu_fp4_cast(bool backward, const Fp4SwigluArgs& sw, const 
 //   q   = E2M1 code of x * (S / E4M3(s_b)) (0, keeping the sign, when s_b = 0).
 // An element's value is E2M1(q) * E4M3(s_b) / S.
 
-__device__ __forceinline__ float nvfp4_tensor_scale(float amax) {
-  if (!(amax > 0.0f)) return 1.0f;
-  return fminf(2688.0f / amax, 18446744073709551616.0f);   // cap 2^64
-}
-
 // 16 values -> 8 code bytes (element 2i in the low nibble) and the E4M3
 // block-scale code.
 __device__ __forceinline__ uint32_t nvfp4_block(const float (&v)[16], float S, uint2& codes) {

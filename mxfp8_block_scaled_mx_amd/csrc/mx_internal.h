@@ -279,6 +279,67 @@ hipError_t launch_gemm_fp4_group_k(const uint8_t* a, const uint8_t* as, const ui
                                    const Fp4KGroups& gr, int64_t M, int64_t N, float* c, int32_t accumulate,
                                    hipStream_t stream);
 
+// Weight formats of the few-row products (mx_decode.hip).
+enum WeightFormat : int { WF_BF16 = MX_W_BF16, WF_MXFP8 = MX_W_MXFP8, WF_MXFP4 = MX_W_MXFP4, WF_NVFP4 = 3 };
+// y[m, n] = x[m, k] . W[n, k]^T: x bf16 with row stride ldx, W rowwise MXFP4
+// or NVFP4 (k % 32 == 0, sizes below 2^31), y bf16 or fp32 [m, n].
+struct GemvArgs {
+  const void* x;
+  int64_t ldx;
+  const uint8_t* w;
+  const uint8_t* ws;
+  const float* amax;                // NVFP4: the weight's tensor amax
+  int64_t m, n, k;
+  void* y;
+  int32_t y_f32;
+};
+hipError_t launch_gemv(int fmt, const GemvArgs& a, hipStream_t stream);
+// The MoE MLP of a few tokens (tokens * topk <= kDecodeMaxEntries).
+constexpr int kDecodeMaxEntries = MX_DECODE_MAX_ENTRIES;
+constexpr int kDecodeTokenChunk = 64;  // tokens of one workgroup of the second product
+struct DecodeArgs {
+  const uint8_t* x;                 // bf16 [tokens, hidden]
+  const int32_t* topk_idx;          // [tokens, topk]
+  const float* topk_w;              // [tokens, topk] or null
+  const uint8_t* w1;                // [experts, 2 ffn, hidden] codes
+  const uint8_t* w1_s;
+  const uint8_t* w2;                // [experts, hidden, ffn] codes
+  const uint8_t* w2_s;
+  uint16_t* act_hi;                 // bf16 [tokens * topk, ffn]: A's leading part
+  uint16_t* act_lo;                 // and what it leaves
+  void* y;                          // bf16 [tokens, hidden]
+  int32_t tokens, topk, experts, hidden, ffn;
+};
+hipError_t launch_decode(int fmt, const DecodeArgs& a, hipStream_t stream);
+
+// Router (mx_route.hip).
+struct RouteArgs {
+  const void* logits;               // bf16 or fp32 [tokens, experts]
+  int32_t f32;
+  const float* bias;                // [experts] or null
+  int64_t tokens;
+  int32_t experts, topk, renorm;
+  int32_t* topk_idx;                // [tokens, topk]
+  float* topk_w;                    // [tokens, topk]
+  float* lse;                       // [tokens]
+};
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+struct RouteBwdArgs {
+  const void* logits;
+  int32_t f32;
+  const float* bias;
+  const int32_t* topk_idx;
+  const float* topk_w;
+  const float* lse;
+  const float* dw;                  // [tokens, topk], or [dw_rows] read through perm
+  const int32_t* perm;              // [tokens, topk] or null
+  int64_t dw_rows;
+  int64_t tokens;
+  int32_t experts, topk, renorm;
+  void* dlogits;
+};
+hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t stream);
+
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kTileK = 128;

@@ -1,0 +1,181 @@
+"""The MoE MLP of a few tokens (grouped_mlp_decode) against the 64-bit form
+with derived elementwise bounds, for bf16, MXFP8 and MXFP4 weights, and the
+whole serving path: router's choice, then the few-token MLP ("Efficient MoE
+training for biological foundation models", Key technical approaches item 3)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import decode_ref as ref
+from tests.gpu_util import canaries_intact, guarded
+
+pytestmark = pytest.mark.gpu
+
+
+def _weights(mx, E, H, F, fmt, gen):
+    """(arguments of the call, w1 and w2 in float64)."""
+    w1 = (0.05 * torch.randn((E, 2 * F, H), generator=gen)).to(torch.bfloat16).cuda()
+    w2 = (0.05 * torch.randn((E, H, F), generator=gen)).to(torch.bfloat16).cuda()
+    if fmt == "bf16":
+        return (w1, w2, None, None), ref.f64(w1), ref.f64(w2)
+    out = []
+    for w in (w1, w2):
+        flat = w.view(-1, w.shape[-1])
+        if fmt == "mxfp8":
+            d = mx.quantize(flat, colwise=False)
+            q, s = d["q_row"], d["s_row"]
+        else:
+            q, s = mx.mx_quantize_fp4(flat)
+        val = ref.mxfp8 if fmt == "mxfp8" else ref.mxfp4
+        out.append((q.view(*w.shape[:2], -1), s.view(*w.shape[:2], -1),
+                    val(q.cpu().numpy(), s.cpu().numpy()).reshape(w.shape)))
+    return (out[0][0], out[1][0], out[0][1], out[1][1]), out[0][2], out[1][2]
+
+
+def _choices(rng, T, k, E):
+    return np.array([rng.permutation(E)[:k] for _ in range(T)], dtype=np.int32).reshape(T, k)
+
+
+def _check(mx, x, idx, wt, args, w1, w2, out=None):
+    y = mx.grouped_mlp_decode(x, torch.from_numpy(idx).cuda(), None if wt is None else torch.from_numpy(wt).cuda(),
+                              *args, out=out)
+    want, bound = ref.moe(ref.f64(x), idx, np.ones(idx.shape) if wt is None else wt.astype(np.float64), w1, w2)
+    err = np.abs(ref.f64(y) - want)
+    assert np.all(err <= bound), float(np.max(err / np.maximum(bound, 1e-300)))
+    return y
+
+
+CASES = [(1, 1, 1, 32, 32), (1, 2, 4, 64, 96), (3, 2, 4, 256, 512), (5, 2, 3, 160, 288), (8, 1, 2, 96, 64),
+         (9, 3, 5, 128, 160), (16, 2, 2, 64, 544), (17, 2, 8, 96, 128), (33, 1, 1, 64, 96), (40, 4, 4, 32, 32),
+         (64, 2, 8, 160, 96), (65, 2, 3, 64, 64), (100, 3, 4, 64, 32), (13, 6, 64, 64, 64), (4, 8, 128, 32, 32),
+         (128, 8, 128, 32, 64), (1, 64, 128, 64, 32)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,k,E,H,F", CASES)
+def test_against_the_definition(gpu_lib, fmt, T, k, E, H, F):
+    gen = torch.Generator().manual_seed(T * 100 + k + E + H + F)
+    rng = np.random.default_rng(T + E)
+    args, w1, w2 = _weights(gpu_lib, E, H, F, fmt, gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = _choices(rng, T, k, E)
+    wt = rng.uniform(0, 1, size=(T, k)).astype(np.float32)
+    buf, out = guarded((T, H), torch.bfloat16)
+    y = _check(gpu_lib, x, idx, wt, args, w1, w2, out=out)
+    assert canaries_intact(buf)
+    again = gpu_lib.grouped_mlp_decode(x, torch.from_numpy(idx).cuda(), torch.from_numpy(wt).cuda(), *args)
+    assert torch.equal(again.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [2, 37])
+def test_dropped_repeated_and_unweighted_choices(gpu_lib, T):
+    gen = torch.Generator().manual_seed(5)
+    rng = np.random.default_rng(6)
+    E, H, F, k = 5, 64, 96, 4
+    args, w1, w2 = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = rng.integers(0, E, size=(T, k)).astype(np.int32)           # an expert may come twice
+    idx[0] = [-1, E, 2 ** 31 - 1, -2 ** 31]                          # nothing left of this token
+    idx[1, 2] = -1
+    y = _check(gpu_lib, x, idx, None, args, w1, w2)
+    assert not y[0].any()
+    y = _check(gpu_lib, x, idx, rng.uniform(-1, 1, size=(T, k)).astype(np.float32), args, w1, w2)
+    assert not y[0].any()
+    none = gpu_lib.grouped_mlp_decode(x, torch.full((T, k), -1, dtype=torch.int32, device="cuda"), None, *args)
+    assert not none.any()
+    assert gpu_lib.grouped_mlp_decode(x[:0], torch.empty((0, k), dtype=torch.int32, device="cuda"), None, *args).shape == (0, H)
+
+
+def test_every_token_on_one_expert_and_unread_experts(gpu_lib):
+    """Experts that no token names may hold anything (here NaN codes)."""
+    gen = torch.Generator().manual_seed(8)
+    E, H, F, T = 4, 96, 64, 50
+    args, w1, w2 = _weights(gpu_lib, E, H, F, "mxfp8", gen)
+    for a in args[:2]:
+        a[[0, 1, 3]] = 0x7F
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = np.full((T, 1), 2, dtype=np.int32)
+    _check(gpu_lib, x, idx, None, args, np.nan_to_num(w1), np.nan_to_num(w2))
+
+
+def test_nonfinite_tokens_stay_apart(gpu_lib):
+    gen = torch.Generator().manual_seed(10)
+    rng = np.random.default_rng(11)
+    E, H, F, T, k = 3, 64, 64, 20, 2
+    args, _, _ = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = torch.from_numpy(_choices(rng, T, k, E)).cuda()
+    clean = gpu_lib.grouped_mlp_decode(x, idx, None, *args)
+    x[4, 7], x[9, 0] = float("nan"), float("inf")
+    got = gpu_lib.grouped_mlp_decode(x, idx, None, *args)
+    keep = [t for t in range(T) if t not in (4, 9)]
+    assert torch.equal(got[keep], clean[keep]) and torch.isnan(got[4]).all()
+
+
+def test_weights_past_four_gib(gpu_lib):
+    """The last of 128 experts lies past 2^32 bytes in w1 and past 2^31 elements."""
+    E, H, F = 128, 4096, 2304
+    w1 = torch.zeros((E, 2 * F, H), dtype=torch.bfloat16, device="cuda")
+    w2 = torch.zeros((E, H, F), dtype=torch.bfloat16, device="cuda")
+    assert w1.numel() * 2 > 1 << 32
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    w1[-1] = (0.05 * torch.randn((2 * F, H), generator=gen, device="cuda")).to(torch.bfloat16)
+    w2[-1] = (0.05 * torch.randn((H, F), generator=gen, device="cuda")).to(torch.bfloat16)
+    x = torch.randn((2, H), generator=gen, device="cuda").to(torch.bfloat16)
+    idx = torch.tensor([[127, 3], [5, 127]], dtype=torch.int32, device="cuda")
+    y = gpu_lib.grouped_mlp_decode(x, idx, None, w1, w2)
+    want, bound = ref.moe(ref.f64(x), np.zeros((2, 1), dtype=np.int32), np.ones((2, 1)), ref.f64(w1[-1:]), ref.f64(w2[-1:]))
+    assert np.all(np.abs(ref.f64(y) - want) <= bound)
+
+
+def test_on_a_stream_and_in_two_graphs_of_one_workspace(gpu_lib):
+    """Two captured calls share a workspace (run one after the other), with
+    new tokens and choices at every replay and eager work in between."""
+    gen = torch.Generator().manual_seed(12)
+    rng = np.random.default_rng(13)
+    E, H, F, T, k = 6, 128, 160, 12, 2
+    args, _, _ = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    ws = torch.empty(gpu_lib.mlp_decode_workspace_bytes(E, T, H, F, k), dtype=torch.uint8, device="cuda")
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = torch.from_numpy(_choices(rng, T, k, E)).cuda()
+    outs, graphs = [torch.empty((T, H), dtype=torch.bfloat16, device="cuda") for _ in range(2)], []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    want = gpu_lib.grouped_mlp_decode(x, idx, None, *args)
+    gpu_lib.grouped_mlp_decode(x, idx, None, *args, out=outs[0], stream=side)
+    side.synchronize()
+    assert torch.equal(outs[0], want)
+    for o in outs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gpu_lib.grouped_mlp_decode(x, idx, None, *args, out=o, workspace=ws)
+        graphs.append(g)
+    for i in range(4):
+        x.copy_(torch.randn((T, H), generator=gen))
+        idx.copy_(torch.from_numpy(_choices(rng, T, k, E)))
+        eager = gpu_lib.grouped_mlp_decode(x, idx, None, *args)
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, eager), i
+
+
+def test_route_then_decode(gpu_lib):
+    """Serving: logits -> choices and weights -> MLP, against the same in 64 bits."""
+    gen = torch.Generator().manual_seed(20)
+    E, H, F, T, k = 8, 128, 96, 11, 2
+    args, w1, w2 = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    logits = torch.randn((T, E), generator=gen).to(torch.bfloat16).cuda()
+    logits[3, 1:] = float("-inf")                                    # one expert open: the second choice is dropped
+    logits[6] = float("-inf")                                        # none
+    idx, w, _ = gpu_lib.mx_moe_route(logits, k)
+    y = gpu_lib.grouped_mlp_decode(x, idx, w, *args)
+    ridx, rw, _, rel, _ = ref.route(ref.f64(logits), None, k, True)
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    want, bound = ref.moe(ref.f64(x), ridx, rw, w1, w2)
+    # a weight that is off by rel moves its part of y by as much: |y| parts sum to what moe's terms bound
+    parts = sum(np.abs(ref.moe(ref.f64(x), ridx[:, j:j + 1], rw[:, j:j + 1], w1, w2)[0]) for j in range(k))
+    assert np.all(np.abs(ref.f64(y) - want) <= bound + 2 * rel * parts)
+    assert not y[6].any()
