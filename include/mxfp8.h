@@ -726,7 +726,7 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
  * have one order for a given shape, so results repeat bit for bit. m or n zero
  * is a no-op. Errors: MX_EINVAL (null pointers, y_dtype), MX_ESHAPE (negative
  * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EUNSUPPORTED
- * (m > 65536, n > 2^30, k > 2^24), MX_EHIP.
+ * (m > 65536, n > 2^30, k or ldx > 2^24), MX_EHIP.
  */
 MX_API mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
                              int64_t k, void* y, mx_dtype y_dtype, void* stream);
@@ -744,7 +744,7 @@ MX_API mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, con
  * bf16 numbers (16 significant bits); y is rounded once. The tokens stay bf16
  * (grouped_mlp_fwd casts them to the weights' format instead).
  *   dims       num_experts, rows = TOKENS (not routed rows), hidden, ffn.
- *   topk       choices per token; rows * topk <= MX_DECODE_MAX_ENTRIES.
+ *   topk       choices per token, at most 64; rows * topk <= MX_DECODE_MAX_ENTRIES.
  *   w_format   MX_W_BF16: w1 [E, 2F, H], w2 [E, H, F] bf16, scales NULL.
  *              MX_W_MXFP8 / MX_W_MXFP4: rowwise codes of the same matrices
  *              (mx_quantize / mx_quantize_fp4 of [E * 2F, H] and [E * H, F])
@@ -760,7 +760,8 @@ MX_API mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, con
  * names are read. Results repeat bit for bit. tokens == 0 is a no-op.
  * Errors: MX_EINVAL, MX_ESHAPE, MX_EALIGN (x, w1, w2, y 16-byte, topk_idx and
  * topk_w 4-byte, workspace 256-byte), MX_EWORKSPACE, MX_EUNSUPPORTED (more
- * than MX_MAX_GROUPS experts, too many entries, H or F above 2^24), MX_EHIP.
+ * than MX_MAX_GROUPS experts, topk, too many entries, H or F above 2^19),
+ * MX_EHIP.
  */
 typedef enum mx_weight_format { MX_W_BF16 = 0, MX_W_MXFP8 = 1, MX_W_MXFP4 = 2 } mx_weight_format;
 #define MX_DECODE_MAX_ENTRIES 1024

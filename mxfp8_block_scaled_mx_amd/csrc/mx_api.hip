@@ -1839,8 +1839,8 @@ mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const 
   if (m < 0 || n < 0 || k <= 0 || k % 32)
     return fail(MX_ESHAPE, "%s: need m, n >= 0 and k a positive multiple of 32", who);
   if (ldx % 8 || (m > 1 && ldx < k)) return fail(MX_ESHAPE, "%s: ldx %lld must be a multiple of 8 and at least k", who, (long long)ldx);
-  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24))
-    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30 and k <= 2^24", who);
+  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24) || ldx > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30, k <= 2^24 and ldx <= 2^24", who);
   if (m == 0 || n == 0) return MX_OK;
   const bool nv = fmt == mx::WF_NVFP4;
   if (!x || !w || !w_s || !y || (nv && !w_amax)) return fail(MX_EINVAL, "%s: null pointer argument", who);
@@ -1857,7 +1857,7 @@ mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const 
 
 // Sizes of a decode call: MX_OK and the byte offsets of its workspace.
 struct DecodeLayout {
-  size_t act_hi, act_lo, total;
+  size_t plan, act, total;
 };
 mx_status decode_layout(const mx_mlp_dims* d, int32_t topk, DecodeLayout* L, const char* who) {
   if (!d) return fail(MX_EINVAL, "%s: null dims", who);
@@ -1867,14 +1867,15 @@ mx_status decode_layout(const mx_mlp_dims* d, int32_t topk, DecodeLayout* L, con
   if (d->rows < 0 || d->hidden <= 0 || d->hidden % 32 || d->ffn <= 0 || d->ffn % 32)
     return fail(MX_ESHAPE, "%s: need tokens >= 0, hidden and ffn positive multiples of 32", who);
   if (topk < 1) return fail(MX_ESHAPE, "%s: topk must be at least 1", who);
+  if (topk > 64) return fail(MX_EUNSUPPORTED, "%s: topk %d exceeds the maximum 64", who, topk);
   if (d->rows > MX_DECODE_MAX_ENTRIES || d->rows * topk > MX_DECODE_MAX_ENTRIES)
     return fail(MX_EUNSUPPORTED, "%s: %lld tokens x top-%d is above %d entries (use mx_moe_dispatch and grouped_mlp_fwd)",
                 who, (long long)d->rows, topk, MX_DECODE_MAX_ENTRIES);
-  if (d->hidden > ((int64_t)1 << 24) || d->ffn > ((int64_t)1 << 24))
-    return fail(MX_EUNSUPPORTED, "%s: hidden or ffn above 2^24", who);
+  if (d->hidden > mx::kDecodeMaxDim || d->ffn > mx::kDecodeMaxDim)
+    return fail(MX_EUNSUPPORTED, "%s: hidden or ffn above 2^19", who);
   size_t cur = 0;
-  L->act_hi = take(cur, (size_t)(d->rows * topk * d->ffn * 2));
-  L->act_lo = take(cur, (size_t)(d->rows * topk * d->ffn * 2));
+  L->plan = take(cur, (size_t)(cdiv(d->rows, mx::kDecodeTokenChunk) * mx::kDecodePlanBytes));
+  L->act = take(cur, (size_t)(d->rows * topk * d->ffn * 4));
   L->total = cur;
   return MX_OK;
 }
@@ -1939,8 +1940,8 @@ mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_weight_fo
   a.topk_idx = topk_idx; a.topk_w = topk_w;
   a.w1 = reinterpret_cast<const uint8_t*>(w1); a.w1_s = w1_s;
   a.w2 = reinterpret_cast<const uint8_t*>(w2); a.w2_s = w2_s;
-  a.act_hi = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act_hi);
-  a.act_lo = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act_lo);
+  a.plan = reinterpret_cast<uint8_t*>(workspace) + L.plan;
+  a.act = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act);
   a.y = y;
   a.tokens = (int32_t)dims->rows; a.topk = topk; a.experts = dims->num_experts;
   a.hidden = (int32_t)dims->hidden; a.ffn = (int32_t)dims->ffn;

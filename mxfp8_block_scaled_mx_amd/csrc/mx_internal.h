@@ -294,9 +294,12 @@ struct GemvArgs {
   int32_t y_f32;
 };
 hipError_t launch_gemv(int fmt, const GemvArgs& a, hipStream_t stream);
-// The MoE MLP of a few tokens (tokens * topk <= kDecodeMaxEntries).
+// The MoE MLP of a few tokens (tokens * topk <= kDecodeMaxEntries; hidden and
+// ffn at most kDecodeMaxDim, so that the kernels' row offsets fit 32 bits).
 constexpr int kDecodeMaxEntries = MX_DECODE_MAX_ENTRIES;
-constexpr int kDecodeTokenChunk = 64;  // tokens of one workgroup of the second product
+constexpr int64_t kDecodeMaxDim = 1 << 19;
+constexpr int kDecodeTokenChunk = 64;  // tokens that one workgroup sees
+constexpr int kDecodePlanBytes = 4 * (2 * MX_MAX_GROUPS + 2) + 2 * kDecodeMaxEntries;   // per chunk of tokens
 struct DecodeArgs {
   const uint8_t* x;                 // bf16 [tokens, hidden]
   const int32_t* topk_idx;          // [tokens, topk]
@@ -305,8 +308,8 @@ struct DecodeArgs {
   const uint8_t* w1_s;
   const uint8_t* w2;                // [experts, hidden, ffn] codes
   const uint8_t* w2_s;
-  uint16_t* act_hi;                 // bf16 [tokens * topk, ffn]: A's leading part
-  uint16_t* act_lo;                 // and what it leaves
+  void* plan;                       // kDecodePlanBytes per chunk of tokens
+  uint16_t* act;                    // bf16 [tokens * topk, 2, ffn]: A's leading part and what it leaves
   void* y;                          // bf16 [tokens, hidden]
   int32_t tokens, topk, experts, hidden, ffn;
 };
