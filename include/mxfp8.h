@@ -722,17 +722,21 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
  *            [n, k/16] (E4M3); w 16-byte, NVFP4 scales 2-byte aligned.
  *   w_amax   device fp32, the weight's amax from mx_quantize_nvfp4.
  *   y        [m, n] row-major, bf16 (rounded once, to nearest even) or fp32.
+ *   workspace  mx_gemv_sizes bytes (0 for m <= 16 and for many shapes above;
+ *            then it may be NULL), 256-byte aligned.
  * Rows of x do not mix: an infinity or NaN in one row stays in that row. Sums
  * have one order for a given shape, so results repeat bit for bit. m or n zero
  * is a no-op. Errors: MX_EINVAL (null pointers, y_dtype), MX_ESHAPE (negative
- * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EUNSUPPORTED
+ * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EWORKSPACE, MX_EUNSUPPORTED
  * (m > 65536, n > 2^30, k or ldx > 2^24), MX_EHIP.
  */
+MX_API mx_status mx_gemv_sizes(int64_t m, int64_t n, int64_t k, size_t* workspace);
 MX_API mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
-                             int64_t k, void* y, mx_dtype y_dtype, void* stream);
+                             int64_t k, void* y, mx_dtype y_dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
 MX_API mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s,
                                const float* w_amax, int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype,
-                               void* stream);
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * grouped_mlp_decode -- the whole MoE MLP of a few tokens, from the router's

@@ -14,6 +14,7 @@ training for biological foundation models", Key technical approaches item 3).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -23,7 +24,7 @@ __all__ = [
     "MAX_GROUPS", "padded_sizes", "quantize", "grouped_gemm", "mlp_sizes",
     "grouped_mlp_fwd", "grouped_mlp_bwd", "GroupedMLP", "MLPState", "MLPRunner",
     "set_stage_events", "FWD_STAGES", "BWD_STAGES", "mx_quantize_fp4", "mx_gemm_fp4", "mx_grouped_gemm_fp4",
-    "mx_gemv_fp4", "mx_gemv_nvfp4", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
+    "mx_gemv_fp4", "mx_gemv_nvfp4", "gemv_workspace_bytes", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
     "mx_moe_route", "mx_moe_route_bwd", "MoERoute",
 ]
 
@@ -155,10 +156,12 @@ def load() -> ctypes.CDLL:
     L.mx_gemm_nvfp4.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
     L.mx_grouped_gemm_nvfp4.restype = ctypes.c_int
     L.mx_grouped_gemm_nvfp4.argtypes = [vp, vp, vp, vp, vp, vp, p64, i32, i64, i64, vp, i32, vp]
+    L.mx_gemv_sizes.restype = ctypes.c_int
+    L.mx_gemv_sizes.argtypes = [i64, i64, i64, ctypes.POINTER(sz)]
     L.mx_gemv_fp4.restype = ctypes.c_int
-    L.mx_gemv_fp4.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.mx_gemv_fp4.argtypes = [vp, i64, vp, vp, i64, i64, i64, vp, i32, vp, sz, vp]
     L.mx_gemv_nvfp4.restype = ctypes.c_int
-    L.mx_gemv_nvfp4.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.mx_gemv_nvfp4.argtypes = [vp, i64, vp, vp, vp, i64, i64, i64, vp, i32, vp, sz, vp]
     L.grouped_mlp_decode_sizes.restype = ctypes.c_int
     L.grouped_mlp_decode_sizes.argtypes = [ctypes.POINTER(_Dims), i32, ctypes.POINTER(sz)]
     L.grouped_mlp_decode.restype = ctypes.c_int
@@ -933,86 +936,120 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
     return y
 
 
-# ---- the few tokens of a decoding step, and the router around the experts
+# ---- the few tokens of a decoding step, and the router around the experts.
+# These calls take a few microseconds on the GPU, so their checks are one
+# expression per tensor.
 
 MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
 
 
-def _expect_on(who, dev, items):
-    """items: (tensor or None, shape, dtype, name, optional), as _expect_all,
-    and all on the device `dev` (one pass, for calls of a few microseconds)."""
-    for t, shape, dtype, name, optional in items:
-        if t is None:
-            if not optional:
-                raise ValueError(f"{who}: {name} is required")
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape:
-            raise ValueError(f"{who}: {name} must be a {dtype} tensor of shape {shape}, got "
-                             + (f"{t.dtype} {tuple(t.shape)}" if isinstance(t, torch.Tensor) else str(type(t))))
-        if not t.is_contiguous() or not t.is_cuda or t.device != dev:
-            raise ValueError(f"{who}: {name} must be contiguous and on the device of the first argument ({dev})")
+def _fits(t, shape, dtype, dev):
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _misfit(who, name, t, shape, dtype, dev):
+    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else str(type(t))
+    return ValueError(f"{who}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {got}")
+
+
+def _need(who, name, t, shape, dtype, dev):
+    if not _fits(t, shape, dtype, dev):
+        raise _misfit(who, name, t, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _opt(who, name, t, shape, dtype, dev):
+    return None if t is None else _need(who, name, t, shape, dtype, dev)
+
+
+def _scratch(who, workspace, nbytes, dev):
+    """The caller's workspace, or a new one of nbytes (None where none is needed)."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == dev
+            and workspace.is_contiguous()):
+        raise ValueError(f"{who}: workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
 
 
 def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with the tensors' device current: its current stream,
-    or the given one."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+    """fn(*args, stream) with the tensors' device current: on its current
+    stream, or the given one."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, (stream if stream is not None else torch.cuda.current_stream()).cuda_stream))
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
+    if status != 0:
+        _check(status)
 
 
-def _gemv(who, fn, group, x, w_q, w_s, amax, out_dtype, out, stream):
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or x.dim() != 2 or not x.is_cuda:
+@functools.lru_cache(maxsize=4096)
+def gemv_workspace_bytes(m: int, n: int, k: int) -> int:
+    """Bytes of the workspace of mx_gemv_fp4 and mx_gemv_nvfp4 (0: none)."""
+    nbytes = ctypes.c_size_t()
+    _check(load().mx_gemv_sizes(m, n, k, ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+def _gemv(who, fn, group, x, w_q, w_s, amax, out_dtype, out, workspace, stream):
+    if not (isinstance(x, torch.Tensor) and x.dtype is torch.bfloat16 and x.dim() == 2 and x.is_cuda):
         raise ValueError(f"{who}: x must be a 2-D bfloat16 CUDA tensor")
-    if not isinstance(w_q, torch.Tensor) or w_q.dim() != 2:
+    if not (isinstance(w_q, torch.Tensor) and w_q.dim() == 2):
         raise ValueError(f"{who}: w_q must be [n, k/2]")
     m, k = x.shape
     n = w_q.shape[0]
-    if k > 1 and m > 0 and x.stride(1) != 1:
+    dev = x.device
+    ldx, inner = x.stride()
+    if inner != 1 and k > 1 and m > 0:
         raise ValueError(f"{who}: the elements of a row of x must be consecutive")
+    weight = [_need(who, "w_q", w_q, (n, k // 2), torch.uint8, dev), _need(who, "w_s", w_s, (n, k // group), torch.uint8, dev)]
+    if group == 16:
+        weight.append(_need(who, "w_amax", amax, (1,), torch.float32, dev))
     if out is not None:
         out_dtype = out.dtype if isinstance(out, torch.Tensor) else None
-    if out_dtype not in (torch.bfloat16, torch.float32):
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
         raise ValueError(f"{who}: the output is bfloat16 or float32")
-    dev = x.device
-    items = [(w_q, (n, k // 2), torch.uint8, "w_q", False), (w_s, (n, k // group), torch.uint8, "w_s", False)]
-    if group == 16:
-        items.append((amax, (1,), torch.float32, "w_amax", False))
-    if out is not None:
-        items.append((out, (m, n), out_dtype, "out", False))
-    _expect_on(who, dev, items)
+    nbytes = gemv_workspace_bytes(m, n, k)
+    if nbytes or workspace is not None:
+        workspace = _scratch(who, workspace, nbytes, dev)
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    weight = (w_q.data_ptr(), w_s.data_ptr()) if group == 32 else (w_q.data_ptr(), w_s.data_ptr(), amax.data_ptr())
-    _call(fn, dev, stream, x.data_ptr(), x.stride(0) if m > 1 else (k + 7) // 8 * 8, *weight, m, n, k, out.data_ptr(),
-          MX_F32 if out_dtype == torch.float32 else MX_BF16)
+        y = out.data_ptr()
+    else:
+        y = _need(who, "out", out, (m, n), out_dtype, dev)
+    _call(fn, dev, stream, x.data_ptr(), ldx if m > 1 else (k + 7) // 8 * 8, *weight, m, n, k, y,
+          MX_F32 if out_dtype is torch.float32 else MX_BF16, None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel())
     return out
 
 
-def mx_gemv_fp4(x, w_q, w_s, out_dtype=torch.bfloat16, out=None, stream=None):
+def mx_gemv_fp4(x, w_q, w_s, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [m, n] = x . W^T (mx_gemv_fp4): x bf16 [m, k] (its rows may be apart,
     by a multiple of 8 elements), W rowwise MXFP4 as mx_quantize_fp4 makes it
-    (w_q [n, k/2], w_s [n, k/32]). Made for m up to 64; bf16 or fp32."""
-    return _gemv("mx_gemv_fp4", load().mx_gemv_fp4, 32, x, w_q, w_s, None, out_dtype, out, stream)
+    (w_q [n, k/2], w_s [n, k/32]). Made for m up to 64; bf16 or fp32.
+    workspace: uint8, gemv_workspace_bytes(m, n, k) (allocated when None)."""
+    return _gemv("mx_gemv_fp4", load().mx_gemv_fp4, 32, x, w_q, w_s, None, out_dtype, out, workspace, stream)
 
 
-def mx_gemv_nvfp4(x, w_q, w_s, w_amax, out_dtype=torch.bfloat16, out=None, stream=None):
+def mx_gemv_nvfp4(x, w_q, w_s, w_amax, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """mx_gemv_fp4 on NVFP4 weights as mx_quantize_nvfp4 makes them (w_q
     [n, k/2], w_s [n, k/16], w_amax [1]); k a multiple of 32."""
-    return _gemv("mx_gemv_nvfp4", load().mx_gemv_nvfp4, 16, x, w_q, w_s, w_amax, out_dtype, out, stream)
+    return _gemv("mx_gemv_nvfp4", load().mx_gemv_nvfp4, 16, x, w_q, w_s, w_amax, out_dtype, out, workspace, stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def _decode_dims(E, T, H, F, k):
+    """The dims of a decode call and its workspace's bytes."""
+    dims, nbytes = _Dims(E, T, H, F), ctypes.c_size_t()
+    _check(load().grouped_mlp_decode_sizes(ctypes.byref(dims), k, ctypes.byref(nbytes)))
+    return dims, nbytes.value
 
 
 def mlp_decode_workspace_bytes(E: int, T: int, H: int, F: int, topk: int) -> int:
     """Bytes of the workspace of grouped_mlp_decode."""
-    n = ctypes.c_size_t()
-    _check(load().grouped_mlp_decode_sizes(ctypes.byref(_dims(E, T, H, F)), topk, ctypes.byref(n)))
-    return n.value
+    return _decode_dims(E, T, H, F, topk)[1]
 
 
 def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out=None, workspace=None, stream=None):
@@ -1023,54 +1060,44 @@ def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out
     [E, H, F/32]: uint8 w1 [E, 2F, H], w2 [E, H, F] (MXFP8) or w1 [E, 2F, H/2],
     w2 [E, H, F/2] (MXFP4). T * k <= 1024."""
     who = "grouped_mlp_decode"
-    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not x.is_cuda:
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda):
         raise ValueError(f"{who}: x must be a [T, H] CUDA tensor")
-    if not all(isinstance(t, torch.Tensor) and t.dim() == d for t, d in ((topk_idx, 2), (w1, 3), (w2, 3))):
-        raise ValueError(f"{who}: topk_idx must be [T, k], w1 and w2 [E, rows, cols] tensors")
+    if not (isinstance(topk_idx, torch.Tensor) and topk_idx.dim() == 2 and isinstance(w1, torch.Tensor) and w1.dim() == 3):
+        raise ValueError(f"{who}: topk_idx must be [T, k] and w1 [E, rows, cols]")
+    dev = x.device
     T, H = x.shape
     k = topk_idx.shape[1]
     E, F2, cols = w1.shape
     F = F2 // 2
-    if w1.dtype == torch.bfloat16:
-        fmt, pack = MX_W_BF16, 1
-    elif cols == H:
-        fmt, pack = MX_W_MXFP8, 1
-    else:
-        fmt, pack = MX_W_MXFP4, 2
-    wt = torch.bfloat16 if fmt == MX_W_BF16 else torch.uint8
-    dev = x.device
-    items = [(x, (T, H), torch.bfloat16, "x", False), (topk_idx, (T, k), torch.int32, "topk_idx", False),
-             (topk_w, (T, k), torch.float32, "topk_w", True), (w1, (E, 2 * F, H // pack), wt, "w1", False),
-             (w2, (E, H, F // pack), wt, "w2", False), (out, (T, H), torch.bfloat16, "out", True)]
-    if fmt == MX_W_BF16:
+    if w1.dtype is torch.bfloat16:
+        fmt, H1, F1, wt = MX_W_BF16, H, F, torch.bfloat16
         if w1_s is not None or w2_s is not None:
             raise ValueError(f"{who}: bf16 weights have no scales")
+        s1 = s2 = None
     else:
-        items += [(w1_s, (E, 2 * F, H // 32), torch.uint8, "w1_s", False),
-                  (w2_s, (E, H, F // 32), torch.uint8, "w2_s", False)]
-    _expect_on(who, dev, items)
-    L = load()
-    dims = ctypes.byref(_Dims(E, T, H, F))
-    need = ctypes.c_size_t()
-    _check(L.grouped_mlp_decode_sizes(dims, k, ctypes.byref(need)))
-    if workspace is None:
-        workspace = _byte_buffer(need.value, dev)
-    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or workspace.device != dev \
-            or not workspace.is_contiguous():
-        raise ValueError(f"{who}: workspace must be a contiguous uint8 tensor on {dev}")
+        fmt, H1, F1, wt = (MX_W_MXFP8, H, F, torch.uint8) if cols == H else (MX_W_MXFP4, H // 2, F // 2, torch.uint8)
+        s1 = _need(who, "w1_s", w1_s, (E, 2 * F, H // 32), torch.uint8, dev)
+        s2 = _need(who, "w2_s", w2_s, (E, H, F // 32), torch.uint8, dev)
+    args = (_need(who, "x", x, (T, H), torch.bfloat16, dev), _need(who, "topk_idx", topk_idx, (T, k), torch.int32, dev),
+            _opt(who, "topk_w", topk_w, (T, k), torch.float32, dev), _need(who, "w1", w1, (E, 2 * F, H1), wt, dev), s1,
+            _need(who, "w2", w2, (E, H, F1), wt, dev), s2)
+    dims, nbytes = _decode_dims(E, T, H, F, k)
+    workspace = _scratch(who, workspace, nbytes, dev)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    _call(L.grouped_mlp_decode, dev, stream, dims, k, fmt, x.data_ptr(), topk_idx.data_ptr(), _address(topk_w),
-          w1.data_ptr(), _address(w1_s), w2.data_ptr(), _address(w2_s), out.data_ptr(), workspace.data_ptr(),
-          workspace.numel())
+        y = out.data_ptr()
+    else:
+        y = _need(who, "out", out, (T, H), torch.bfloat16, dev)
+    _call(load().grouped_mlp_decode, dev, stream, ctypes.byref(dims), k, fmt, *args, y,
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out
 
 
 def _logits_dtype(who, logits):
-    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or not logits.is_cuda or not logits.is_contiguous() \
-            or logits.dtype not in (torch.bfloat16, torch.float32):
+    if not (isinstance(logits, torch.Tensor) and logits.dim() == 2 and logits.is_cuda and logits.is_contiguous()
+            and logits.dtype in (torch.bfloat16, torch.float32)):
         raise ValueError(f"{who}: logits must be a contiguous [T, E] bfloat16 or float32 CUDA tensor")
-    return MX_F32 if logits.dtype == torch.float32 else MX_BF16
+    return MX_F32 if logits.dtype is torch.float32 else MX_BF16
 
 
 def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=None):
@@ -1081,12 +1108,12 @@ def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=
     dt = _logits_dtype("mx_moe_route", logits)
     T, E = logits.shape
     dev = logits.device
-    if bias is not None:
-        _expect_on("mx_moe_route", dev, [(bias, (E,), torch.float32, "bias", False)])
-    idx = torch.empty((T, max(int(topk), 0)), dtype=torch.int32, device=dev)
-    w = torch.empty(idx.shape, dtype=torch.float32, device=dev)
+    b = _opt("mx_moe_route", "bias", bias, (E,), torch.float32, dev)
+    k = topk if topk > 0 else 0
+    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
     lse = torch.empty((T,), dtype=torch.float32, device=dev)
-    _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, _address(bias), T, E, topk, int(bool(renormalize)),
+    _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, b, T, E, topk, 1 if renormalize else 0,
           idx.data_ptr(), w.data_ptr(), lse.data_ptr())
     return idx, w, lse
 
@@ -1100,19 +1127,18 @@ def mx_moe_route_bwd(logits, topk_idx, topk_w, lse, dw, perm=None, bias=None, re
     dt = _logits_dtype(who, logits)
     T, E = logits.shape
     dev = logits.device
-    if not isinstance(topk_idx, torch.Tensor) or topk_idx.dim() != 2:
-        raise ValueError(f"{who}: topk_idx must be [T, k]")
+    if not (isinstance(topk_idx, torch.Tensor) and topk_idx.dim() == 2 and isinstance(dw, torch.Tensor)):
+        raise ValueError(f"{who}: topk_idx must be [T, k] and dw a tensor")
     k = topk_idx.shape[1]
-    if perm is not None and (not isinstance(dw, torch.Tensor) or dw.dim() != 1):
+    if perm is not None and dw.dim() != 1:
         raise ValueError(f"{who}: with perm, dw holds one value per routed row")
-    _expect_on(who, dev, [(topk_idx, (T, k), torch.int32, "topk_idx", False),
-                          (topk_w, (T, k), torch.float32, "topk_w", False), (lse, (T,), torch.float32, "lse", False),
-                          (perm, (T, k), torch.int32, "perm", True), (bias, (E,), torch.float32, "bias", True),
-                          (dw, (T, k) if perm is None else tuple(dw.shape), torch.float32, "dw", False)])
+    args = (_opt(who, "bias", bias, (E,), torch.float32, dev), _need(who, "topk_idx", topk_idx, (T, k), torch.int32, dev),
+            _need(who, "topk_w", topk_w, (T, k), torch.float32, dev), _need(who, "lse", lse, (T,), torch.float32, dev),
+            _need(who, "dw", dw, (T, k) if perm is None else dw.shape, torch.float32, dev), dw.numel(),
+            _opt(who, "perm", perm, (T, k), torch.int32, dev))
     dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, _address(bias), topk_idx.data_ptr(),
-          topk_w.data_ptr(), lse.data_ptr(), dw.data_ptr(), dw.numel(), _address(perm), T, E, k,
-          int(bool(renormalize)), dlogits.data_ptr())
+    _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, *args, T, E, k, 1 if renormalize else 0,
+          dlogits.data_ptr())
     return dlogits
 
 

@@ -1833,23 +1833,42 @@ mx_status grouped_mlp_bwd_fp4_cached(const mx_mlp_dims* dims, const int64_t* spl
 
 namespace {
 
-mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s,
-                    const float* w_amax, int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* stream) {
-  if (y_dtype != MX_BF16 && y_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad output dtype %d", who, (int)y_dtype);
+// Sizes of a few-row product: MX_OK and its workspace, the planes of sums of a
+// product that splits k over workgroups.
+mx_status gemv_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes, const char* who) {
   if (m < 0 || n < 0 || k <= 0 || k % 32)
     return fail(MX_ESHAPE, "%s: need m, n >= 0 and k a positive multiple of 32", who);
+  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30 and k <= 2^24", who);
+  const int splits = m > 0 && n > 0 ? mx::gemv_splits(m, n, k) : 0;
+  *bytes = splits > 1 ? (size_t)splits * m * n * 4 : 0;
+  return MX_OK;
+}
+
+mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s,
+                    const float* w_amax, int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  if (y_dtype != MX_BF16 && y_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad output dtype %d", who, (int)y_dtype);
+  size_t need = 0;
+  mx_status st = gemv_workspace(m, n, k, &need, who);
+  if (st != MX_OK) return st;
   if (ldx % 8 || (m > 1 && ldx < k)) return fail(MX_ESHAPE, "%s: ldx %lld must be a multiple of 8 and at least k", who, (long long)ldx);
-  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24) || ldx > ((int64_t)1 << 24))
-    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30, k <= 2^24 and ldx <= 2^24", who);
+  if (ldx > ((int64_t)1 << 24)) return fail(MX_EUNSUPPORTED, "%s: need ldx <= 2^24", who);
   if (m == 0 || n == 0) return MX_OK;
   const bool nv = fmt == mx::WF_NVFP4;
   if (!x || !w || !w_s || !y || (nv && !w_amax)) return fail(MX_EINVAL, "%s: null pointer argument", who);
   if (!aligned(x, 16) || !aligned(w, 16) || (nv && (!aligned(w_s, 2) || !aligned(w_amax, 4))) ||
       !aligned(y, y_dtype == MX_F32 ? 4 : 2))
     return fail(MX_EALIGN, "%s: x and w must be 16-byte aligned, NVFP4 scales 2-byte, y by its element", who);
+  if (need > 0 && !workspace) return fail(MX_EINVAL, "%s: null workspace", who);
+  if (!aligned(workspace, 256)) return fail(MX_EALIGN, "%s: workspace must be 256-byte aligned", who);
+  if (workspace_bytes < need)
+    return fail(MX_EWORKSPACE, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, need);
   mx::GemvArgs a;
   a.x = x; a.ldx = ldx; a.w = w; a.ws = w_s; a.amax = w_amax;
   a.m = m; a.n = n; a.k = k; a.y = y; a.y_f32 = y_dtype == MX_F32;
+  a.sums = reinterpret_cast<float*>(workspace);
+  a.splits = mx::gemv_splits(m, n, k);
   hipError_t e = mx::launch_gemv(fmt, a, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return MX_OK;
@@ -1857,7 +1876,8 @@ mx_status gemv_impl(const char* who, int fmt, const void* x, int64_t ldx, const 
 
 // Sizes of a decode call: MX_OK and the byte offsets of its workspace.
 struct DecodeLayout {
-  size_t plan, act, total;
+  size_t plan, act, sums, total;
+  int splits;
 };
 mx_status decode_layout(const mx_mlp_dims* d, int32_t topk, DecodeLayout* L, const char* who) {
   if (!d) return fail(MX_EINVAL, "%s: null dims", who);
@@ -1876,6 +1896,8 @@ mx_status decode_layout(const mx_mlp_dims* d, int32_t topk, DecodeLayout* L, con
   size_t cur = 0;
   L->plan = take(cur, (size_t)(cdiv(d->rows, mx::kDecodeTokenChunk) * mx::kDecodePlanBytes));
   L->act = take(cur, (size_t)(d->rows * topk * d->ffn * 4));
+  L->splits = d->rows > 0 ? mx::decode_splits(d->rows, topk, d->num_experts, d->hidden, d->ffn) : 0;
+  L->sums = take(cur, (size_t)(L->splits * d->rows * topk * d->hidden * 4));
   L->total = cur;
   return MX_OK;
 }
@@ -1894,16 +1916,28 @@ mx_status route_checks(const char* who, mx_dtype dt, int64_t tokens, int32_t E, 
 
 extern "C" {
 
-mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
-                      int64_t k, void* y, mx_dtype y_dtype, void* stream) {
+mx_status mx_gemv_sizes(int64_t m, int64_t n, int64_t k, size_t* workspace) {
   g_err[0] = 0;
-  return gemv_impl("mx_gemv_fp4", mx::WF_MXFP4, x, ldx, w, w_s, nullptr, m, n, k, y, y_dtype, stream);
+  size_t bytes = 0;
+  mx_status st = gemv_workspace(m, n, k, &bytes, "mx_gemv_sizes");
+  if (st != MX_OK) return st;
+  if (workspace) *workspace = bytes;
+  return MX_OK;
+}
+
+mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
+                      int64_t k, void* y, mx_dtype y_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  return gemv_impl("mx_gemv_fp4", mx::WF_MXFP4, x, ldx, w, w_s, nullptr, m, n, k, y, y_dtype, workspace,
+                   workspace_bytes, stream);
 }
 
 mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, const float* w_amax,
-                        int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* stream) {
+                        int64_t m, int64_t n, int64_t k, void* y, mx_dtype y_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
-  return gemv_impl("mx_gemv_nvfp4", mx::WF_NVFP4, x, ldx, w, w_s, w_amax, m, n, k, y, y_dtype, stream);
+  return gemv_impl("mx_gemv_nvfp4", mx::WF_NVFP4, x, ldx, w, w_s, w_amax, m, n, k, y, y_dtype, workspace,
+                   workspace_bytes, stream);
 }
 
 mx_status grouped_mlp_decode_sizes(const mx_mlp_dims* dims, int32_t topk, size_t* workspace) {
@@ -1942,6 +1976,9 @@ mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_weight_fo
   a.w2 = reinterpret_cast<const uint8_t*>(w2); a.w2_s = w2_s;
   a.plan = reinterpret_cast<uint8_t*>(workspace) + L.plan;
   a.act = reinterpret_cast<uint16_t*>(reinterpret_cast<uint8_t*>(workspace) + L.act);
+  a.sums = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + L.sums);
+  a.splits = L.splits;
+  a.slots = 0;
   a.y = y;
   a.tokens = (int32_t)dims->rows; a.topk = topk; a.experts = dims->num_experts;
   a.hidden = (int32_t)dims->hidden; a.ffn = (int32_t)dims->ffn;

@@ -80,7 +80,14 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Values of k in one step of the walk below: 128-byte pieces of a 4-bit or
+// A barrier of the workgroup that orders LDS and leaves global loads in flight.
+__device__ __forceinline__ void team_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Values of k in one step of the walks below: 128-byte pieces of a 4-bit or
 // 8-bit row (whole cache lines, which nontemporal loads want), 256-byte pieces
 // of a bf16 row.
 template <int FMT>
@@ -101,47 +108,39 @@ __device__ __forceinline__ int part_start(int nb, int i, int n) {
   return min(steps, (int)((int64_t)k_units<FMT>(nb) * i / n) * kUnit<FMT>);
 }
 
-// One wave's part of the products of NT tiles of 16 weight rows with MT tiles
-// of R activation rows (R = 16; or 4 with MT = 1, repeated over the MFMA's 16)
-// over the k-steps [s0, s1). Result: acc[n][m] register r of lane l =
-// activation row (l / 16) * 4 + r, weight row l % 16.
+// A wave's weights: NT tiles of 16 rows, loaded D steps ahead into registers and
+// passed step by step through a private LDS tile.
 //
 // The MFMA's lane layout (lane l holds row l % 16) makes neighbouring lanes
 // read different rows, which costs the load path one cache line per lane. So
-// both operands are loaded as whole row pieces (consecutive lanes, consecutive
-// 16-byte chunks), kept in registers D steps (weights) and DX half steps
-// (activations) ahead, and pass through a private LDS tile of the wave, whose
-// chunks are swizzled so that neither side conflicts on banks. Scales come 1 KiB
-// (G steps) at a time. No barrier: the tile is the wave's own. MFMA j of 128
-// values contracts values 8 j .. 8 j + 7 of the four lane groups' blocks, the
-// same permutation of k on both sides.
+// rows are loaded as whole pieces (consecutive lanes, consecutive 16-byte
+// chunks) and the tile's chunks are swizzled so that neither its writes nor its
+// reads conflict on banks. Scales come 1 KiB (G steps) at a time. No barrier:
+// the tile is the wave's own.
 //
 // WHOLE: k is a multiple of the step, and scale rows of 16 bytes. Otherwise
 // blocks past the end repeat the last one and count as zero.
-template <int FMT, int NT, int R, int MT, bool WHOLE, int D, int DX>
-struct Walk {
+template <int FMT, int NT, bool WHOLE, int D>
+struct Weights {
   static constexpr int H = kHalves<FMT>, S = kScaleBytes<FMT>, BW = kWords<FMT>;
   static constexpr int W = BW * H;                                          // 16-byte loads of a tile and step
   static constexpr int SB = 4 * H * S;                                      // scale bytes of a row and step
   static constexpr int LR = 4 / NT;                                         // lanes of a scale row
   static constexpr int G = SB > 0 ? 16 * LR / SB : D;                       // steps of a scale load
-  static constexpr int kWTile = 1024 * W, kXTile = 256 * R, kScales = S > 0 ? 1024 : 0;
-  static constexpr int kLds = NT * kWTile + kScales + MT * kXTile;          // bytes of one wave
-  static constexpr int XL = R / 4;                                          // loads of an activation tile
-  static_assert(MT == 1 || R == 16);
-  static_assert((D * H) % DX == 0 && G % D == 0 && (S == 0 || kUnit<FMT> * SB == 16));
+  static constexpr int kTile = 1024 * W;
+  static constexpr int kLds = NT * kTile + (S > 0 ? 1024 : 0);              // bytes of one wave
+  static_assert(G % D == 0 && (S == 0 || kUnit<FMT> * SB == 16));
 
   const uint8_t* w[NT];             // first row of each tile (wave-uniform)
   uint32_t woff[W];                 // the lane's row within a tile, in bytes
   const uint8_t* ws;                // the lane's scale row
-  const uint8_t* x;                 // activations (uniform)
-  uint32_t xoff[MT][XL];            // the lane's rows, in bytes
   int nb;                           // blocks of a row
+  int s1;                           // end of the steps
+  u32x4 wr[D][NT][W], sr;
 
   // tile t: consecutive rows from row first[t]; the last row is repeated where
   // fewer than 16 are left
-  __device__ __forceinline__ void weight_tiles(const uint8_t* base, const uint8_t* sbase, const int64_t (&first)[NT],
-                                               int left) {
+  __device__ __forceinline__ void tiles(const uint8_t* base, const uint8_t* sbase, const int64_t (&first)[NT], int left) {
     const int lane = threadIdx.x & 63;
     if constexpr (S > 0) {
       const int row = lane / LR, t = row >> 4;
@@ -157,137 +156,239 @@ struct Walk {
       woff[i] = (uint32_t)min((i * 64 + lane) / (4 * W), left - 1) * (uint32_t)(nb * 16 * BW);
   }
 
-  __device__ __forceinline__ void run(uint8_t* lds, int s0, int s1, v4f (&acc)[NT][MT]) const {
-    if (s0 >= s1) return;
-    const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
-    u32x4 wr[D][NT][W], xr[DX][MT][XL], sr;
-    uint8_t* const sl = lds + NT * kWTile;
-    uint8_t* const xl = sl + kScales;
-    const int last = s1 * H - 1;
-
-    // a load past the end is issued all the same (the number of loads in
-    // flight stays fixed), with every lane at one address
-    auto load_w = [&](int t, u32x4 (&to)[NT][W]) __attribute__((always_inline)) {
+  // a load past the end is issued all the same (the number of loads in flight
+  // stays fixed), with every lane at one address
+  __device__ __forceinline__ void load(int t, u32x4 (&to)[NT][W]) {
+    const int lane = threadIdx.x & 63;
+    const int c = lane % (4 * W);
+    const uint32_t at = WHOLE ? (uint32_t)(t * 64 * W + c * 16)
+                              : (uint32_t)(min(kStepBlocks<FMT> * t + c / BW, nb - 1) * 16 * BW + (c % BW) * 16);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        to[n][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[n] + (t < s1 ? woff[i] + at : 0u)));
+  }
+  // 16 bytes of a scale row per lane: the G steps from s
+  __device__ __forceinline__ void load_scales(int s) {
+    if constexpr (S > 0) {
+      const int lane = threadIdx.x & 63, row_bytes = nb * S, at = s * SB + lane % LR * 16;
+      if constexpr (WHOLE) {
+        sr = *reinterpret_cast<const u32x4*>(ws + (at < row_bytes ? at : 0));
+      } else {
+        // byte by byte, the row's last one repeated (its blocks count as zero)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int i = at + 4 * q + b;
+            v |= (uint32_t)ws[i < row_bytes ? i : row_bytes - S + (i & (S - 1))] << (8 * b);
+          }
+          sr[q] = v;
+        }
+      }
+    }
+  }
+  // the scales of the group that begins at step s, and the next group's load
+  __device__ __forceinline__ void stage_scales(uint8_t* lds, int s) {
+    if constexpr (S > 0) {
+      wave_lds_fence();                                   // after the previous steps' reads
+      *reinterpret_cast<u32x4*>(lds + NT * kTile + (threadIdx.x & 63) * 16) = sr;
+      if (s + G < s1) load_scales(s + G);
+    }
+  }
+  // step t from registers wr[u] to the tile
+  __device__ __forceinline__ void stage(uint8_t* lds, int t, const u32x4 (&from)[NT][W]) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        const int c = lane % (4 * W);
-        const uint32_t at = WHOLE ? (uint32_t)(t * 64 * W + c * 16)
-                                  : (uint32_t)(min(kStepBlocks<FMT> * t + c / BW, nb - 1) * 16 * BW + (c % BW) * 16);
-        const uint32_t off = t < s1 ? woff[i] + at : 0u;
+        const int row = (i * 64 + lane) / (4 * W), c = lane % (4 * W);
+        u32x4 v = from[n][i];
+        if constexpr (!WHOLE)
+          if (kStepBlocks<FMT> * (t + 1) > nb) {
+            const bool ok = kStepBlocks<FMT> * t + c / BW < nb;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) to[n][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[n] + off));
+            for (int q = 0; q < 4; ++q) v[q] = ok ? v[q] : 0u;
+          }
+        *reinterpret_cast<u32x4*>(lds + n * kTile + (row * 4 * W + (c ^ (row & (4 * W - 1)))) * 16) = v;
       }
-    };
-    auto load_x = [&](int t, u32x4 (&to)[MT][XL]) __attribute__((always_inline)) {
+  }
+  // tile n's block of the lane (half h of the step, step in_group of its scale group) as 4 fragments
+  __device__ __forceinline__ void fragments(const uint8_t* lds, int n, int h, int in_group, bf16x8 (&wf)[4]) const {
+    const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+    u32x4 q[BW];
+    uint32_t sc = 0;
+#pragma unroll
+    for (int i = 0; i < BW; ++i)
+      q[i] = *reinterpret_cast<const u32x4*>(lds + n * kTile + (li * 4 * W + (((h * 4 + g) * BW + i) ^ (li & (4 * W - 1)))) * 16);
+    const uint8_t* p = lds + NT * kTile + (n * 16 + li) * 16 * LR + in_group * SB + (h * 4 + g) * S;
+    if constexpr (S == 1) sc = *p;
+    if constexpr (S == 2) sc = *reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wf[j] = expand<FMT>(q, sc, j);
+  }
+};
+
+// One wave's part of the products of NT tiles of 16 weight rows with R
+// activation rows (16, or 4 repeated over the MFMA's 16) over the k-steps
+// [s0, s1). Result: acc[n][0] register r of lane l = activation row
+// (l / 16) * 4 + r, weight row l % 16. The activations go the weights' way.
+// Loads complete in the order of their issue as far as a wave can tell, so both
+// are issued equally far ahead, the activations first: waiting for either then
+// leaves everything younger in flight. MFMA j of 128 values contracts values 8 j .. 8 j + 7 of the
+// four lane groups' blocks, the same permutation of k on both sides.
+template <int FMT, int NT, int R, bool WHOLE, int D>
+struct Walk : Weights<FMT, NT, WHOLE, D> {
+  typedef Weights<FMT, NT, WHOLE, D> Wt;
+  static constexpr int H = Wt::H, G = Wt::G;
+  static constexpr int kLds = Wt::kLds + 256 * R;                           // bytes of one wave
+  static constexpr int XL = R / 4;                                          // loads of an activation tile
+  static constexpr int DX = D * H;                                          // half steps ahead
+
+  const uint8_t* x;                 // activations (uniform)
+  uint32_t xoff[XL];                // the lane's rows, in bytes
+
+  __device__ __forceinline__ void run(uint8_t* lds, int s0, int s1_, v4f (&acc)[NT][1]) {
+    if (s0 >= s1_) return;
+    this->s1 = s1_;
+    const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+    const int nb = this->nb, s1 = s1_, last = s1 * H - 1;
+    u32x4 xr[DX][XL];
+    uint8_t* const xl = lds + Wt::kLds;
+    auto load_x = [&](int t, u32x4 (&to)[XL]) __attribute__((always_inline)) {
       const uint32_t at = WHOLE ? t * 256 + li * 16 : min(4 * t + li / 4, nb - 1) * 64 + (li % 4) * 16;
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < XL; ++i)
-          to[m][i] = *reinterpret_cast<const u32x4*>(x + (t <= last ? xoff[m][i] + at : xoff[0][0]));
+      for (int i = 0; i < XL; ++i) to[i] = *reinterpret_cast<const u32x4*>(x + (t <= last ? xoff[i] + at : xoff[0]));
     };
-    // 16 bytes of a scale row per lane: the G steps from s
-    auto load_s = [&](int s) __attribute__((always_inline)) {
-      if constexpr (S > 0) {
-        const int row_bytes = nb * S;
-        const int at = s * SB + lane % LR * 16;
-        if constexpr (WHOLE) {
-          sr = *reinterpret_cast<const u32x4*>(ws + (at < row_bytes ? at : 0));
-        } else {
-          // byte by byte, the row's last one repeated (its blocks count as zero)
+    this->load_scales(s0);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int i = at + 4 * q + b;
-              v |= (uint32_t)ws[i < row_bytes ? i : row_bytes - S + (i & (S - 1))] << (8 * b);
-            }
-            sr[q] = v;
-          }
-        }
-      }
-    };
-
-    load_s(s0);
-#pragma unroll
-    for (int d = 0; d < D; ++d) load_w(s0 + d, wr[d]);
-#pragma unroll
-    for (int d = 0; d < DX; ++d) load_x(s0 * H + d, xr[d]);
+    for (int d = 0; d < DX; ++d) {
+      load_x(s0 * H + d, xr[d]);
+      if (d % H == 0) this->load(s0 + d / H, this->wr[d / H]);
+    }
     int in_group = 0;
     for (int s = s0; s < s1; s += D) {
-      if constexpr (S > 0) {
-        if (in_group == 0) {
-          wave_lds_fence();                               // after the previous steps' reads
-          *reinterpret_cast<u32x4*>(sl + lane * 16) = sr;
-          if (s + G < s1) load_s(s + G);
-        }
-      }
+      if (in_group == 0) this->stage_scales(lds, s);
 #pragma unroll
       for (int uh = 0; uh < D * H; ++uh) {
         const int u = uh / H, h = uh % H, t = s + u, th = t * H + h;
         if (h == 0 && t >= s1) return;
         wave_lds_fence();
-        if (h == 0) {
+        if (h == 0) this->stage(lds, t, this->wr[u]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < XL; ++i) {
+          const int row = i * 4 + g;
+          u32x4 v = xr[uh][i];
+          if constexpr (!WHOLE)
+            if (4 * th + 4 > nb) {
+              const bool ok = 4 * th + li / 4 < nb;
 #pragma unroll
-            for (int i = 0; i < W; ++i) {
-              const int row = (i * 64 + lane) / (4 * W), c = lane % (4 * W);
-              u32x4 v = wr[u][n][i];
-              if constexpr (!WHOLE)
-                if (kStepBlocks<FMT> * (t + 1) > nb) {
-                  const bool ok = kStepBlocks<FMT> * t + c / BW < nb;
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) v[q] = ok ? v[q] : 0u;
-                }
-              *reinterpret_cast<u32x4*>(lds + n * kWTile + (row * 4 * W + (c ^ (row & (4 * W - 1)))) * 16) = v;
+              for (int q = 0; q < 4; ++q) v[q] = ok ? v[q] : 0u;
             }
+          *reinterpret_cast<u32x4*>(xl + (row * 16 + (li ^ row)) * 16) = v;
         }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < XL; ++i) {
-            const int row = i * 4 + g;
-            u32x4 v = xr[uh % DX][m][i];
-            if constexpr (!WHOLE)
-              if (4 * th + 4 > nb) {
-                const bool ok = 4 * th + li / 4 < nb;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = ok ? v[q] : 0u;
-              }
-            *reinterpret_cast<u32x4*>(xl + m * kXTile + (row * 16 + (li ^ row)) * 16) = v;
-          }
-        if (h == 0) load_w(t + D, wr[u]);
-        load_x(th + DX, xr[uh % DX]);
+        load_x(th + DX, xr[uh]);
+        if (h == 0) this->load(t + D, this->wr[u]);
         wave_lds_fence();
-        bf16x8 xf[MT][4];
+        bf16x8 xf[4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = li % R;
-            xf[m][j] = *reinterpret_cast<const bf16x8*>(xl + m * kXTile + (row * 16 + ((g * 4 + j) ^ row)) * 16);
-          }
+        for (int j = 0; j < 4; ++j) {
+          const int row = li % R;
+          xf[j] = *reinterpret_cast<const bf16x8*>(xl + (row * 16 + ((g * 4 + j) ^ row)) * 16);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          u32x4 q[BW];
-          uint32_t sc = 0;
+          bf16x8 wf[4];
+          this->fragments(lds, n, h, in_group + u, wf);
 #pragma unroll
-          for (int i = 0; i < BW; ++i)
-            q[i] = *reinterpret_cast<const u32x4*>(
-                lds + n * kWTile + (li * 4 * W + (((h * 4 + g) * BW + i) ^ (li & (4 * W - 1)))) * 16);
-          const uint8_t* p = sl + (n * 16 + li) * 16 * LR + (in_group + u) * SB + (h * 4 + g) * S;
-          if constexpr (S == 1) sc = *p;
-          if constexpr (S == 2) sc = *reinterpret_cast<const uint16_t*>(p);
+          for (int j = 0; j < 4; ++j) acc[n][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], wf[j], acc[n][0], 0, 0, 0);
+        }
+      }
+      in_group = in_group + D < G ? in_group + D : 0;
+    }
+  }
+};
+
+// The same for more rows: the 4 waves of a workgroup own NT tiles each and walk
+// the same steps, so that each activation tile (MT tiles of 16 rows) is loaded
+// once for all four and shared through LDS, in two buffers with one barrier per
+// half step. All four waves call run() with the same steps.
+template <int FMT, int NT, int MT, bool WHOLE, int D>
+struct WideWalk : Weights<FMT, NT, WHOLE, D> {
+  typedef Weights<FMT, NT, WHOLE, D> Wt;
+  static constexpr int H = Wt::H, G = Wt::G;
+  static constexpr int kXTile = 4096;                                       // 16 rows of 128 values
+  static constexpr int kShared = 2 * MT * kXTile;                           // bytes of the workgroup, and Wt::kLds for each wave
+  static constexpr int DX = D * H;                                          // half steps ahead
+
+  const uint8_t* x;                 // activations (uniform)
+  uint32_t xoff[MT];                // the thread's row (tid / 16) of each tile, in bytes
+
+  __device__ __forceinline__ void run(uint8_t* shared, uint8_t* lds, int s0, int s1_, v4f (&acc)[NT][MT]) {
+    if (s0 >= s1_) return;
+    this->s1 = s1_;
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, g = lane >> 4, xrow = tid >> 4;
+    const int nb = this->nb, s1 = s1_, last = s1 * H - 1;
+    u32x4 xr[DX][MT];
+    auto load_x = [&](int t, u32x4 (&to)[MT]) __attribute__((always_inline)) {
+      const uint32_t at = WHOLE ? t * 256 + li * 16 : min(4 * t + li / 4, nb - 1) * 64 + (li % 4) * 16;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) to[m] = *reinterpret_cast<const u32x4*>(x + (t <= last ? xoff[m] + at : xoff[0]));
+    };
+    auto stage_x = [&](int t, const u32x4 (&from)[MT]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        u32x4 v = from[m];
+        if constexpr (!WHOLE)
+          if (4 * t + 4 > nb) {
+            const bool ok = 4 * t + li / 4 < nb;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = ok ? v[q] : 0u;
+          }
+        *reinterpret_cast<u32x4*>(shared + ((t & 1) * MT + m) * kXTile + (xrow * 16 + (li ^ xrow)) * 16) = v;
+      }
+    };
+    // half step t's activations are in LDS before it begins; those of the DX after it are on their way
+    this->load_scales(s0);
+    load_x(s0 * H, xr[0]);
+    team_barrier();                                       // the buffers are free
+    stage_x(s0 * H, xr[0]);
+#pragma unroll
+    for (int d = 0; d < DX; ++d) {
+      load_x(s0 * H + d + 1, xr[d]);
+      if (d % H == 0) this->load(s0 + d / H, this->wr[d / H]);
+    }
+    team_barrier();
+    int in_group = 0;
+    for (int s = s0; s < s1; s += D) {
+      if (in_group == 0) this->stage_scales(lds, s);
+#pragma unroll
+      for (int uh = 0; uh < D * H; ++uh) {
+        const int u = uh / H, h = uh % H, t = s + u, th = t * H + h;
+        if (h == 0 && t >= s1) return;
+        wave_lds_fence();
+        if (h == 0) this->stage(lds, t, this->wr[u]);
+        stage_x(th + 1, xr[uh]);                          // into the buffer that half step th - 1 read
+        load_x(th + 1 + DX, xr[uh]);
+        if (h == 0) this->load(t + D, this->wr[u]);
+        wave_lds_fence();
+        bf16x8 wf[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) this->fragments(lds, n, h, in_group + u, wf[n]);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bf16x8 wf = expand<FMT>(q, sc, j);
+            const bf16x8 xf = *reinterpret_cast<const bf16x8*>(shared + ((th & 1) * MT + m) * kXTile +
+                                                               (li * 16 + ((g * 4 + j) ^ li)) * 16);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-              acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m][j], wf, acc[n][m], 0, 0, 0);
+            for (int n = 0; n < NT; ++n)
+              acc[n][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, wf[n][j], acc[n][m], 0, 0, 0);
           }
-        }
+        team_barrier();
       }
       in_group = in_group + D < G ? in_group + D : 0;
     }
@@ -302,68 +403,129 @@ __device__ __forceinline__ void clear(v4f (&acc)[NT][MT]) {
     for (int m = 0; m < MT; ++m) acc[n][m] = v4f{0.f, 0.f, 0.f, 0.f};
 }
 
-// y[m, n] = x[m, k] . W[n, k]^T. A team of `parts` waves owns 16 * NT weight
-// rows and R * MT activation rows; its waves split k and add up through LDS in
-// wave order (one order whatever the timing). A workgroup is waves / parts
-// teams.
-template <int FMT, int NT, int R, int MT, bool WHOLE, int D, int DX>
+// Writes the lane's results of one register row: row m, column n of y.
+__device__ __forceinline__ void store_y(const GemvArgs& a, int row, int col, float v) {
+  const int64_t at = (int64_t)row * a.n + col;
+  if (a.y_f32)
+    reinterpret_cast<float*>(a.y)[at] = v;
+  else
+    reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
+}
+// The factor of a result: 1 / S of an NVFP4 weight.
+template <int FMT>
+__device__ __forceinline__ float result_scale(const GemvArgs& a) {
+  if constexpr (FMT == WF_NVFP4) return (float)(1.0 / (double)nvfp4_tensor_scale(*a.amax));
+  return 1.0f;
+}
+// First rows of the tiles from row n0: one that passes the end moves back (its
+// columns before n0 are another's); a matrix of less than 16 rows repeats its last.
+template <int NT>
+__device__ __forceinline__ void tile_rows(int n0, int n, int64_t (&first)[NT]) {
+#pragma unroll
+  for (int t = 0; t < NT; ++t) first[t] = max(0, min(n0 + 16 * t, n - 16));
+}
+
+// y[m, n] = x[m, k] . W[n, k]^T for at most R rows. A team of `parts` waves
+// owns 16 * NT weight rows; its waves split k and add up through LDS in wave
+// order (one order whatever the timing). A workgroup is waves / parts teams.
+template <int FMT, int NT, int R, bool WHOLE, int D>
 __global__ __launch_bounds__(512, 2) void gemv_kernel(GemvArgs a, int parts) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int waves = blockDim.x >> 6;
   const int team = wave / parts, part = wave % parts;
-  const int n0 = (blockIdx.x * (waves / parts) + team) * 16 * NT, m0 = blockIdx.y * R * MT;
+  const int n0 = (blockIdx.x * (waves / parts) + team) * 16 * NT;
   const int m = (int)a.m, n = (int)a.n;
-  typedef Walk<FMT, NT, R, MT, WHOLE, D, DX> Wk;
+  typedef Walk<FMT, NT, R, WHOLE, D> Wk;
   Wk k;
   k.nb = (int)(a.k / 32);
   int64_t first[NT];
-  // a tile that passes the end moves back; a matrix of less than 16 rows repeats its last
+  tile_rows<NT>(n0, n, first);
+  k.tiles(a.w, a.ws, first, min(16, n));
+  k.x = reinterpret_cast<const uint8_t*>(a.x);
 #pragma unroll
-  for (int t = 0; t < NT; ++t) first[t] = max(0, min(n0 + 16 * t, n - 16));
-  k.weight_tiles(a.w, a.ws, first, min(16, n));
-  k.x = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)m0 * a.ldx * 2;
-#pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int i = 0; i < Wk::XL; ++i)
-      k.xoff[t][i] = (uint32_t)min(R * t + 4 * i + (lane >> 4), m - 1 - m0) * (uint32_t)(a.ldx * 2);
-  v4f acc[NT][MT];
+  for (int i = 0; i < Wk::XL; ++i) k.xoff[i] = (uint32_t)min(4 * i + (lane >> 4), m - 1) * (uint32_t)(a.ldx * 2);
+  v4f acc[NT][1];
   clear(acc);
   k.run(smem + wave * Wk::kLds, part_start<FMT>(k.nb, part, parts), part_start<FMT>(k.nb, part + 1, parts), acc);
-  float inv = 1.0f;
-  if constexpr (FMT == WF_NVFP4) inv = (float)(1.0 / (double)nvfp4_tensor_scale(*a.amax));
-  constexpr int kOut = NT * MT * 256;
+  const float scale = result_scale<FMT>(a);
+  constexpr int kOut = NT * 256;
   float* red = reinterpret_cast<float*>(smem);
   if (parts > 1) {
     __syncthreads();
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int u = 0; u < MT; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wave * kOut + ((t * MT + u) * 4 + r) * 64 + lane] = acc[t][u][r];
+      for (int r = 0; r < 4; ++r) red[wave * kOut + (t * 4 + r) * 64 + lane] = acc[t][0][r];
     __syncthreads();
   }
   // each wave finishes its share of the team's results
 #pragma unroll
-  for (int o = 0; o < NT * MT * 4; ++o) {
+  for (int o = 0; o < NT * 4; ++o) {
     if (o % parts != part) continue;
-    const int r = o & 3, u = (o >> 2) % MT, t = (o >> 2) / MT;
+    const int r = o & 3, t = o >> 2;
     float v = 0.f;
     if (parts > 1)
       for (int i = 0; i < parts; ++i) v += red[(team * parts + i) * kOut + o * 64 + lane];
     else
-      v = acc[t][u][r];
-    const int in_tile = (lane >> 4) * 4 + r, row = m0 + R * u + in_tile;
-    const int col = (int)first[t] + (lane & 15);
-    if (in_tile >= R || row >= m || col >= n || col < n0 + 16 * t) continue;
-    if constexpr (FMT == WF_NVFP4) v *= inv;
-    const int64_t at = (int64_t)row * n + col;
+      v = acc[t][0][r];
+    const int row = (lane >> 4) * 4 + r, col = (int)first[t] + (lane & 15);
+    if (row < R && row < m && col < n && col >= n0 + 16 * t) store_y(a, row, col, v * scale);
+  }
+}
+
+// The same for more rows: a workgroup owns 64 * NT weight rows, 16 * MT rows of
+// x and split blockIdx.z of k. With more than one split its sums go to the
+// split's plane of a.sums, which the next kernel adds.
+template <int FMT, int NT, int MT, bool WHOLE, int D>
+__global__ __launch_bounds__(256, 2) void gemv_wide_kernel(GemvArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = (blockIdx.x * 4 + wave) * 16 * NT, m0 = blockIdx.y * 16 * MT;
+  const int m = (int)a.m, n = (int)a.n, split = blockIdx.z;
+  typedef WideWalk<FMT, NT, MT, WHOLE, D> Wk;
+  Wk k;
+  k.nb = (int)(a.k / 32);
+  int64_t first[NT];
+  tile_rows<NT>(n0, n, first);
+  k.tiles(a.w, a.ws, first, min(16, n));
+  k.x = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)m0 * a.ldx * 2;
+#pragma unroll
+  for (int t = 0; t < MT; ++t) k.xoff[t] = (uint32_t)min(16 * t + (tid >> 4), m - 1 - m0) * (uint32_t)(a.ldx * 2);
+  v4f acc[NT][MT];
+  clear(acc);
+  k.run(smem, smem + Wk::kShared + wave * Wk::Wt::kLds, part_start<FMT>(k.nb, split, a.splits),
+        part_start<FMT>(k.nb, split + 1, a.splits), acc);
+  const float scale = result_scale<FMT>(a);
+  float* const plane = a.sums + (int64_t)split * m * n;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int u = 0; u < MT; ++u)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = m0 + 16 * u + (lane >> 4) * 4 + r, col = (int)first[t] + (lane & 15);
+        if (row >= m || col >= n || col < n0 + 16 * t) continue;
+        if (a.splits > 1)
+          plane[(int64_t)row * n + col] = acc[t][u][r];
+        else
+          store_y(a, row, col, acc[t][u][r] * scale);
+      }
+}
+
+// y = the splits' sums, added in order.
+template <int FMT>
+__global__ __launch_bounds__(256) void gemv_sum_kernel(GemvArgs a) {
+  const int64_t n = a.m * a.n;
+  const float scale = result_scale<FMT>(a);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    float v = 0.f;
+    for (int s = 0; s < a.splits; ++s) v += a.sums[s * n + i];
+    v *= scale;
     if (a.y_f32)
-      reinterpret_cast<float*>(a.y)[at] = v;
+      reinterpret_cast<float*>(a.y)[i] = v;
     else
-      reinterpret_cast<__bf16*>(a.y)[at] = (__bf16)v;
+      reinterpret_cast<__bf16*>(a.y)[i] = (__bf16)v;
   }
 }
 
@@ -376,39 +538,65 @@ static bool whole_steps(int64_t k, const uint8_t* scales) {
          (kScaleBytes<FMT> == 0 || (k / 32 * kScaleBytes<FMT> % 16 == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0));
 }
 
+constexpr int kGemvWideTiles = 1;
 // Waves a launch splits k for: 16 per compute unit, all resident at once.
 constexpr int64_t kWavesWanted = 4096;
 
-template <int FMT, int NT, int R, int MT, int D, int DX>
+template <int FMT, int NT, int R, int D>
 static void gemv_go(const GemvArgs& a, hipStream_t stream) {
-  const int64_t ns = k_units<FMT>((int)(a.k / 32)), mt = (a.m + R * MT - 1) / (R * MT), tiles = (a.n + 16 * NT - 1) / (16 * NT);
+  const int64_t units = k_units<FMT>((int)(a.k / 32)), tiles = (a.n + 16 * NT - 1) / (16 * NT);
   int parts = 1;
-  while (parts < 8 && parts * 2 <= ns && tiles * mt * parts * 2 <= kWavesWanted) parts *= 2;
+  while (parts < 8 && parts * 2 <= units && tiles * parts * 2 <= kWavesWanted) parts *= 2;
   const int waves = std::max(4, parts), teams = waves / parts;
-  const dim3 grid((unsigned)((tiles + teams - 1) / teams), (unsigned)mt);
-  const bool whole = whole_steps<FMT>(a.k, a.ws);
-  const size_t lds = (size_t)waves * std::max(Walk<FMT, NT, R, MT, true, D, DX>::kLds, NT * MT * 1024);
-  if (whole)
-    hipLaunchKernelGGL((gemv_kernel<FMT, NT, R, MT, true, D, DX>), grid, dim3(64 * waves), lds, stream, a, parts);
+  const dim3 grid((unsigned)((tiles + teams - 1) / teams));
+  const size_t lds = (size_t)waves * std::max(Walk<FMT, NT, R, true, D>::kLds, NT * 1024);
+  if (whole_steps<FMT>(a.k, a.ws))
+    hipLaunchKernelGGL((gemv_kernel<FMT, NT, R, true, D>), grid, dim3(64 * waves), lds, stream, a, parts);
   else
-    hipLaunchKernelGGL((gemv_kernel<FMT, NT, R, MT, false, D, DX>), grid, dim3(64 * waves), lds, stream, a, parts);
+    hipLaunchKernelGGL((gemv_kernel<FMT, NT, R, false, D>), grid, dim3(64 * waves), lds, stream, a, parts);
+}
+
+template <int FMT, int MT>
+static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
+  constexpr int NT = kGemvWideTiles, D = 1;
+  const dim3 grid((unsigned)((a.n + 64 * NT - 1) / (64 * NT)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT)), a.splits);
+  typedef WideWalk<FMT, NT, MT, true, D> Wk;
+  const size_t lds = Wk::kShared + 4 * Wk::Wt::kLds;
+  if (whole_steps<FMT>(a.k, a.ws))
+    hipLaunchKernelGGL((gemv_wide_kernel<FMT, NT, MT, true, D>), grid, dim3(256), lds, stream, a);
+  else
+    hipLaunchKernelGGL((gemv_wide_kernel<FMT, NT, MT, false, D>), grid, dim3(256), lds, stream, a);
+  if (a.splits > 1)
+    hipLaunchKernelGGL((gemv_sum_kernel<FMT>), dim3((unsigned)std::min<int64_t>(2048, (a.m * a.n + 255) / 256)), dim3(256), 0,
+                       stream, a);
 }
 
 template <int FMT>
 static void gemv_format(const GemvArgs& a, hipStream_t stream) {
   if (a.m <= 4) {
     if (a.n >= 16384)
-      gemv_go<FMT, 2, 4, 1, 1, 2>(a, stream);
+      gemv_go<FMT, 2, 4, 1>(a, stream);
     else
-      gemv_go<FMT, 1, 4, 1, 2, 2>(a, stream);
+      gemv_go<FMT, 1, 4, 2>(a, stream);
   } else if (a.m <= 16) {
     if (a.n >= 8192)
-      gemv_go<FMT, 2, 16, 1, 1, 1>(a, stream);
+      gemv_go<FMT, 2, 16, 1>(a, stream);
     else
-      gemv_go<FMT, 1, 16, 1, 2, 2>(a, stream);
+      gemv_go<FMT, 1, 16, 1>(a, stream);
+  } else if (a.m <= 32) {
+    gemv_wide_go<FMT, 2>(a, stream);
   } else {
-    gemv_go<FMT, 2, 16, 2, 1, 1>(a, stream);
+    gemv_wide_go<FMT, 4>(a, stream);
   }
+}
+
+// Splits of k of the wide product (0: the narrow one runs): up to 512
+// workgroups, 2 a compute unit, of at least 512 values of k each. (64 x 14336 x
+// 4096: 2 splits 24.2 us, 3 26.7 us; 64 x 28672 x 4096: 1 split 31.7 us.)
+int gemv_splits(int64_t m, int64_t n, int64_t k) {
+  if (m <= 16) return 0;
+  const int64_t groups = (n + 64 * kGemvWideTiles - 1) / (64 * kGemvWideTiles) * ((m + 63) / 64);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, k / 512), 512 / groups));
 }
 
 hipError_t launch_gemv(int fmt, const GemvArgs& a, hipStream_t stream) {
@@ -461,6 +649,7 @@ struct DecodePlan {
   int32_t slot_e[kMaxGroups];
   int32_t first[kMaxGroups + 1];    // of slot s in list
   int16_t list[kDecodeMaxEntries];
+  uint8_t used[kDecodeMaxEntries];  // whether entry i is in list
 };
 static_assert(sizeof(DecodePlan) == kDecodePlanBytes);
 
@@ -517,6 +706,7 @@ __device__ void write_plan(const DecodeArgs& a, int chunk, uint8_t* smem) {
   // the order of an expert's entries among themselves changes no result
   for (int i = tid; i < en.n; i += blockDim.x) {
     const int e = counted(i);
+    plan->used[i] = e >= 0;
     if (e >= 0) plan->list[atomicAdd(&cnt[kMaxGroups + e], 1)] = (int16_t)i;
   }
 }
@@ -526,273 +716,421 @@ constexpr int kPlanLds = 8 * kMaxGroups + 2 * kDecodeMaxEntries;
 template <int FMT>
 constexpr int kUpAhead = 1;
 template <int FMT>
-constexpr int kDownAhead = FMT == WF_BF16 ? 1 : 2;
+constexpr int kDownAhead = (FMT == WF_BF16 ? 1 : 2);
+template <int FMT>
+constexpr int kWideAhead = FMT == WF_BF16 ? 1 : 1;
 
 constexpr int kRowList = kDecodeTokenChunk * 8;           // a wave's list of rows: entry and weight
 
-// A = w silu(g) u of every entry, [g | u] = W1_e x_t. A team of `parts` waves
-// owns 16 values of f of the slot-th expert that the chunk's entries name, for
-// all of that expert's entries, and splits the hidden dimension; a workgroup
-// is waves / parts teams. Every wave finds its expert and rows by itself. A is
-// kept as a sum of two bf16 numbers (16 bits), since the second product takes
-// bf16. ROWS: the most rows an expert can have (4, 16 or more).
+// The slot-th expert that the chunk's entries name, and its rows in the wave's
+// own LDS: entries and their weights. Every lane of the wave takes part.
+struct ExpertRows {
+  int expert, count;                // -1: fewer experts are named than slots
+  const int32_t* entry;
+  const float* weight;
+
+  __device__ __forceinline__ ExpertRows(const DecodeArgs& a, const Entries& en, int chunk, int slot, uint8_t* lds) {
+    const int lane = threadIdx.x & 63;
+    uint32_t* const set = reinterpret_cast<uint32_t*>(lds);
+    if (lane < kMaxGroups / 32) set[lane] = 0;
+    wave_lds_fence();
+    for (int g0 = 0; g0 < en.n; g0 += en.per) {
+      const int e = en.expert(g0, lane, a.experts);
+      if (e >= 0) atomicOr(&set[e >> 5], 1u << (e & 31));
+    }
+    wave_lds_fence();
+    expert = -1;
+    count = 0;
+    int left = slot;
+#pragma unroll
+    for (int q = 0; q < kMaxGroups / 32; ++q) {
+      uint32_t bits = __builtin_amdgcn_readfirstlane(set[q]);
+      const int c = __popc(bits);
+      if (expert < 0 && left < c) {
+        for (int i = 0; i < left; ++i) bits &= bits - 1;
+        expert = 32 * q + __ffs(bits) - 1;
+      }
+      left -= c;
+    }
+    wave_lds_fence();
+    if (expert < 0) return;
+    int32_t* const rows = reinterpret_cast<int32_t*>(lds);
+    float* const w = reinterpret_cast<float*>(lds) + kDecodeTokenChunk;
+    const float* wts = a.topk_w != nullptr ? a.topk_w + (int64_t)chunk * kDecodeTokenChunk * a.topk : nullptr;
+    for (int g0 = 0; g0 < en.n; g0 += en.per) {
+      const uint64_t same = __ballot(en.expert(g0, lane, a.experts) == expert);
+      if (same == 0) continue;
+      const bool keep = en.first_of_token(same, lane);
+      const uint64_t firsts = __ballot(keep);
+      if (keep) {
+        float wt = 0.f;
+        const int end = lane - lane % en.topk + en.topk;
+        for (int j = lane; j < end; ++j)
+          if ((same >> j) & 1ull) wt += wts != nullptr ? wts[g0 + j] : 1.0f;
+        const int at = count + bits_below(firsts, lane);
+        rows[at] = g0 + lane;
+        w[at] = wt;
+      }
+      count += __popcll(firsts);
+    }
+    wave_lds_fence();
+    entry = rows;
+    weight = w;
+  }
+};
+
+// A = w silu(g) u of one value, kept as the sum of two bf16 numbers (16 bits),
+// since the second product takes bf16. to: the entry's row, ffn further the second part.
+__device__ __forceinline__ void store_act(uint16_t* to, int ffn, float w, float g, float u) {
+  const float v = w * (g / (1.0f + expf(-g))) * u;
+  const __bf16 hi = (__bf16)v;
+  // an infinite or NaN value has no second part
+  const __bf16 lo = abs_bits((float)hi) < 0x7F800000u ? (__bf16)(v - (float)hi) : (__bf16)0.0f;
+  to[0] = __builtin_bit_cast(uint16_t, hi);
+  to[ffn] = __builtin_bit_cast(uint16_t, lo);
+}
+
+typedef std::integral_constant<int, 1> One;
+typedef std::integral_constant<int, 2> Two;
+typedef std::integral_constant<int, 3> Three;
+typedef std::integral_constant<int, 4> Four;
+typedef std::integral_constant<int, 8> Eight;
+typedef std::integral_constant<int, 16> Sixteen;
+
+// A = w silu(g) u of every entry, [g | u] = W1_e x_t, for at most ROWS (4 or
+// 16) tokens. A team of `parts` waves owns 16 values of f of the slot-th expert
+// that the entries name, for all of that expert's entries, and splits the
+// hidden dimension; a workgroup is waves / parts teams. Every wave finds its
+// expert and rows by itself.
 template <int FMT, bool WHOLE, int ROWS>
-__global__ __launch_bounds__(256, 3) void decode_up_kernel(DecodeArgs a, int parts, int tile_bytes) {
+__global__ __launch_bounds__(512, 2) void decode_up_kernel(DecodeArgs a, int parts, int tile_bytes) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int waves = blockDim.x >> 6;
+  const int slot = blockIdx.y;
+  if (blockIdx.x == gridDim.x - 1) {
+    if (slot == 0) write_plan(a, 0, smem);
+    return;
+  }
+  uint8_t* const mine = smem + wave * tile_bytes;
+  const Entries en(a, 0);
+  const ExpertRows rows(a, en, 0, slot, mine);
+  if (rows.expert < 0) return;                            // all of the workgroup leaves
+  const int team = wave / parts, part = wave % parts;
+  const int tile = (int)blockIdx.x * (waves / parts) + team, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
+  const int nb = a.hidden / 32;
+  const int s0 = part_start<FMT>(nb, part, parts), s1 = part_start<FMT>(nb, part + 1, parts);
+  auto go = [&](auto r_) __attribute__((always_inline)) {
+    constexpr int R = decltype(r_)::value;
+    typedef Walk<FMT, 2, R, WHOLE, kUpAhead<FMT>> Wk;
+    Wk k;
+    k.nb = nb;
+    const int64_t first[2] = {(int64_t)rows.expert * 2 * a.ffn + f0, (int64_t)rows.expert * 2 * a.ffn + a.ffn + f0};
+    k.tiles(a.w1, a.w1_s, first, 16);
+    k.x = a.x;
+#pragma unroll
+    for (int i = 0; i < Wk::XL; ++i)
+      k.xoff[i] = (uint32_t)(rows.entry[min(4 * i + (lane >> 4), rows.count - 1)] / en.topk) * (uint32_t)(a.hidden * 2);
+    v4f acc[2][1];
+    clear(acc);
+    k.run(mine + kRowList, s0, s1, acc);
+    if (parts > 1) {
+      __syncthreads();
+      float* p = reinterpret_cast<float*>(mine + kRowList) + lane;
+#pragma unroll
+      for (int o = 0; o < 8; ++o) p[o * 64] = acc[o >> 2][0][o & 3];
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r % parts != part) continue;
+      float g = acc[0][0][r], up = acc[1][0][r];
+      if (parts > 1) {
+        g = up = 0.f;
+        for (int i = 0; i < parts; ++i) {
+          const float* p = reinterpret_cast<const float*>(smem + (size_t)(wave - part + i) * tile_bytes + kRowList) + lane;
+          g += p[r * 64];
+          up += p[(4 + r) * 64];
+        }
+      }
+      const int row = (lane >> 4) * 4 + r;
+      if (row < R && row < rows.count && tile < tiles)
+        store_act(a.act + (int64_t)rows.entry[row] * 2 * a.ffn + f0 + (lane & 15), a.ffn, rows.weight[row], g, up);
+    }
+  };
+  if (ROWS <= 4 || rows.count <= 4)
+    go(Four{});
+  else
+    go(Sixteen{});
+}
+
+// The same for more tokens: a workgroup owns 64 values of f of one expert, for
+// the expert's entries among a chunk of tokens.
+template <int FMT, bool WHOLE, int TILES>
+__global__ __launch_bounds__(256, 2) void decode_up_wide_kernel(DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = blockIdx.y, chunk = blockIdx.z;
   if (blockIdx.x == gridDim.x - 1) {
     if (slot == 0) write_plan(a, chunk, smem);
     return;
   }
-  uint8_t* const mine = smem + wave * tile_bytes;
   const Entries en(a, chunk);
-  // the slot-th named expert: a set of the named ones in the wave's own LDS
-  uint32_t* const set = reinterpret_cast<uint32_t*>(mine);
-  if (lane < kMaxGroups / 32) set[lane] = 0;
-  wave_lds_fence();
-  for (int g0 = 0; g0 < en.n; g0 += en.per) {
-    const int e = en.expert(g0, lane, a.experts);
-    if (e >= 0) atomicOr(&set[e >> 5], 1u << (e & 31));
-  }
-  wave_lds_fence();
-  int e = -1, left_slots = slot;
-#pragma unroll
-  for (int q = 0; q < kMaxGroups / 32; ++q) {
-    uint32_t bits = __builtin_amdgcn_readfirstlane(set[q]);
-    const int c = __popc(bits);
-    if (e < 0 && left_slots < c) {
-      for (int i = 0; i < left_slots; ++i) bits &= bits - 1;
-      e = 32 * q + __ffs(bits) - 1;
-    }
-    left_slots -= c;
-  }
-  wave_lds_fence();
-  if (e < 0) return;                                      // fewer experts named than slots: all of the workgroup leaves
-  // its rows
-  int32_t* const row_entry = reinterpret_cast<int32_t*>(mine);
-  float* const row_w = reinterpret_cast<float*>(mine) + kDecodeTokenChunk;
-  const float* wts = a.topk_w != nullptr ? a.topk_w + (int64_t)chunk * kDecodeTokenChunk * a.topk : nullptr;
-  int count = 0;
-  for (int g0 = 0; g0 < en.n; g0 += en.per) {
-    const uint64_t same = __ballot(en.expert(g0, lane, a.experts) == e);
-    if (same == 0) continue;
-    const bool keep = en.first_of_token(same, lane);
-    const uint64_t firsts = __ballot(keep);
-    if (keep) {
-      float wt = 0.f;
-      const int last = lane - lane % en.topk + en.topk;
-      for (int j = lane; j < last; ++j)
-        if ((same >> j) & 1ull) wt += wts != nullptr ? wts[g0 + j] : 1.0f;
-      const int at = count + bits_below(firsts, lane);
-      row_entry[at] = g0 + lane;
-      row_w[at] = wt;
-    }
-    count += __popcll(firsts);
-  }
-  wave_lds_fence();
-
-  const int team = wave / parts, part = wave % parts;
-  const int tile = (int)blockIdx.x * (waves / parts) + team, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
+  const ExpertRows rows(a, en, chunk, slot, smem + wave * kRowList);
+  if (rows.expert < 0) return;
+  const int tile = (int)blockIdx.x * 4 + wave, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
   const int nb = a.hidden / 32;
-  const int s0 = part_start<FMT>(nb, part, parts), s1 = part_start<FMT>(nb, part + 1, parts);
-  float* const red = reinterpret_cast<float*>(smem + (size_t)(wave - part) * tile_bytes + kRowList);
-  auto rows_from = [&](auto r_, auto mt_, int c0) __attribute__((always_inline)) {
-    constexpr int R = decltype(r_)::value, MT = decltype(mt_)::value;
-    typedef Walk<FMT, 2, R, MT, WHOLE, kUpAhead<FMT>, 1> Wk;
+  auto go = [&](auto mt_, int c0) __attribute__((always_inline)) {
+    constexpr int MT = decltype(mt_)::value;
+    typedef WideWalk<FMT, 2, MT, WHOLE, kWideAhead<FMT>> Wk;
     Wk k;
     k.nb = nb;
-    const int64_t first[2] = {(int64_t)e * 2 * a.ffn + f0, (int64_t)e * 2 * a.ffn + a.ffn + f0};
-    k.weight_tiles(a.w1, a.w1_s, first, 16);
+    const int64_t first[2] = {(int64_t)rows.expert * 2 * a.ffn + f0, (int64_t)rows.expert * 2 * a.ffn + a.ffn + f0};
+    k.tiles(a.w1, a.w1_s, first, 16);
     k.x = a.x + (int64_t)chunk * kDecodeTokenChunk * a.hidden * 2;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int i = 0; i < Wk::XL; ++i) {
-        const int entry = row_entry[min(c0 + R * t + 4 * i + (lane >> 4), count - 1)];
-        k.xoff[t][i] = (uint32_t)(entry / en.topk) * (uint32_t)(a.hidden * 2);
-      }
+      k.xoff[t] = (uint32_t)(rows.entry[min(c0 + 16 * t + (tid >> 4), rows.count - 1)] / en.topk) * (uint32_t)(a.hidden * 2);
     v4f acc[2][MT];
     clear(acc);
-    k.run(mine + kRowList, s0, s1, acc);
-    if (parts > 1) {
-      __syncthreads();
+    k.run(smem + 4 * kRowList, smem + 4 * kRowList + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, 0,
+          part_start<FMT>(nb, 1, 1), acc);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int u = 0; u < MT; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            *(reinterpret_cast<float*>(mine + kRowList) + ((t * MT + u) * 4 + r) * 64 + lane) = acc[t][u][r];
-      __syncthreads();
-    }
-#pragma unroll
-    for (int o = 0; o < MT * 4; ++o) {
-      if (o % parts != part) continue;
-      const int u = o >> 2, r = o & 3;
-      float g = acc[0][u][r], up = acc[1][u][r];
-      if (parts > 1) {
-        g = up = 0.f;
-        for (int i = 0; i < parts; ++i) {
-          const float* p = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(red) + (size_t)i * tile_bytes);
-          g += p[o * 64 + lane];
-          up += p[(MT * 4 + o) * 64 + lane];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int row = c0 + 16 * t + (lane >> 4) * 4 + r;
+        if (row < rows.count && tile < tiles)
+          store_act(a.act + ((int64_t)chunk * kDecodeTokenChunk * en.topk + rows.entry[row]) * 2 * a.ffn + f0 + (lane & 15),
+                    a.ffn, rows.weight[row], acc[0][t][r], acc[1][t][r]);
       }
-      const int in_tile = (lane >> 4) * 4 + r, row = c0 + R * u + in_tile;
-      if (in_tile >= R || row >= count || tile >= tiles) continue;
-      const float v = row_w[row] * (g / (1.0f + expf(-g))) * up;
-      const __bf16 hi = (__bf16)v;
-      // an infinite or NaN value has no second part
-      const __bf16 lo = abs_bits((float)hi) < 0x7F800000u ? (__bf16)(v - (float)hi) : (__bf16)0.0f;
-      uint16_t* const to = a.act + ((int64_t)chunk * kDecodeTokenChunk * en.topk + row_entry[row]) * 2 * a.ffn + f0 + (lane & 15);
-      to[0] = __builtin_bit_cast(uint16_t, hi);
-      to[a.ffn] = __builtin_bit_cast(uint16_t, lo);
-    }
-    if (parts > 1) __syncthreads();                       // before the tiles are used again
   };
-  typedef std::integral_constant<int, 1> One;
-  typedef std::integral_constant<int, 16> Sixteen;
-  if constexpr (ROWS <= 4) {
-    rows_from(std::integral_constant<int, 4>{}, One{}, 0);
-  } else if constexpr (ROWS <= 16) {
-    rows_from(Sixteen{}, One{}, 0);
-  } else {
-    for (int c0 = 0; c0 < count; c0 += 32) {
-      if (count - c0 <= 16)
-        rows_from(Sixteen{}, One{}, c0);
-      else
-        rows_from(Sixteen{}, std::integral_constant<int, 2>{}, c0);
-    }
+  for (int c0 = 0; c0 < rows.count; c0 += 16 * TILES) {
+    if (rows.count - c0 <= 16)
+      go(One{}, c0);
+    else if (TILES == 2 || rows.count - c0 <= 32)
+      go(Two{}, c0);
+    else
+      go(std::integral_constant<int, TILES>{}, c0);
   }
 }
 
-// y[t] = sum over the token's entries of W2_e . A. Workgroup (h-tile, token
-// chunk): 16 values of h for up to kDecodeTokenChunk tokens; the k-steps of
-// all named experts, one after the other, are split evenly over its waves.
-// A tile's activation rows are 8 entries' high parts and the same 8 entries'
-// low parts, whose results are added. Each wave adds its results to a slice
-// of its own in LDS (a token appears once among an expert's entries), and the
-// slices are added in wave order, so the sum has one order whatever the
-// timing.
+// The chunk's plan in LDS.
+__device__ __forceinline__ void read_plan(const DecodeArgs& a, int chunk, int tokens, DecodePlan& plan) {
+  const int32_t* from = reinterpret_cast<const int32_t*>(reinterpret_cast<const DecodePlan*>(a.plan) + chunk);
+  const int words = offsetof(DecodePlan, list) / 4 + (tokens * a.topk + 1) / 2;
+  for (int i = threadIdx.x; i < words; i += blockDim.x) reinterpret_cast<int32_t*>(&plan)[i] = from[i];
+}
+
+// One stretch of the k-steps of all named experts, one expert after the other:
+// units [u, end) of unit_steps each. next() gives the steps of the next expert in it.
+template <int FMT>
+struct Stretch {
+  int64_t u, end;
+  int ns, steps;                    // units and steps of an expert
+  int slot, s0, s1;
+
+  __device__ __forceinline__ Stretch(int slots, int nb, int part, int parts) {
+    ns = k_units<FMT>(nb);
+    steps = (nb + kStepBlocks<FMT> - 1) / kStepBlocks<FMT>;
+    const int64_t units = (int64_t)slots * ns;
+    u = units * part / parts;
+    end = units * (part + 1) / parts;
+  }
+  __device__ __forceinline__ bool next() {
+    if (u >= end) return false;
+    slot = (int)(u / ns);
+    const int u0 = (int)(u % ns), u1 = (int)min((int64_t)ns, u0 + (end - u));
+    s0 = u0 * kUnit<FMT>;
+    s1 = min(u1 * kUnit<FMT>, steps);
+    u += u1 - u0;
+    return true;
+  }
+};
+
+// y[t] = sum over the token's entries of W2_e . A, for at most ROWS (2 or 16)
+// tokens. A workgroup owns 16 values of h; the k-steps of all named experts,
+// one after the other, are split evenly over its waves. A tile's activation
+// rows are up to 8 (2) entries' leading parts and the same entries' second
+// parts, whose results are added. Each wave adds its results to a slice of its
+// own in LDS (a token appears once among an expert's entries), and the slices
+// are added in wave order, so the sum has one order whatever the timing.
 template <int FMT, bool WHOLE, int ROWS>
-__global__ __launch_bounds__(512, 2) void decode_down_kernel(DecodeArgs a, int tile_bytes) {
-  extern __shared__ __align__(16) uint8_t smem[];         // [waves][tokens of the chunk][16] sums, then the waves' tiles
+__global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, int tile_bytes) {
+  extern __shared__ __align__(16) uint8_t smem[];         // [waves][tokens][16] sums, then the waves' tiles
   __shared__ DecodePlan plan;
   float* const ys = reinterpret_cast<float*>(smem);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int waves = blockDim.x >> 6;
-  const int t0 = blockIdx.y * kDecodeTokenChunk, nt = min(a.tokens - t0, kDecodeTokenChunk);
-  {
-    const DecodePlan* p = reinterpret_cast<const DecodePlan*>(a.plan) + blockIdx.y;
-    const int n = min(nt * a.topk, kDecodeMaxEntries);
-    constexpr int kHead = offsetof(DecodePlan, list) / 4;
-    for (int i = tid; i < kHead + (n + 1) / 2; i += blockDim.x)
-      reinterpret_cast<int32_t*>(&plan)[i] = reinterpret_cast<const int32_t*>(p)[i];
-  }
+  const int waves = blockDim.x >> 6, nt = a.tokens;
+  read_plan(a, 0, nt, plan);
   for (int o = tid; o < waves * nt * 16; o += blockDim.x) ys[o] = 0.f;
   __syncthreads();
-  const int nb = a.ffn / 32, ns = k_units<FMT>(nb), steps = (nb + kStepBlocks<FMT> - 1) / kStepBlocks<FMT>;
-  const int h0 = blockIdx.x * 16;
-  const int64_t units = (int64_t)plan.slots * ns;
-  int64_t u = units * wave / waves;
-  const int64_t u_end = units * (wave + 1) / waves;
+  const int nb = a.ffn / 32, h0 = blockIdx.x * 16;
   float* mine = ys + wave * nt * 16;
-  while (u < u_end) {
-    const int slot = (int)(u / ns), u0 = (int)(u % ns), u1 = (int)min((int64_t)ns, u0 + (u_end - u));
-    const int s0 = u0 * kUnit<FMT>, s1 = min(u1 * kUnit<FMT>, steps);
-    const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[slot]);
-    const int row0 = __builtin_amdgcn_readfirstlane(plan.first[slot]);
-    const int rows = __builtin_amdgcn_readfirstlane(plan.first[slot + 1]) - row0;
-    u += u1 - u0;
-    auto rows_from = [&](auto r_, auto mt_, int c0) __attribute__((always_inline)) {
-      constexpr int R = decltype(r_)::value, MT = decltype(mt_)::value, H = R / 2;
-      typedef Walk<FMT, 1, R, MT, WHOLE, MT == 1 ? kDownAhead<FMT> : 1, 1> Wk;
+  for (Stretch<FMT> st(plan.slots, nb, wave, waves); st.next();) {
+    const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[st.slot]);
+    const int row0 = __builtin_amdgcn_readfirstlane(plan.first[st.slot]);
+    const int rows = __builtin_amdgcn_readfirstlane(plan.first[st.slot + 1]) - row0;
+    auto go = [&](auto r_, int c0) __attribute__((always_inline)) {
+      constexpr int R = decltype(r_)::value, H = R / 2;
+      typedef Walk<FMT, 1, R, WHOLE, kDownAhead<FMT>> Wk;
       Wk k;
       k.nb = nb;
       const int64_t first[1] = {(int64_t)e * a.hidden + h0};
-      k.weight_tiles(a.w2, a.w2_s, first, 16);
-      k.x = reinterpret_cast<const uint8_t*>(a.act) + (int64_t)t0 * a.topk * a.ffn * 4;
+      k.tiles(a.w2, a.w2_s, first, 16);
+      k.x = reinterpret_cast<const uint8_t*>(a.act);
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int i = 0; i < Wk::XL; ++i) {
-          const int r = 4 * i + (lane >> 4);
-          const int entry = plan.list[row0 + min(c0 + H * t + r % H, rows - 1)];
-          k.xoff[t][i] = (uint32_t)(2 * entry + (r < H ? 0 : 1)) * (uint32_t)(a.ffn * 2);
-        }
-      v4f acc[1][MT];
-      clear(acc);
-      k.run(smem + waves * nt * 64 + wave * tile_bytes, s0, s1, acc);
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float v;
-          int row;
-          if constexpr (R == 4) {
-            if (q >= 2) continue;
-            v = acc[0][t][q] + acc[0][t][q + 2];
-            row = lane < 16 ? c0 + q : rows;
-          } else {
-            v = sum_halves(acc[0][t][q]);
-            row = lane < 32 ? c0 + 8 * t + (lane >> 4) * 4 + q : rows;
-          }
-          if (row < rows) mine[plan.list[row0 + row] / a.topk * 16 + (lane & 15)] += v;
-        }
-    };
-    typedef std::integral_constant<int, 1> One;
-    typedef std::integral_constant<int, 16> Sixteen;
-    if constexpr (ROWS <= 2) {
-      rows_from(std::integral_constant<int, 4>{}, One{}, 0);
-    } else if constexpr (ROWS <= 8) {
-      rows_from(Sixteen{}, One{}, 0);
-    } else {
-      for (int c0 = 0; c0 < rows; c0 += 16) {
-        if (rows - c0 <= 8)
-          rows_from(Sixteen{}, One{}, c0);
-        else
-          rows_from(Sixteen{}, std::integral_constant<int, 2>{}, c0);
+      for (int i = 0; i < Wk::XL; ++i) {
+        const int r = 4 * i + (lane >> 4);
+        k.xoff[i] = (uint32_t)(2 * plan.list[row0 + min(c0 + r % H, rows - 1)] + (r < H ? 0 : 1)) * (uint32_t)(a.ffn * 2);
       }
-    }
+      v4f acc[1][1];
+      clear(acc);
+      k.run(smem + waves * nt * 64 + wave * tile_bytes, st.s0, st.s1, acc);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v;
+        int row;
+        if constexpr (R == 4) {
+          if (q >= 2) continue;
+          v = acc[0][0][q] + acc[0][0][q + 2];
+          row = lane < 16 ? c0 + q : rows;
+        } else {
+          v = sum_halves(acc[0][0][q]);
+          row = lane < 32 ? c0 + (lane >> 4) * 4 + q : rows;
+        }
+        if (row < rows) mine[plan.list[row0 + row] / a.topk * 16 + (lane & 15)] += v;
+      }
+    };
+    if (ROWS <= 2 || rows <= 2)
+      go(Four{}, 0);
+    else
+      for (int c0 = 0; c0 < rows; c0 += 8) go(Sixteen{}, c0);
   }
   __syncthreads();
   for (int o = tid; o < nt * 16; o += blockDim.x) {
     float v = 0.f;
     for (int i = 0; i < waves; ++i) v += ys[i * nt * 16 + o];
-    reinterpret_cast<__bf16*>(a.y)[(int64_t)(t0 + (o >> 4)) * a.hidden + h0 + (o & 15)] = (__bf16)v;
+    reinterpret_cast<__bf16*>(a.y)[(int64_t)(o >> 4) * a.hidden + h0 + (o & 15)] = (__bf16)v;
   }
+}
+
+// The same for more tokens: a workgroup owns 64 * NT values of h of one expert,
+// for the expert's entries among a chunk of tokens, and split blockIdx.y of the
+// ffn dimension. Its sums go to the split's plane of a.sums, a row an entry,
+// which the next kernel adds. TILES: most row tiles (8 entries each) of a pass.
+template <int FMT, bool WHOLE, int TILES, int NT>
+__global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];         // the shared tiles, the waves' tiles
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int split = blockIdx.y / a.slots, slot = blockIdx.y % a.slots, chunk = blockIdx.z;
+  const DecodePlan& plan = *(reinterpret_cast<const DecodePlan*>(a.plan) + chunk);
+  if (slot >= plan.slots) return;
+  const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[slot]);
+  const int row0 = __builtin_amdgcn_readfirstlane(plan.first[slot]);
+  const int rows = __builtin_amdgcn_readfirstlane(plan.first[slot + 1]) - row0;
+  const int64_t entry0 = (int64_t)chunk * kDecodeTokenChunk * a.topk;
+  const int nb = a.ffn / 32, n0 = (blockIdx.x * 4 + wave) * 16 * NT;
+  int64_t first[NT];
+  tile_rows<NT>(n0, a.hidden, first);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) first[n] += (int64_t)e * a.hidden;
+  auto go = [&](auto mt_, int c0) __attribute__((always_inline)) {
+    constexpr int MT = decltype(mt_)::value;
+    typedef WideWalk<FMT, NT, MT, WHOLE, 1> Wk;
+    Wk k;
+    k.nb = nb;
+    k.tiles(a.w2, a.w2_s, first, 16);
+    k.x = reinterpret_cast<const uint8_t*>(a.act + entry0 * 2 * a.ffn);
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int r = tid >> 4;
+      k.xoff[t] = (uint32_t)(2 * plan.list[row0 + min(c0 + 8 * t + (r & 7), rows - 1)] + (r >> 3)) * (uint32_t)(a.ffn * 2);
+    }
+    v4f acc[NT][MT];
+    clear(acc);
+    k.run(smem, smem + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, part_start<FMT>(nb, split, a.splits),
+          part_start<FMT>(nb, split + 1, a.splits), acc);
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = c0 + 8 * t + (lane >> 4) * 4 + q;
+        const bool ok = lane < 32 && row < rows;
+        float* to = a.sums + ((int64_t)split * a.tokens * a.topk + entry0 + (ok ? plan.list[row0 + row] : 0)) * a.hidden;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float v = sum_halves(acc[n][t][q]);
+          const int h = (int)(first[n] - (int64_t)e * a.hidden) + (lane & 15);
+          if (ok && h >= n0 + 16 * n && h < a.hidden) to[h] = v;
+        }
+      }
+  };
+  for (int c0 = 0; c0 < rows; c0 += 8 * TILES) {
+    if (rows - c0 <= 8)
+      go(One{}, c0);
+    else if (rows - c0 <= 16)
+      go(Two{}, c0);
+    else if (rows - c0 <= 24)
+      go(Three{}, c0);
+    else if (rows - c0 <= 32)
+      go(Four{}, c0);
+    else
+      go(std::integral_constant<int, TILES>{}, c0);
+  }
+}
+
+// y[t] = the sums of the token's entries and splits, added in order; 4 values a
+// thread. The rows of entries that are in no list were not written.
+__global__ __launch_bounds__(256) void decode_sum_kernel(DecodeArgs a) {
+  const int quads = a.hidden / 4, t = blockIdx.y, q = blockIdx.x * 256 + threadIdx.x;
+  if (q >= quads) return;
+  const DecodePlan& plan = *(reinterpret_cast<const DecodePlan*>(a.plan) + t / kDecodeTokenChunk);
+  v4f v = {0.f, 0.f, 0.f, 0.f};
+  for (int j = 0; j < a.topk; ++j) {
+    if (!plan.used[t % kDecodeTokenChunk * a.topk + j]) continue;
+    for (int s = 0; s < a.splits; ++s)
+      v += *reinterpret_cast<const v4f*>(a.sums + (((int64_t)s * a.tokens + t) * a.topk + j) * a.hidden + 4 * q);
+  }
+  bf16x2 o[2];
+  o[0].x = (__bf16)v.x;
+  o[0].y = (__bf16)v.y;
+  o[1].x = (__bf16)v.z;
+  o[1].y = (__bf16)v.w;
+  *reinterpret_cast<uint2*>(reinterpret_cast<__bf16*>(a.y) + (int64_t)t * a.hidden + 4 * q) =
+      make_uint2(__builtin_bit_cast(uint32_t, o[0]), __builtin_bit_cast(uint32_t, o[1]));
 }
 
 }  // namespace
 
 template <int FMT, bool WHOLE, int ROWS>
 static void decode_up_rows(const DecodeArgs& a, hipStream_t stream) {
-  const int chunks = (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk;
-  const int slots = std::min(std::min(a.tokens, kDecodeTokenChunk) * a.topk, a.experts);
-  const int ns = k_units<FMT>(a.hidden / 32), tiles = a.ffn / 16;
+  const int slots = std::min(a.tokens * a.topk, a.experts);
+  const int units = k_units<FMT>(a.hidden / 32), tiles = a.ffn / 16;
   int parts = 1;
-  while (parts < 4 && parts * 2 <= ns && (int64_t)tiles * slots * chunks * parts * 2 <= kWavesWanted) parts *= 2;
-  constexpr int A = kUpAhead<FMT>;
-  constexpr int tile = kRowList + (ROWS <= 4 ? std::max(Walk<FMT, 2, 4, 1, WHOLE, A, 1>::kLds, 2048)
-                                   : ROWS <= 16 ? std::max(Walk<FMT, 2, 16, 1, WHOLE, A, 1>::kLds, 2048)
-                                                : std::max(Walk<FMT, 2, 16, 2, WHOLE, A, 1>::kLds, 4096));
-  const int teams = 4 / parts;
-  hipLaunchKernelGGL((decode_up_kernel<FMT, WHOLE, ROWS>), dim3((tiles + teams - 1) / teams + 1, slots, chunks), dim3(256),
-                     (size_t)std::max(4 * tile, kPlanLds), stream, a, parts, tile);
+  while (parts < 4 && parts * 2 <= units) parts *= 2;
+  constexpr int tile = kRowList + std::max(Walk<FMT, 2, ROWS, WHOLE, kUpAhead<FMT>>::kLds, 2048);
+  const int waves = std::max(4, parts), teams = waves / parts;
+  hipLaunchKernelGGL((decode_up_kernel<FMT, WHOLE, ROWS>), dim3((tiles + teams - 1) / teams + 1, slots), dim3(64 * waves),
+                     (size_t)std::max(waves * tile, kPlanLds), stream, a, parts, tile);
 }
 
-template <int FMT, bool WHOLE, int ROWS>
-static void decode_down_rows(const DecodeArgs& a, hipStream_t stream) {
-  const int nt = std::min(a.tokens, kDecodeTokenChunk), waves = 8;
-  constexpr int A = kDownAhead<FMT>;
-  constexpr int tile = ROWS <= 2   ? Walk<FMT, 1, 4, 1, WHOLE, A, 1>::kLds
-                       : ROWS <= 8 ? Walk<FMT, 1, 16, 1, WHOLE, A, 1>::kLds
-                                   : std::max(Walk<FMT, 1, 16, 1, WHOLE, A, 1>::kLds, Walk<FMT, 1, 16, 2, WHOLE, 1, 1>::kLds);
-  hipLaunchKernelGGL((decode_down_kernel<FMT, WHOLE, ROWS>),
-                     dim3(a.hidden / 16, (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk), dim3(64 * waves),
-                     (size_t)waves * (nt * 64 + tile), stream, a, tile);
+// Experts that a chunk of tokens can name.
+static int decode_slots(int tokens, int topk, int experts) {
+  return std::min(std::min(tokens, kDecodeTokenChunk) * topk, experts);
+}
+// Whether few of a chunk's entries fall to one expert in the mean.
+static bool few_each(const DecodeArgs& a, int rows) {
+  return (int64_t)std::min(a.tokens, kDecodeTokenChunk) * a.topk <= (int64_t)rows * a.experts;
+}
+
+template <int FMT, bool WHOLE, int TILES>
+static void decode_up_wide(const DecodeArgs& a, hipStream_t stream) {
+  const int chunks = (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk;
+  typedef WideWalk<FMT, 2, TILES, WHOLE, kWideAhead<FMT>> Wk;
+  hipLaunchKernelGGL((decode_up_wide_kernel<FMT, WHOLE, TILES>),
+                     dim3((a.ffn / 16 + 3) / 4 + 1, decode_slots(a.tokens, a.topk, a.experts), chunks), dim3(256),
+                     (size_t)std::max(4 * kRowList + Wk::kShared + 4 * Wk::Wt::kLds, kPlanLds), stream, a);
 }
 
 template <int FMT, bool WHOLE>
@@ -801,18 +1139,39 @@ static void decode_up_go(const DecodeArgs& a, hipStream_t stream) {
     decode_up_rows<FMT, WHOLE, 4>(a, stream);
   else if (a.tokens <= 16)
     decode_up_rows<FMT, WHOLE, 16>(a, stream);
+  else if (few_each(a, 16))
+    decode_up_wide<FMT, WHOLE, 3>(a, stream);
   else
-    decode_up_rows<FMT, WHOLE, kDecodeTokenChunk>(a, stream);
+    decode_up_wide<FMT, WHOLE, 4>(a, stream);
+}
+
+template <int FMT, bool WHOLE, int ROWS>
+static void decode_down_rows(const DecodeArgs& a, hipStream_t stream) {
+  constexpr int waves = 8, tile = Walk<FMT, 1, ROWS <= 2 ? 4 : 16, WHOLE, kDownAhead<FMT>>::kLds;
+  hipLaunchKernelGGL((decode_down_kernel<FMT, WHOLE, ROWS>), dim3(a.hidden / 16), dim3(64 * waves),
+                     (size_t)waves * (a.tokens * 64 + tile), stream, a, tile);
+}
+
+template <int FMT, bool WHOLE, int TILES, int NT>
+static void decode_down_wide(DecodeArgs a, hipStream_t stream) {
+  const int chunks = (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk;
+  typedef WideWalk<FMT, NT, TILES, WHOLE, 1> Wk;
+  a.slots = decode_slots(a.tokens, a.topk, a.experts);
+  hipLaunchKernelGGL((decode_down_wide_kernel<FMT, WHOLE, TILES, NT>),
+                     dim3((a.hidden + 64 * NT - 1) / (64 * NT), a.slots * a.splits, chunks), dim3(256),
+                     (size_t)(Wk::kShared + 4 * Wk::Wt::kLds), stream, a);
 }
 
 template <int FMT, bool WHOLE>
 static void decode_down_go(const DecodeArgs& a, hipStream_t stream) {
-  if (a.tokens <= 2)
-    decode_down_rows<FMT, WHOLE, 2>(a, stream);
-  else if (a.tokens <= 8)
-    decode_down_rows<FMT, WHOLE, 8>(a, stream);
+  if (a.tokens <= 2) return decode_down_rows<FMT, WHOLE, 2>(a, stream);
+  if (a.splits == 0) return decode_down_rows<FMT, WHOLE, 16>(a, stream);
+  // three row tiles hold the 24 entries that few experts pass where 16 are the mean
+  if (few_each(a, 16))
+    decode_down_wide<FMT, WHOLE, 6, 2>(a, stream);
   else
-    decode_down_rows<FMT, WHOLE, kDecodeTokenChunk>(a, stream);
+    decode_down_wide<FMT, WHOLE, 8, 2>(a, stream);
+  hipLaunchKernelGGL(decode_sum_kernel, dim3((a.hidden / 4 + 255) / 256, a.tokens), dim3(256), 0, stream, a);
 }
 
 template <int FMT>
@@ -826,6 +1185,16 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
   else
     decode_down_go<FMT, false>(a, stream);
   return hipGetLastError();
+}
+
+// Splits of the wide second product, 0 where the narrow one runs: for up to 8
+// tokens, and up to 16 with few entries an expert. About two workgroups a
+// compute unit, at least 512 values of k each.
+int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn) {
+  if (tokens <= 8 || (tokens <= 16 && tokens * topk <= 4 * experts)) return 0;
+  const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
+  const int64_t slots = decode_slots((int)tokens, topk, experts);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, ffn / 512), 1536 / (groups * slots)));
 }
 
 hipError_t launch_decode(int fmt, const DecodeArgs& a, hipStream_t stream) {

@@ -292,14 +292,17 @@ struct GemvArgs {
   int64_t m, n, k;
   void* y;
   int32_t y_f32;
+  float* sums;                      // [splits, m, n] (splits > 1)
+  int32_t splits;                   // of gemv_splits
 };
+int gemv_splits(int64_t m, int64_t n, int64_t k);
 hipError_t launch_gemv(int fmt, const GemvArgs& a, hipStream_t stream);
 // The MoE MLP of a few tokens (tokens * topk <= kDecodeMaxEntries; hidden and
 // ffn at most kDecodeMaxDim, so that the kernels' row offsets fit 32 bits).
 constexpr int kDecodeMaxEntries = MX_DECODE_MAX_ENTRIES;
 constexpr int64_t kDecodeMaxDim = 1 << 19;
 constexpr int kDecodeTokenChunk = 64;  // tokens that one workgroup sees
-constexpr int kDecodePlanBytes = 4 * (2 * MX_MAX_GROUPS + 2) + 2 * kDecodeMaxEntries;   // per chunk of tokens
+constexpr int kDecodePlanBytes = 4 * (2 * MX_MAX_GROUPS + 2) + 3 * kDecodeMaxEntries;   // per chunk of tokens
 struct DecodeArgs {
   const uint8_t* x;                 // bf16 [tokens, hidden]
   const int32_t* topk_idx;          // [tokens, topk]
@@ -310,9 +313,12 @@ struct DecodeArgs {
   const uint8_t* w2_s;
   void* plan;                       // kDecodePlanBytes per chunk of tokens
   uint16_t* act;                    // bf16 [tokens * topk, 2, ffn]: A's leading part and what it leaves
+  float* sums;                      // [splits, tokens, topk, hidden] of the wide second product
+  int32_t splits, slots;            // its splits of ffn (0: not used), experts that a chunk can name
   void* y;                          // bf16 [tokens, hidden]
   int32_t tokens, topk, experts, hidden, ffn;
 };
+int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn);
 hipError_t launch_decode(int fmt, const DecodeArgs& a, hipStream_t stream);
 
 // Router (mx_route.hip).

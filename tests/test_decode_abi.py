@@ -22,11 +22,11 @@ def L():
 
 
 def test_gemv_refusals(L):
-    def fp4(x=FAKE, ldx=64, w=FAKE, ws=FAKE, m=2, n=5, k=64, y=FAKE, dt=0):
-        return L.mx_gemv_fp4(x, ldx, w, ws, m, n, k, y, dt, None)
+    def fp4(x=FAKE, ldx=64, w=FAKE, ws=FAKE, m=2, n=5, k=64, y=FAKE, dt=0, wk=None, nb=0):
+        return L.mx_gemv_fp4(x, ldx, w, ws, m, n, k, y, dt, wk, nb, None)
 
-    def nv(x=FAKE, ldx=64, w=FAKE, ws=FAKE, am=FAKE, m=2, n=5, k=64, y=FAKE, dt=1):
-        return L.mx_gemv_nvfp4(x, ldx, w, ws, am, m, n, k, y, dt, None)
+    def nv(x=FAKE, ldx=64, w=FAKE, ws=FAKE, am=FAKE, m=2, n=5, k=64, y=FAKE, dt=1, wk=None, nb=0):
+        return L.mx_gemv_nvfp4(x, ldx, w, ws, am, m, n, k, y, dt, wk, nb, None)
 
     assert fp4(x=None) == fp4(w=None) == fp4(ws=None) == fp4(y=None) == nv(am=None) == EINVAL
     assert fp4(dt=2) == EINVAL
@@ -37,6 +37,16 @@ def test_gemv_refusals(L):
     assert fp4(x=ODD) == fp4(w=ODD) == fp4(y=ODD) == nv(ws=ODD) == nv(am=ODD) == EALIGN
     assert b"mx_gemv_nvfp4" in L.mx_last_error()
     assert fp4(m=0) == fp4(n=0) == nv(m=0, x=None) == OK
+    # a product that splits k over workgroups needs its planes
+    n = ctypes.c_size_t()
+    assert L.mx_gemv_sizes(16, 4096, 14336, ctypes.byref(n)) == OK and n.value == 0
+    assert L.mx_gemv_sizes(40, 4096, 14336, ctypes.byref(n)) == OK and n.value % (40 * 4096 * 4) == 0 and n.value > 0
+    big = dict(m=40, n=4096, k=14336, ldx=14336)
+    assert fp4(**big) == nv(**big) == EINVAL
+    assert fp4(**big, wk=FAKE, nb=n.value - 1) == nv(**big, wk=FAKE, nb=0) == EWORKSPACE
+    assert fp4(**big, wk=ctypes.c_void_p(0x100010), nb=n.value) == EALIGN
+    assert L.mx_gemv_sizes(1, 1, 31, None) == L.mx_gemv_sizes(-1, 1, 32, None) == ESHAPE
+    assert L.mx_gemv_sizes(65537, 1, 32, None) == EUNSUPPORTED
 
 
 def test_decode_refusals(L):

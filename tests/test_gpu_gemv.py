@@ -27,7 +27,7 @@ def _u8(a):
 
 SIZES = [(1, 1, 32), (1, 16, 32), (1, 17, 64), (2, 33, 96), (3, 250, 160), (1, 999, 544), (7, 64, 2080), (8, 48, 1024),
          (9, 100, 480), (16, 130, 4096), (17, 31, 288), (31, 65, 512), (33, 20, 2336), (48, 80, 352), (64, 100, 704),
-         (65, 35, 96), (130, 50, 224)]
+         (65, 35, 96), (130, 50, 224), (40, 300, 4096), (64, 129, 7200)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
