@@ -943,19 +943,15 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
 MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
 
 
-def _fits(t, shape, dtype, dev):
-    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous()
-
-
-def _misfit(who, name, t, shape, dtype, dev):
-    got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else str(type(t))
-    return ValueError(f"{who}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {got}")
-
-
 def _need(who, name, t, shape, dtype, dev):
-    if not _fits(t, shape, dtype, dev):
-        raise _misfit(who, name, t, shape, dtype, dev)
-    return t.data_ptr()
+    """The address of t, a contiguous tensor of that shape, dtype and device."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+        got = f"{t.dtype} {tuple(t.shape)} on {t.device}"
+    except AttributeError:
+        got = str(type(t))
+    raise ValueError(f"{who}: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {got}")
 
 
 def _opt(who, name, t, shape, dtype, dev):
@@ -976,7 +972,7 @@ def _call(fn, dev, stream, *args):
     """fn(*args, stream) with the tensors' device current: on its current
     stream, or the given one."""
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
@@ -1042,8 +1038,8 @@ def mx_gemv_nvfp4(x, w_q, w_s, w_amax, out_dtype=torch.bfloat16, out=None, works
 @functools.lru_cache(maxsize=4096)
 def _decode_dims(E, T, H, F, k):
     """The dims of a decode call and its workspace's bytes."""
-    dims, nbytes = _Dims(E, T, H, F), ctypes.c_size_t()
-    _check(load().grouped_mlp_decode_sizes(ctypes.byref(dims), k, ctypes.byref(nbytes)))
+    dims, nbytes = ctypes.byref(_Dims(E, T, H, F)), ctypes.c_size_t()
+    _check(load().grouped_mlp_decode_sizes(dims, k, ctypes.byref(nbytes)))
     return dims, nbytes.value
 
 
@@ -1088,7 +1084,7 @@ def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out
         y = out.data_ptr()
     else:
         y = _need(who, "out", out, (T, H), torch.bfloat16, dev)
-    _call(load().grouped_mlp_decode, dev, stream, ctypes.byref(dims), k, fmt, *args, y,
+    _call(load().grouped_mlp_decode, dev, stream, dims, k, fmt, *args, y,
           None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
     return out
 

@@ -169,26 +169,31 @@ struct Weights {
       for (int i = 0; i < W; ++i)
         to[n][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[n] + (t < s1 ? woff[i] + at : 0u)));
   }
-  // 16 bytes of a scale row per lane: the G steps from s
+  // 16 bytes of a scale row per lane: the G steps from s. Where rows are not
+  // whole steps, a window that would pass the row's end begins earlier
+  // (scale_shift), and a row of less than 16 bytes is read byte by byte.
   __device__ __forceinline__ void load_scales(int s) {
     if constexpr (S > 0) {
       const int lane = threadIdx.x & 63, row_bytes = nb * S, at = s * SB + lane % LR * 16;
       if constexpr (WHOLE) {
         sr = *reinterpret_cast<const u32x4*>(ws + (at < row_bytes ? at : 0));
+      } else if (row_bytes >= 16) {
+        __builtin_memcpy(&sr, ws + min(at, row_bytes - 16), 16);
       } else {
-        // byte by byte, the row's last one repeated (its blocks count as zero)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           uint32_t v = 0;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int i = at + 4 * q + b;
-            v |= (uint32_t)ws[i < row_bytes ? i : row_bytes - S + (i & (S - 1))] << (8 * b);
-          }
+          for (int b = 0; b < 4; ++b) v |= (uint32_t)ws[min(4 * q + b, row_bytes - 1)] << (8 * b);
           sr[q] = v;
         }
       }
     }
+  }
+  // how much later the scale at byte `at` of a row lies in its window
+  __device__ __forceinline__ int scale_shift(int at) const {
+    const int row_bytes = nb * S;
+    return WHOLE || row_bytes < 16 ? 0 : max(0, (at & ~15) + 16 - row_bytes);
   }
   // the scales of the group that begins at step s, and the next group's load
   __device__ __forceinline__ void stage_scales(uint8_t* lds, int s) {
@@ -216,15 +221,17 @@ struct Weights {
         *reinterpret_cast<u32x4*>(lds + n * kTile + (row * 4 * W + (c ^ (row & (4 * W - 1)))) * 16) = v;
       }
   }
-  // tile n's block of the lane (half h of the step, step in_group of its scale group) as 4 fragments
-  __device__ __forceinline__ void fragments(const uint8_t* lds, int n, int h, int in_group, bf16x8 (&wf)[4]) const {
+  // tile n's block of the lane (half h of step t, the in_group-th of its scale group) as 4 fragments
+  __device__ __forceinline__ void fragments(const uint8_t* lds, int n, int t, int h, int in_group, bf16x8 (&wf)[4]) const {
     const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
     u32x4 q[BW];
     uint32_t sc = 0;
 #pragma unroll
     for (int i = 0; i < BW; ++i)
       q[i] = *reinterpret_cast<const u32x4*>(lds + n * kTile + (li * 4 * W + (((h * 4 + g) * BW + i) ^ (li & (4 * W - 1)))) * 16);
-    const uint8_t* p = lds + NT * kTile + (n * 16 + li) * 16 * LR + in_group * SB + (h * 4 + g) * S;
+    // (a block past the row's end has codes of zero, and its scale is any of the row's)
+    const int shift = min(scale_shift(t * SB + (h * 4 + g) * S), 15 - ((in_group * SB + (h * 4 + g) * S) & 15));
+    const uint8_t* p = lds + NT * kTile + (n * 16 + li) * 16 * LR + in_group * SB + (h * 4 + g) * S + (S == 2 ? shift & ~1 : shift);
     if constexpr (S == 1) sc = *p;
     if constexpr (S == 2) sc = *reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
@@ -302,7 +309,7 @@ struct Walk : Weights<FMT, NT, WHOLE, D> {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           bf16x8 wf[4];
-          this->fragments(lds, n, h, in_group + u, wf);
+          this->fragments(lds, n, t, h, in_group + u, wf);
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[n][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], wf[j], acc[n][0], 0, 0, 0);
         }
@@ -377,7 +384,7 @@ struct WideWalk : Weights<FMT, NT, WHOLE, D> {
         wave_lds_fence();
         bf16x8 wf[NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) this->fragments(lds, n, h, in_group + u, wf[n]);
+        for (int n = 0; n < NT; ++n) this->fragments(lds, n, t, h, in_group + u, wf[n]);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll

@@ -331,6 +331,7 @@ struct RouteArgs {
   int32_t* topk_idx;                // [tokens, topk]
   float* topk_w;                    // [tokens, topk]
   float* lse;                       // [tokens]
+  int32_t vec;                      // set by the launch: rows can be read four values at a time
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 struct RouteBwdArgs {
@@ -346,6 +347,7 @@ struct RouteBwdArgs {
   int64_t tokens;
   int32_t experts, topk, renorm;
   void* dlogits;
+  int32_t vec;                      // as in RouteArgs
 };
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t stream);
 
