@@ -1114,8 +1114,13 @@ template <int FMT, bool WHOLE, int ROWS>
 static void decode_up_rows(const DecodeArgs& a, hipStream_t stream) {
   const int slots = std::min(a.tokens * a.topk, a.experts);
   const int units = k_units<FMT>(a.hidden / 32), tiles = a.ffn / 16;
+  // A team of 4 reads whole rows at about one time (one row a wave, 4096 bytes
+  // apart, is what memory likes least: 8-bit, 7 tokens of 8 experts, 4096 x
+  // 14336: parts 1 171 us, 4 133 us). Rows of less than 8 units are split only as
+  // far as two units a wave, unless that leaves the chip empty (128 experts, 8
+  // tokens, 2048 x 768, 4-bit: 4 units in 4 parts 23.0 us, in 2 parts 20.5 us).
   int parts = 1;
-  while (parts < 4 && parts * 2 <= units) parts *= 2;
+  while (parts < 4 && parts * 2 <= units && (parts * 4 <= units || (int64_t)tiles * slots * parts <= 1024)) parts *= 2;
   constexpr int tile = kRowList + std::max(Walk<FMT, 2, ROWS, WHOLE, kUpAhead<FMT>>::kLds, 2048);
   const int waves = std::max(4, parts), teams = waves / parts;
   hipLaunchKernelGGL((decode_up_kernel<FMT, WHOLE, ROWS>), dim3((tiles + teams - 1) / teams + 1, slots), dim3(64 * waves),
@@ -1171,7 +1176,7 @@ static void decode_down_wide(DecodeArgs a, hipStream_t stream) {
 
 template <int FMT, bool WHOLE>
 static void decode_down_go(const DecodeArgs& a, hipStream_t stream) {
-  if (a.tokens <= 2) return decode_down_rows<FMT, WHOLE, 2>(a, stream);
+  if (a.splits == 0 && a.tokens <= 2) return decode_down_rows<FMT, WHOLE, 2>(a, stream);
   if (a.splits == 0) return decode_down_rows<FMT, WHOLE, 16>(a, stream);
   // three row tiles hold the 24 entries that few experts pass where 16 are the mean
   if (few_each(a, 16))
@@ -1194,13 +1199,16 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Splits of the wide second product, 0 where the narrow one runs: for up to 8
-// tokens, and up to 16 with few entries an expert. About two workgroups a
-// compute unit, at least 512 values of k each.
+// Splits of the wide second product, 0 where the narrow one runs: for up to 16
+// tokens that can name up to 16 experts (each expert is a stretch of its own of
+// every wave there: 128 experts of 2048 x 768, 16 tokens: narrow 75 us for the
+// layer, wide 66 us; 8 experts of 4096 x 14336, 1 token: narrow 38 us, wide 47
+// us). About six workgroups a compute unit (4 resident at once, 64 tokens of 8
+// experts: 3 a unit 126 us, 6 a unit 100 us), at least 512 values of k each.
 int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn) {
-  if (tokens <= 8 || (tokens <= 16 && tokens * topk <= 4 * experts)) return 0;
-  const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
   const int64_t slots = decode_slots((int)tokens, topk, experts);
+  if (tokens <= 16 && slots <= 16 && tokens * topk <= 4 * slots) return 0;
+  const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, ffn / 512), 1536 / (groups * slots)));
 }
 
