@@ -400,6 +400,17 @@ struct WideWalk : Weights<FMT, NT, WHOLE, D> {
       in_group = in_group + D < G ? in_group + D : 0;
     }
   }
+
+  // Steps [s0, s1), beginning at a place of the workgroup's own where rows are a
+  // multiple of 4096 bytes apart: workgroups that walk such rows from the same k
+  // at one time meet in the same memory channels (8-bit, 24 tokens of 8 experts,
+  // 4096 x 14336: 300 us from one k, 258 us from four).
+  __device__ __forceinline__ void run_around(uint8_t* shared, uint8_t* lds, int s0, int s1, int turn, v4f (&acc)[NT][MT]) {
+    int from = s0;
+    if (this->nb * 16 * Wt::BW % 4096 == 0) from += (s1 - s0) / kUnit<FMT> * (turn % 4) / 4 * kUnit<FMT>;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) run(shared, lds, i == 0 ? from : s0, i == 0 ? s1 : from, acc);
+  }
 };
 
 template <int NT, int MT>
@@ -501,8 +512,8 @@ __global__ __launch_bounds__(256, 2) void gemv_wide_kernel(GemvArgs a) {
   for (int t = 0; t < MT; ++t) k.xoff[t] = (uint32_t)min(16 * t + (tid >> 4), m - 1 - m0) * (uint32_t)(a.ldx * 2);
   v4f acc[NT][MT];
   clear(acc);
-  k.run(smem, smem + Wk::kShared + wave * Wk::Wt::kLds, part_start<FMT>(k.nb, split, a.splits),
-        part_start<FMT>(k.nb, split + 1, a.splits), acc);
+  k.run_around(smem, smem + Wk::kShared + wave * Wk::Wt::kLds, part_start<FMT>(k.nb, split, a.splits),
+               part_start<FMT>(k.nb, split + 1, a.splits), blockIdx.x, acc);
   const float scale = result_scale<FMT>(a);
   float* const plane = a.sums + (int64_t)split * m * n;
 #pragma unroll
@@ -900,8 +911,8 @@ __global__ __launch_bounds__(256, 2) void decode_up_wide_kernel(DecodeArgs a) {
       k.xoff[t] = (uint32_t)(rows.entry[min(c0 + 16 * t + (tid >> 4), rows.count - 1)] / en.topk) * (uint32_t)(a.hidden * 2);
     v4f acc[2][MT];
     clear(acc);
-    k.run(smem + 4 * kRowList, smem + 4 * kRowList + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, 0,
-          part_start<FMT>(nb, 1, 1), acc);
+    k.run_around(smem + 4 * kRowList, smem + 4 * kRowList + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, 0,
+                 part_start<FMT>(nb, 1, 1), blockIdx.x, acc);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -1056,8 +1067,8 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
     }
     v4f acc[NT][MT];
     clear(acc);
-    k.run(smem, smem + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, part_start<FMT>(nb, split, a.splits),
-          part_start<FMT>(nb, split + 1, a.splits), acc);
+    k.run_around(smem, smem + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, part_start<FMT>(nb, split, a.splits),
+                 part_start<FMT>(nb, split + 1, a.splits), blockIdx.x, acc);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
