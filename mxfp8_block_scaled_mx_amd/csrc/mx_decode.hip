@@ -156,8 +156,11 @@ struct Weights {
       woff[i] = (uint32_t)min((i * 64 + lane) / (4 * W), left - 1) * (uint32_t)(nb * 16 * BW);
   }
 
-  // a load past the end is issued all the same (the number of loads in flight
-  // stays fixed), with every lane at one address
+  // A load past the end is issued all the same (the number of loads in flight
+  // stays fixed), with every lane at one address. Pieces of ragged rows share
+  // their first and last cache line with the next step, so they are not
+  // nontemporal (4-bit, 3 rows, 11740 x 14624: 26.8 us nontemporal, 19.2 us
+  // plain; whole rows gain from it: reading alone 6.25 TB/s plain, 6.9 TB/s).
   __device__ __forceinline__ void load(int t, u32x4 (&to)[NT][W]) {
     const int lane = threadIdx.x & 63;
     const int c = lane % (4 * W);
@@ -166,8 +169,13 @@ struct Weights {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        to[n][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[n] + (t < s1 ? woff[i] + at : 0u)));
+      for (int i = 0; i < W; ++i) {
+        const u32x4* from = reinterpret_cast<const u32x4*>(w[n] + (t < s1 ? woff[i] + at : 0u));
+        if constexpr (WHOLE)
+          to[n][i] = __builtin_nontemporal_load(from);
+        else
+          to[n][i] = *from;
+      }
   }
   // 16 bytes of a scale row per lane: the G steps from s. Where rows are not
   // whole steps, a window that would pass the row's end begins earlier
@@ -360,14 +368,15 @@ struct WideWalk : Weights<FMT, NT, WHOLE, D> {
     };
     // half step t's activations are in LDS before it begins; those of the DX after it are on their way
     this->load_scales(s0);
-    load_x(s0 * H, xr[0]);
-    team_barrier();                                       // the buffers are free
-    stage_x(s0 * H, xr[0]);
+    u32x4 x0[MT];
+    load_x(s0 * H, x0);
 #pragma unroll
     for (int d = 0; d < DX; ++d) {
       load_x(s0 * H + d + 1, xr[d]);
       if (d % H == 0) this->load(s0 + d / H, this->wr[d / H]);
     }
+    team_barrier();                                       // the buffers are free
+    stage_x(s0 * H, x0);
     team_barrier();
     int in_group = 0;
     for (int s = s0; s < s1; s += D) {
@@ -538,6 +547,7 @@ __global__ __launch_bounds__(256) void gemv_sum_kernel(GemvArgs a) {
   const float scale = result_scale<FMT>(a);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
     float v = 0.f;
+#pragma unroll 4
     for (int s = 0; s < a.splits; ++s) v += a.sums[s * n + i];
     v *= scale;
     if (a.y_f32)
@@ -632,10 +642,14 @@ namespace {
 // outside [0, E) matches no expert; of a token's entries that name the same
 // expert, the first stands for all, with the sum of their weights.
 //
-// Entries are taken in groups of whole tokens, at most 64 entries.
+// Entries are taken in groups of whole tokens, at most 64 entries. stage() puts
+// them into LDS for the workgroup, so that what follows waits for memory once
+// (61 tokens, 5 choices among 60 experts of 544 x 4288, 4-bit, first product:
+// BEFORE us reading them from memory, AFTER us).
 struct Entries {
   const int32_t* idx;               // the chunk's entries
   int n, topk, per;                 // entries, choices per token, entries per group (topk * floor(64 / topk))
+  float* weight;                    // in LDS: the weights of n entries, then their experts (0xFF: none)
 
   __device__ __forceinline__ Entries(const DecodeArgs& a, int chunk) {
     const int t0 = chunk * kDecodeTokenChunk;
@@ -644,12 +658,21 @@ struct Entries {
     n = min(a.tokens - t0, kDecodeTokenChunk) * topk;
     per = 64 / topk * topk;
   }
-  // the lane's expert in the group from entry g0, or -1
-  __device__ __forceinline__ int expert(int g0, int lane, int32_t E) const {
+  __host__ __device__ static constexpr int bytes(int entries) { return (entries * 5 + 15) & ~15; }
+  __device__ __forceinline__ void stage(const DecodeArgs& a, int chunk, uint8_t* lds) {
+    weight = reinterpret_cast<float*>(lds);
+    const float* w = a.topk_w != nullptr ? a.topk_w + (int64_t)chunk * kDecodeTokenChunk * topk : nullptr;
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const int32_t e = idx[i];
+      weight[i] = w != nullptr ? w[i] : 1.0f;
+      lds[4 * n + i] = e < 0 || e >= a.experts ? 0xFF : (uint8_t)e;
+    }
+    __syncthreads();
+  }
+  // the lane's expert in the group from entry g0, or 0xFF
+  __device__ __forceinline__ int expert(int g0, int lane) const {
     const int i = g0 + lane;
-    if (lane >= per || i >= n) return -1;
-    const int32_t e = idx[i];
-    return e < 0 || e >= E ? -1 : e;
+    return lane < per && i < n ? reinterpret_cast<const uint8_t*>(weight)[4 * n + i] : 0xFF;
   }
   // of the lanes in `same` (those that name one expert), the first of each token
   __device__ __forceinline__ bool first_of_token(uint64_t same, int lane) const {
@@ -747,14 +770,14 @@ struct ExpertRows {
   const int32_t* entry;
   const float* weight;
 
-  __device__ __forceinline__ ExpertRows(const DecodeArgs& a, const Entries& en, int chunk, int slot, uint8_t* lds) {
+  __device__ __forceinline__ ExpertRows(const Entries& en, int slot, uint8_t* lds) {
     const int lane = threadIdx.x & 63;
     uint32_t* const set = reinterpret_cast<uint32_t*>(lds);
     if (lane < kMaxGroups / 32) set[lane] = 0;
     wave_lds_fence();
     for (int g0 = 0; g0 < en.n; g0 += en.per) {
-      const int e = en.expert(g0, lane, a.experts);
-      if (e >= 0) atomicOr(&set[e >> 5], 1u << (e & 31));
+      const int e = en.expert(g0, lane);
+      if (e < kMaxGroups) atomicOr(&set[e >> 5], 1u << (e & 31));
     }
     wave_lds_fence();
     expert = -1;
@@ -774,9 +797,8 @@ struct ExpertRows {
     if (expert < 0) return;
     int32_t* const rows = reinterpret_cast<int32_t*>(lds);
     float* const w = reinterpret_cast<float*>(lds) + kDecodeTokenChunk;
-    const float* wts = a.topk_w != nullptr ? a.topk_w + (int64_t)chunk * kDecodeTokenChunk * a.topk : nullptr;
     for (int g0 = 0; g0 < en.n; g0 += en.per) {
-      const uint64_t same = __ballot(en.expert(g0, lane, a.experts) == expert);
+      const uint64_t same = __ballot(en.expert(g0, lane) == expert);
       if (same == 0) continue;
       const bool keep = en.first_of_token(same, lane);
       const uint64_t firsts = __ballot(keep);
@@ -784,7 +806,7 @@ struct ExpertRows {
         float wt = 0.f;
         const int end = lane - lane % en.topk + en.topk;
         for (int j = lane; j < end; ++j)
-          if ((same >> j) & 1ull) wt += wts != nullptr ? wts[g0 + j] : 1.0f;
+          if ((same >> j) & 1ull) wt += en.weight[g0 + j];
         const int at = count + bits_below(firsts, lane);
         rows[at] = g0 + lane;
         w[at] = wt;
@@ -830,9 +852,11 @@ __global__ __launch_bounds__(512, 2) void decode_up_kernel(DecodeArgs a, int par
     if (slot == 0) write_plan(a, 0, smem);
     return;
   }
-  uint8_t* const mine = smem + wave * tile_bytes;
-  const Entries en(a, 0);
-  const ExpertRows rows(a, en, 0, slot, mine);
+  Entries en(a, 0);
+  en.stage(a, 0, smem);
+  uint8_t* const tiles_at = smem + Entries::bytes(en.n);
+  uint8_t* const mine = tiles_at + wave * tile_bytes;
+  const ExpertRows rows(en, slot, mine);
   if (rows.expert < 0) return;                            // all of the workgroup leaves
   const int team = wave / parts, part = wave % parts;
   const int tile = (int)blockIdx.x * (waves / parts) + team, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
@@ -866,7 +890,7 @@ __global__ __launch_bounds__(512, 2) void decode_up_kernel(DecodeArgs a, int par
       if (parts > 1) {
         g = up = 0.f;
         for (int i = 0; i < parts; ++i) {
-          const float* p = reinterpret_cast<const float*>(smem + (size_t)(wave - part + i) * tile_bytes + kRowList) + lane;
+          const float* p = reinterpret_cast<const float*>(tiles_at + (wave - part + i) * tile_bytes + kRowList) + lane;
           g += p[r * 64];
           up += p[(4 + r) * 64];
         }
@@ -893,8 +917,10 @@ __global__ __launch_bounds__(256, 2) void decode_up_wide_kernel(DecodeArgs a) {
     if (slot == 0) write_plan(a, chunk, smem);
     return;
   }
-  const Entries en(a, chunk);
-  const ExpertRows rows(a, en, chunk, slot, smem + wave * kRowList);
+  Entries en(a, chunk);
+  uint8_t* const tiles_at = smem + 4 * kRowList;
+  en.stage(a, chunk, tiles_at + 2 * TILES * 4096 + 4 * Weights<FMT, 2, WHOLE, kWideAhead<FMT>>::kLds);
+  const ExpertRows rows(en, slot, smem + wave * kRowList);
   if (rows.expert < 0) return;
   const int tile = (int)blockIdx.x * 4 + wave, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
   const int nb = a.hidden / 32;
@@ -911,7 +937,7 @@ __global__ __launch_bounds__(256, 2) void decode_up_wide_kernel(DecodeArgs a) {
       k.xoff[t] = (uint32_t)(rows.entry[min(c0 + 16 * t + (tid >> 4), rows.count - 1)] / en.topk) * (uint32_t)(a.hidden * 2);
     v4f acc[2][MT];
     clear(acc);
-    k.run_around(smem + 4 * kRowList, smem + 4 * kRowList + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, 0,
+    k.run_around(tiles_at, tiles_at + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, 0,
                  part_start<FMT>(nb, 1, 1), blockIdx.x, acc);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -1043,10 +1069,11 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = blockIdx.y / a.slots, slot = blockIdx.y % a.slots, chunk = blockIdx.z;
   const DecodePlan& plan = *(reinterpret_cast<const DecodePlan*>(a.plan) + chunk);
-  if (slot >= plan.slots) return;
-  const int e = __builtin_amdgcn_readfirstlane(plan.slot_e[slot]);
-  const int row0 = __builtin_amdgcn_readfirstlane(plan.first[slot]);
-  const int rows = __builtin_amdgcn_readfirstlane(plan.first[slot + 1]) - row0;
+  // (all four loads at once; those of a slot past the last are not used)
+  const int slots = plan.slots, expert = plan.slot_e[slot], from = plan.first[slot], to = plan.first[slot + 1];
+  if (slot >= slots) return;
+  const int e = __builtin_amdgcn_readfirstlane(expert), row0 = __builtin_amdgcn_readfirstlane(from);
+  const int rows = __builtin_amdgcn_readfirstlane(to) - row0;
   const int64_t entry0 = (int64_t)chunk * kDecodeTokenChunk * a.topk;
   const int nb = a.ffn / 32, n0 = (blockIdx.x * 4 + wave) * 16 * NT;
   int64_t first[NT];
@@ -1098,18 +1125,38 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
   }
 }
 
-// y[t] = the sums of the token's entries and splits, added in order; 4 values a
-// thread. The rows of entries that are in no list were not written.
+// y[t] = the sums of the token's entries and splits; 4 values a thread. The
+// planes of a token (its entries in order, each with its splits) go round the
+// four waves, whose sums are added in wave order. The rows of entries that are
+// in no list were not written.
 __global__ __launch_bounds__(256) void decode_sum_kernel(DecodeArgs a) {
-  const int quads = a.hidden / 4, t = blockIdx.y, q = blockIdx.x * 256 + threadIdx.x;
-  if (q >= quads) return;
+  __shared__ v4f part[3][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quads = a.hidden / 4, t = blockIdx.y, q = blockIdx.x * 64 + lane;
   const DecodePlan& plan = *(reinterpret_cast<const DecodePlan*>(a.plan) + t / kDecodeTokenChunk);
+  const uint64_t used = __ballot(lane < a.topk && plan.used[t % kDecodeTokenChunk * a.topk + min(lane, a.topk - 1)] != 0);
+  const float* from = a.sums + (int64_t)t * a.topk * a.hidden + 4 * min(q, quads - 1);
+  const int64_t plane = (int64_t)a.tokens * a.topk * a.hidden;
   v4f v = {0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < a.topk; ++j) {
-    if (!plan.used[t % kDecodeTokenChunk * a.topk + j]) continue;
-    for (int s = 0; s < a.splits; ++s)
-      v += *reinterpret_cast<const v4f*>(a.sums + (((int64_t)s * a.tokens + t) * a.topk + j) * a.hidden + 4 * q);
+  const int n = a.topk * a.splits;
+  for (int p0 = wave; p0 < n; p0 += 16) {                 // 4 loads in flight
+    v4f x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = min(p0 + 4 * i, n - 1), j = p / a.splits, s = p - j * a.splits;
+      const v4f r = *reinterpret_cast<const v4f*>(from + s * plane + (int64_t)j * a.hidden);
+      const bool ok = p0 + 4 * i < n && ((used >> j) & 1ull);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[i][c] = ok ? r[c] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v += x[i];
   }
+  if (wave > 0) part[wave - 1][lane] = v;
+  __syncthreads();
+  if (wave > 0 || q >= quads) return;
+#pragma unroll
+  for (int w = 0; w < 3; ++w) v += part[w][lane];
   bf16x2 o[2];
   o[0].x = (__bf16)v.x;
   o[0].y = (__bf16)v.y;
@@ -1135,7 +1182,7 @@ static void decode_up_rows(const DecodeArgs& a, hipStream_t stream) {
   constexpr int tile = kRowList + std::max(Walk<FMT, 2, ROWS, WHOLE, kUpAhead<FMT>>::kLds, 2048);
   const int waves = std::max(4, parts), teams = waves / parts;
   hipLaunchKernelGGL((decode_up_kernel<FMT, WHOLE, ROWS>), dim3((tiles + teams - 1) / teams + 1, slots), dim3(64 * waves),
-                     (size_t)std::max(waves * tile, kPlanLds), stream, a, parts, tile);
+                     (size_t)std::max(Entries::bytes(a.tokens * a.topk) + waves * tile, kPlanLds), stream, a, parts, tile);
 }
 
 // Experts that a chunk of tokens can name.
@@ -1153,7 +1200,8 @@ static void decode_up_wide(const DecodeArgs& a, hipStream_t stream) {
   typedef WideWalk<FMT, 2, TILES, WHOLE, kWideAhead<FMT>> Wk;
   hipLaunchKernelGGL((decode_up_wide_kernel<FMT, WHOLE, TILES>),
                      dim3((a.ffn / 16 + 3) / 4 + 1, decode_slots(a.tokens, a.topk, a.experts), chunks), dim3(256),
-                     (size_t)std::max(4 * kRowList + Wk::kShared + 4 * Wk::Wt::kLds, kPlanLds), stream, a);
+                     (size_t)std::max(4 * kRowList + Wk::kShared + 4 * Wk::Wt::kLds +
+                                          Entries::bytes(std::min(a.tokens, kDecodeTokenChunk) * a.topk), kPlanLds), stream, a);
 }
 
 template <int FMT, bool WHOLE>
@@ -1193,8 +1241,8 @@ static void decode_down_go(const DecodeArgs& a, hipStream_t stream) {
   if (few_each(a, 16))
     decode_down_wide<FMT, WHOLE, 6, 2>(a, stream);
   else
-    decode_down_wide<FMT, WHOLE, 8, 2>(a, stream);
-  hipLaunchKernelGGL(decode_sum_kernel, dim3((a.hidden / 4 + 255) / 256, a.tokens), dim3(256), 0, stream, a);
+    decode_down_wide<FMT, WHOLE, (FMT == WF_MXFP4 && !WHOLE) ? 6 : 8, 2>(a, stream);   // (8 would spill there)
+  hipLaunchKernelGGL(decode_sum_kernel, dim3((a.hidden / 4 + 63) / 64, a.tokens), dim3(256), 0, stream, a);
 }
 
 template <int FMT>
@@ -1214,13 +1262,18 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
 // tokens that can name up to 16 experts (each expert is a stretch of its own of
 // every wave there: 128 experts of 2048 x 768, 16 tokens: narrow 75 us for the
 // layer, wide 66 us; 8 experts of 4096 x 14336, 1 token: narrow 38 us, wide 47
-// us). About six workgroups a compute unit (4 resident at once, 64 tokens of 8
-// experts: 3 a unit 126 us, 6 a unit 100 us), at least 512 values of k each.
+// us), unless its hidden / 16 workgroups leave half the chip empty and have a
+// long way each (second product alone, 8 bf16 experts of 192 x 8960, 8 tokens:
+// narrow 58 us, wide and sum 14 us; 2048 x 5632, 4 tokens: narrow 27 us, 30 us;
+// two 4-bit ones of 1024 x 4096: narrow 6 us). About six workgroups a compute
+// unit (4 resident at once, 64 tokens of 8 experts: 3 a unit 126 us, 6 a unit 100
+// us), at least 512 values of k each, and no more than 16 planes to add (one 8-bit
+// expert of 2016 x 10432, 58 tokens: 8 splits 34 us, 16 28 us, 20 41 us).
 int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn) {
   const int64_t slots = decode_slots((int)tokens, topk, experts);
-  if (tokens <= 16 && slots <= 16 && tokens * topk <= 4 * slots) return 0;
+  if (tokens <= 16 && slots <= 16 && tokens * topk <= 4 * slots && (hidden >= 2048 || slots * ffn < 16384)) return 0;
   const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(8, ffn / 512), 1536 / (groups * slots)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, ffn / 512), 1536 / (groups * slots)));
 }
 
 hipError_t launch_decode(int fmt, const DecodeArgs& a, hipStream_t stream) {
