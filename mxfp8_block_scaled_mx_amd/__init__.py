@@ -10,6 +10,9 @@ Entry points mirror the C ABI: quantize (mx_quantize), grouped_gemm
 autograd Function over the fused forward/backward pair (GroupedLinear ->
 ScaledSwiGLU -> GroupedLinear with routing-weight scaling: "Efficient MoE
 training for biological foundation models", Key technical approaches item 3).
+For decoding steps: mx_gemv_fp4 / mx_gemv_nvfp4 (a few rows times 4-bit
+weights) and grouped_mlp_decode (the MoE MLP of a few tokens); for routers:
+mx_moe_route / mx_moe_route_bwd, and MoERoute, an autograd Function over them.
 """
 from __future__ import annotations
 
@@ -958,10 +961,18 @@ def _opt(who, name, t, shape, dtype, dev):
     return None if t is None else _need(who, name, t, shape, dtype, dev)
 
 
-def _scratch(who, workspace, nbytes, dev):
+def _new(shape, dtype, dev, stream):
+    """A new tensor that the call fills (or uses) on the given stream."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None and t.numel():
+        t.record_stream(stream)         # not handed out again before that stream's work is done
+    return t
+
+
+def _scratch(who, workspace, nbytes, dev, stream):
     """The caller's workspace, or a new one of nbytes (None where none is needed)."""
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        return _new((nbytes,), torch.uint8, dev, stream) if nbytes else None
     if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == dev
             and workspace.is_contiguous()):
         raise ValueError(f"{who}: workspace must be a contiguous uint8 tensor on {dev}")
@@ -1009,9 +1020,9 @@ def _gemv(who, fn, group, x, w_q, w_s, amax, out_dtype, out, workspace, stream):
         raise ValueError(f"{who}: the output is bfloat16 or float32")
     nbytes = gemv_workspace_bytes(m, n, k)
     if nbytes or workspace is not None:
-        workspace = _scratch(who, workspace, nbytes, dev)
+        workspace = _scratch(who, workspace, nbytes, dev, stream)
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        out = _new((m, n), out_dtype, dev, stream)
         y = out.data_ptr()
     else:
         y = _need(who, "out", out, (m, n), out_dtype, dev)
@@ -1078,9 +1089,9 @@ def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out
             _opt(who, "topk_w", topk_w, (T, k), torch.float32, dev), _need(who, "w1", w1, (E, 2 * F, H1), wt, dev), s1,
             _need(who, "w2", w2, (E, H, F1), wt, dev), s2)
     dims, nbytes = _decode_dims(E, T, H, F, k)
-    workspace = _scratch(who, workspace, nbytes, dev)
+    workspace = _scratch(who, workspace, nbytes, dev, stream)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _new((T, H), torch.bfloat16, dev, stream)
         y = out.data_ptr()
     else:
         y = _need(who, "out", out, (T, H), torch.bfloat16, dev)
@@ -1106,9 +1117,9 @@ def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=
     dev = logits.device
     b = _opt("mx_moe_route", "bias", bias, (E,), torch.float32, dev)
     k = topk if topk > 0 else 0
-    idx = torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = torch.empty((T, k), dtype=torch.float32, device=dev)
-    lse = torch.empty((T,), dtype=torch.float32, device=dev)
+    idx = _new((T, k), torch.int32, dev, stream)
+    w = _new((T, k), torch.float32, dev, stream)
+    lse = _new((T,), torch.float32, dev, stream)
     _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, b, T, E, topk, 1 if renormalize else 0,
           idx.data_ptr(), w.data_ptr(), lse.data_ptr())
     return idx, w, lse
@@ -1132,7 +1143,7 @@ def mx_moe_route_bwd(logits, topk_idx, topk_w, lse, dw, perm=None, bias=None, re
             _need(who, "topk_w", topk_w, (T, k), torch.float32, dev), _need(who, "lse", lse, (T,), torch.float32, dev),
             _need(who, "dw", dw, (T, k) if perm is None else dw.shape, torch.float32, dev), dw.numel(),
             _opt(who, "perm", perm, (T, k), torch.int32, dev))
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    dlogits = _new((T, E), logits.dtype, dev, stream)
     _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, *args, T, E, k, 1 if renormalize else 0,
           dlogits.data_ptr())
     return dlogits
@@ -1342,7 +1353,10 @@ class GroupedMLP(torch.autograd.Function):
 
 class MoERoute(torch.autograd.Function):
     """topk_idx, topk_w = MoERoute.apply(logits, topk, bias, renormalize): the
-    router's choice with the gradient of the weights for the logits."""
+    router's choice with the gradient of the weights for the logits (once: the
+    gradient has none of its own). A training step that is captured into a
+    graph calls mx_moe_route and mx_moe_route_bwd instead: a captured backward()
+    fails while an eager autograd graph of the same leaves lives."""
 
     @staticmethod
     def forward(ctx, logits, topk, bias=None, renormalize=True):
@@ -1354,6 +1368,7 @@ class MoERoute(torch.autograd.Function):
         return idx, w
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, _, dw):
         logits, bias, idx, w, lse = ctx.saved_tensors
         return mx_moe_route_bwd(logits, idx, w, lse, dw.contiguous(), bias=bias, renormalize=ctx.renormalize), None, None, None

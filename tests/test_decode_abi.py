@@ -34,6 +34,7 @@ def test_gemv_refusals(L):
         assert fp4(k=k) == nv(k=k) == ESHAPE
     assert fp4(m=-1) == fp4(n=-1) == fp4(ldx=56) == fp4(ldx=68) == fp4(ldx=-64) == ESHAPE
     assert fp4(m=65537) == fp4(n=(1 << 30) + 1) == fp4(k=(1 << 24) + 32, ldx=1 << 25) == EUNSUPPORTED
+    assert fp4(ldx=(1 << 24) + 8) == EUNSUPPORTED
     assert fp4(x=ODD) == fp4(w=ODD) == fp4(y=ODD) == nv(ws=ODD) == nv(am=ODD) == EALIGN
     assert b"mx_gemv_nvfp4" in L.mx_last_error()
     assert fp4(m=0) == fp4(n=0) == nv(m=0, x=None) == OK
@@ -61,6 +62,9 @@ def test_decode_refusals(L):
     assert size(H=48) == size(F=48) == size(H=0) == size(F=-32) == size(T=-1) == size(k=0) == ESHAPE
     assert size(T=513) == size(T=2 ** 40) == size(T=1, k=1025) == size(k=2 ** 31 - 1) == EUNSUPPORTED
     assert size(T=1024, k=1) == OK
+    assert size(T=1, k=64) == size(T=16, k=64) == OK and size(T=1, k=65) == EUNSUPPORTED
+    assert size(H=1 << 19) == size(F=1 << 19) == OK
+    assert size(H=(1 << 19) + 32) == size(F=(1 << 19) + 32) == size(F=1 << 62) == EUNSUPPORTED
     assert L.grouped_mlp_decode_sizes(None, 2, ctypes.byref(n)) == EINVAL
 
     def run(fmt=2, x=FAKE, idx=FAKE, wt=FAKE, w1=FAKE, s1=FAKE, w2=FAKE, s2=FAKE, y=FAKE, ws=FAKE, nb=need, T=3):

@@ -67,6 +67,48 @@ def test_against_the_definition(gpu_lib, fmt, T, k, E, H, F):
     assert torch.equal(again.view(torch.int16), y.view(torch.int16))
 
 
+# rows a multiple of 4096 bytes apart; many splits of a long ffn dimension; a
+# hidden dimension of a few tiles; the longest sums of planes
+WIDE = [("bf16", 20, 2, 3, 2048, 96), ("bf16", 20, 2, 3, 96, 2048), ("mxfp8", 33, 1, 2, 4096, 64),
+        ("mxfp8", 18, 2, 4, 64, 4096), ("mxfp4", 24, 3, 4, 8192, 32), ("mxfp4", 64, 2, 2, 32, 8192),
+        ("bf16", 8, 4, 8, 64, 2080), ("mxfp4", 1, 2, 9, 96, 8224), ("mxfp8", 20, 1, 1, 64, 8736),
+        ("mxfp4", 16, 8, 128, 160, 1056), ("mxfp8", 16, 8, 40, 2080, 96), ("mxfp4", 30, 34, 60, 32, 512)]
+
+
+@pytest.mark.parametrize("fmt,T,k,E,H,F", WIDE)
+def test_long_and_paged_rows(gpu_lib, fmt, T, k, E, H, F):
+    gen = torch.Generator().manual_seed(T + k + E + H + F)
+    rng = np.random.default_rng(T + E)
+    args, w1, w2 = _weights(gpu_lib, E, H, F, fmt, gen)
+    x = (0.25 * torch.randn((T, H), generator=gen)).to(torch.bfloat16).cuda()
+    idx = _choices(rng, T, k, E)
+    idx[rng.uniform(size=idx.shape) < 0.1] = -1
+    _check(gpu_lib, x, idx, rng.uniform(0, 1, size=(T, k)).astype(np.float32), args, w1, w2)
+
+
+def test_workspace_of_a_call_on_another_stream(gpu_lib):
+    """The call's own workspace is not handed out again before the stream that
+    it was given has run the call."""
+    gen = torch.Generator().manual_seed(21)
+    E, H, F, T, k = 8, 512, 1024, 64, 2
+    args, _, _ = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    idx = torch.from_numpy(_choices(np.random.default_rng(1), T, k, E)).cuda()
+    want = gpu_lib.grouped_mlp_decode(x, idx, None, *args)
+    out = torch.empty_like(want)
+    nbytes = gpu_lib.mlp_decode_workspace_bytes(E, T, H, F, k)
+    big = torch.randn((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            big = torch.mm(big, big).clamp_(-1, 1)
+    gpu_lib.grouped_mlp_decode(x, idx, None, *args, out=out, stream=side)
+    later = [torch.zeros(nbytes, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    side.synchronize()
+    assert torch.equal(out, want) and all(not t.any() for t in later)
+
+
 @pytest.mark.parametrize("T", [2, 37])
 def test_dropped_repeated_and_unweighted_choices(gpu_lib, T):
     gen = torch.Generator().manual_seed(5)

@@ -65,6 +65,22 @@ def test_nvfp4_integers_are_exact(gpu_lib, m, n, k):
         assert torch.equal(out.cpu(), torch.from_numpy(want).to(torch.float32).to(dt))
 
 
+@pytest.mark.parametrize("m,n,k", [(17, 70, 8192), (64, 200, 8192), (100, 65, 8192), (16, 50, 8192)])
+def test_rows_a_page_apart(gpu_lib, m, n, k):
+    """Code rows a multiple of 4096 bytes apart, where workgroups begin at
+    places of their own. Integer rows of at most 4: the products are multiples
+    of 1/16 of at most 96, so sums below 8192 * 96 < 2^20 are exact."""
+    rng = np.random.default_rng(m + n)
+    x = _ints(rng, (m, k), 4)
+    q = rng.integers(0, 256, size=(n, k // 2), dtype=np.uint8)
+    s4 = rng.integers(126, 130, size=(n, k // 32), dtype=np.uint8)
+    sn = rng.integers(0x38, 0x48, size=(n, k // 16), dtype=np.uint8)
+    got = gpu_lib.mx_gemv_fp4(_bf16(x), _u8(q), _u8(s4), out_dtype=torch.float32)
+    assert np.array_equal(ref.f64(got), x @ ref.mxfp4(q, s4).T)
+    got = gpu_lib.mx_gemv_nvfp4(_bf16(x), _u8(q), _u8(sn), torch.tensor([2688.0], device="cuda"), out_dtype=torch.float32)
+    assert np.array_equal(ref.f64(got), x @ ref.nvfp4(q, sn, 2688.0).T)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 @pytest.mark.parametrize("m,n,k", [(1, 384, 4096), (5, 200, 1568), (40, 96, 2048)])
 def test_quantized_weights_within_the_summation_bound(gpu_lib, fmt, m, n, k):

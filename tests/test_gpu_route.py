@@ -179,6 +179,15 @@ def test_autograd_function(gpu_lib):
         assert torch.equal(z.grad, gpu_lib.mx_moe_route_bwd(z.detach(), i0, w0, l0, c, bias=bias, renormalize=renorm))
 
 
+def test_autograd_function_refuses_a_second_derivative(gpu_lib):
+    z, _ = _inputs(5, 8, torch.float32, 10, masked=False)
+    z.requires_grad_()
+    _, w = gpu_lib.MoERoute.apply(z, 2)
+    (g,) = torch.autograd.grad((w * w).sum(), z, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
 def test_training_chain(gpu_lib):
     """route -> dispatch -> fused MLP forward and backward -> dprobs -> the
     router's gradient, with tokens that have one open expert, or none."""
