@@ -566,9 +566,10 @@ static bool whole_steps(int64_t k, const uint8_t* scales) {
          (kScaleBytes<FMT> == 0 || (k / 32 * kScaleBytes<FMT> % 16 == 0 && reinterpret_cast<uintptr_t>(scales) % 16 == 0));
 }
 
-constexpr int kGemvWideTiles = 1;
-// Waves a launch splits k for: 16 per compute unit, all resident at once.
-constexpr int64_t kWavesWanted = 4096;
+// Waves a launch splits k for: 8 per compute unit, all resident at once (one
+// row, 28672 x 4096 and 14336 x 4096, 4-bit: 8 a unit 12.6 and 8.9 us, 16 a unit
+// 13.2 and 9.1 us, 32 a unit 13.0 and 10.3 us).
+constexpr int64_t kWavesWanted = 2048;
 
 template <int FMT, int NT, int R, int D>
 static void gemv_go(const GemvArgs& a, hipStream_t stream) {
@@ -586,7 +587,7 @@ static void gemv_go(const GemvArgs& a, hipStream_t stream) {
 
 template <int FMT, int MT>
 static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
-  constexpr int NT = kGemvWideTiles, D = 1;
+  constexpr int NT = 1, D = 1;
   const dim3 grid((unsigned)((a.n + 64 * NT - 1) / (64 * NT)), (unsigned)((a.m + 16 * MT - 1) / (16 * MT)), a.splits);
   typedef WideWalk<FMT, NT, MT, true, D> Wk;
   const size_t lds = Wk::kShared + 4 * Wk::Wt::kLds;
@@ -599,6 +600,14 @@ static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
                        stream, a);
 }
 
+// Which form runs. Two tiles of weight rows a wave halve the work on the
+// activations, one tile gives twice the teams. For up to 4 rows two pay once one
+// tile a wave already fills the chip (4-bit, one row, one tile two steps ahead
+// against two tiles one step ahead: 4096 x 14336 8.7 and 11.6 us, 28672 x 4096
+// 14.2 and 13.2 us); for up to 16 rows, where an activation tile is four times the
+// loads, earlier (one tile, two: 4096 x 14336 14.0 and 16.4 us, 8192 x 4096 9.0 and
+// 7.8 us, 28672 x 4096 24.8 and 20.4 us). The wide form takes 32 rows at a time or
+// 64 (32 rows, 28672 x 4096: 21.2 us, 35.0 us).
 template <int FMT>
 static void gemv_format(const GemvArgs& a, hipStream_t stream) {
   if (a.m <= 4) {
@@ -623,7 +632,7 @@ static void gemv_format(const GemvArgs& a, hipStream_t stream) {
 // 4096: 2 splits 24.2 us, 3 26.7 us; 64 x 28672 x 4096: 1 split 31.7 us.)
 int gemv_splits(int64_t m, int64_t n, int64_t k) {
   if (m <= 16) return 0;
-  const int64_t groups = (n + 64 * kGemvWideTiles - 1) / (64 * kGemvWideTiles) * ((m + 63) / 64);
+  const int64_t groups = (n + 63) / 64 * ((m + 63) / 64);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, k / 512), 512 / groups));
 }
 
@@ -753,13 +762,13 @@ __device__ void write_plan(const DecodeArgs& a, int chunk, uint8_t* smem) {
 }
 constexpr int kPlanLds = 8 * kMaxGroups + 2 * kDecodeMaxEntries;
 
-// Steps that the weights are loaded ahead: about 4 KiB of a wave in flight.
+// Steps that the second product's weights are loaded ahead: 4 KiB of a wave in
+// flight, as the first product has them from one step of its two tiles (two
+// steps there: one 4-bit token of 8 experts, 4096 x 14336, 25.1 us, one 23.1 us; here,
+// one step and two: 14.1 and 13.5 us, 8-bit with 7 tokens 85 and 75 us, bf16 no
+// difference).
 template <int FMT>
-constexpr int kUpAhead = 1;
-template <int FMT>
-constexpr int kDownAhead = (FMT == WF_BF16 ? 1 : 2);
-template <int FMT>
-constexpr int kWideAhead = FMT == WF_BF16 ? 1 : 1;
+constexpr int kDownAhead = FMT == WF_BF16 ? 1 : 2;
 
 constexpr int kRowList = kDecodeTokenChunk * 8;           // a wave's list of rows: entry and weight
 
@@ -834,7 +843,6 @@ typedef std::integral_constant<int, 1> One;
 typedef std::integral_constant<int, 2> Two;
 typedef std::integral_constant<int, 3> Three;
 typedef std::integral_constant<int, 4> Four;
-typedef std::integral_constant<int, 8> Eight;
 typedef std::integral_constant<int, 16> Sixteen;
 
 // A = w silu(g) u of every entry, [g | u] = W1_e x_t, for at most ROWS (4 or
@@ -864,7 +872,7 @@ __global__ __launch_bounds__(512, 2) void decode_up_kernel(DecodeArgs a, int par
   const int s0 = part_start<FMT>(nb, part, parts), s1 = part_start<FMT>(nb, part + 1, parts);
   auto go = [&](auto r_) __attribute__((always_inline)) {
     constexpr int R = decltype(r_)::value;
-    typedef Walk<FMT, 2, R, WHOLE, kUpAhead<FMT>> Wk;
+    typedef Walk<FMT, 2, R, WHOLE, 1> Wk;
     Wk k;
     k.nb = nb;
     const int64_t first[2] = {(int64_t)rows.expert * 2 * a.ffn + f0, (int64_t)rows.expert * 2 * a.ffn + a.ffn + f0};
@@ -919,14 +927,14 @@ __global__ __launch_bounds__(256, 2) void decode_up_wide_kernel(DecodeArgs a) {
   }
   Entries en(a, chunk);
   uint8_t* const tiles_at = smem + 4 * kRowList;
-  en.stage(a, chunk, tiles_at + 2 * TILES * 4096 + 4 * Weights<FMT, 2, WHOLE, kWideAhead<FMT>>::kLds);
+  en.stage(a, chunk, tiles_at + 2 * TILES * 4096 + 4 * Weights<FMT, 2, WHOLE, 1>::kLds);
   const ExpertRows rows(en, slot, smem + wave * kRowList);
   if (rows.expert < 0) return;
   const int tile = (int)blockIdx.x * 4 + wave, tiles = a.ffn / 16, f0 = min(tile, tiles - 1) * 16;
   const int nb = a.hidden / 32;
   auto go = [&](auto mt_, int c0) __attribute__((always_inline)) {
     constexpr int MT = decltype(mt_)::value;
-    typedef WideWalk<FMT, 2, MT, WHOLE, kWideAhead<FMT>> Wk;
+    typedef WideWalk<FMT, 2, MT, WHOLE, 1> Wk;
     Wk k;
     k.nb = nb;
     const int64_t first[2] = {(int64_t)rows.expert * 2 * a.ffn + f0, (int64_t)rows.expert * 2 * a.ffn + a.ffn + f0};
@@ -992,14 +1000,14 @@ struct Stretch {
   }
 };
 
-// y[t] = sum over the token's entries of W2_e . A, for at most ROWS (2 or 16)
+// y[t] = sum over the token's entries of W2_e . A, for at most 16
 // tokens. A workgroup owns 16 values of h; the k-steps of all named experts,
 // one after the other, are split evenly over its waves. A tile's activation
 // rows are up to 8 (2) entries' leading parts and the same entries' second
 // parts, whose results are added. Each wave adds its results to a slice of its
 // own in LDS (a token appears once among an expert's entries), and the slices
 // are added in wave order, so the sum has one order whatever the timing.
-template <int FMT, bool WHOLE, int ROWS>
+template <int FMT, bool WHOLE>
 __global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, int tile_bytes) {
   extern __shared__ __align__(16) uint8_t smem[];         // [waves][tokens][16] sums, then the waves' tiles
   __shared__ DecodePlan plan;
@@ -1046,7 +1054,7 @@ __global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, in
         if (row < rows) mine[plan.list[row0 + row] / a.topk * 16 + (lane & 15)] += v;
       }
     };
-    if (ROWS <= 2 || rows <= 2)
+    if (rows <= 2)
       go(Four{}, 0);
     else
       for (int c0 = 0; c0 < rows; c0 += 8) go(Sixteen{}, c0);
@@ -1062,8 +1070,12 @@ __global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, in
 // The same for more tokens: a workgroup owns 64 * NT values of h of one expert,
 // for the expert's entries among a chunk of tokens, and split blockIdx.y of the
 // ffn dimension. Its sums go to the split's plane of a.sums, a row an entry,
-// which the next kernel adds. TILES: most row tiles (8 entries each) of a pass.
-template <int FMT, bool WHOLE, int TILES, int NT>
+// which the next kernel adds. A pass takes up to six row tiles of 8 entries
+// each: eight would let fewer workgroups share a compute unit's LDS (4-bit, 64
+// tokens of 8 experts, 4096 x 14336: four tiles 93 us, six 87 us, eight 127 us; of 2 experts, 2048
+// x 8192: six 29 us, eight 39 us; 8-bit, 60 tokens, 4 choices: 179, 158 and 178 us).
+constexpr int kDownTiles = 6;
+template <int FMT, bool WHOLE, int NT>
 __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];         // the shared tiles, the waves' tiles
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1094,7 +1106,7 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
     }
     v4f acc[NT][MT];
     clear(acc);
-    k.run_around(smem, smem + 2 * TILES * Wk::kXTile + wave * Wk::Wt::kLds, part_start<FMT>(nb, split, a.splits),
+    k.run_around(smem, smem + 2 * kDownTiles * Wk::kXTile + wave * Wk::Wt::kLds, part_start<FMT>(nb, split, a.splits),
                  part_start<FMT>(nb, split + 1, a.splits), blockIdx.x, acc);
 #pragma unroll
     for (int t = 0; t < MT; ++t)
@@ -1111,7 +1123,7 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
         }
       }
   };
-  for (int c0 = 0; c0 < rows; c0 += 8 * TILES) {
+  for (int c0 = 0; c0 < rows; c0 += 8 * kDownTiles) {
     if (rows - c0 <= 8)
       go(One{}, c0);
     else if (rows - c0 <= 16)
@@ -1121,7 +1133,7 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
     else if (rows - c0 <= 32)
       go(Four{}, c0);
     else
-      go(std::integral_constant<int, TILES>{}, c0);
+      go(std::integral_constant<int, kDownTiles>{}, c0);
   }
 }
 
@@ -1179,7 +1191,7 @@ static void decode_up_rows(const DecodeArgs& a, hipStream_t stream) {
   // tokens, 2048 x 768, 4-bit: 4 units in 4 parts 23.0 us, in 2 parts 20.5 us).
   int parts = 1;
   while (parts < 4 && parts * 2 <= units && (parts * 4 <= units || (int64_t)tiles * slots * parts <= 1024)) parts *= 2;
-  constexpr int tile = kRowList + std::max(Walk<FMT, 2, ROWS, WHOLE, kUpAhead<FMT>>::kLds, 2048);
+  constexpr int tile = kRowList + std::max(Walk<FMT, 2, ROWS, WHOLE, 1>::kLds, 2048);
   const int waves = std::max(4, parts), teams = waves / parts;
   hipLaunchKernelGGL((decode_up_kernel<FMT, WHOLE, ROWS>), dim3((tiles + teams - 1) / teams + 1, slots), dim3(64 * waves),
                      (size_t)std::max(Entries::bytes(a.tokens * a.topk) + waves * tile, kPlanLds), stream, a, parts, tile);
@@ -1197,7 +1209,7 @@ static bool few_each(const DecodeArgs& a, int rows) {
 template <int FMT, bool WHOLE, int TILES>
 static void decode_up_wide(const DecodeArgs& a, hipStream_t stream) {
   const int chunks = (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk;
-  typedef WideWalk<FMT, 2, TILES, WHOLE, kWideAhead<FMT>> Wk;
+  typedef WideWalk<FMT, 2, TILES, WHOLE, 1> Wk;
   hipLaunchKernelGGL((decode_up_wide_kernel<FMT, WHOLE, TILES>),
                      dim3((a.ffn / 16 + 3) / 4 + 1, decode_slots(a.tokens, a.topk, a.experts), chunks), dim3(256),
                      (size_t)std::max(4 * kRowList + Wk::kShared + 4 * Wk::Wt::kLds +
@@ -1206,42 +1218,47 @@ static void decode_up_wide(const DecodeArgs& a, hipStream_t stream) {
 
 template <int FMT, bool WHOLE>
 static void decode_up_go(const DecodeArgs& a, hipStream_t stream) {
+  // Four activation rows a tile instead of 16 (one 4-bit token of 8 experts, 4096
+  // x 14336: 23.1 us, 24.2 us).
   if (a.tokens <= 4)
     decode_up_rows<FMT, WHOLE, 4>(a, stream);
   else if (a.tokens <= 16)
     decode_up_rows<FMT, WHOLE, 16>(a, stream);
+  // Most row tiles of a pass: fewer leave LDS for more workgroups (4-bit, 61 tokens, 5
+  // choices among 60 experts of 544 x 4288: two 61 us, three 73 us), but a pass
+  // more reads the weights again (64 tokens of 8 experts, 4096 x 14336, 16 entries
+  // an expert: two 112 us, three 103 us, four 113 us; 8-bit, 4 choices: three 218
+  // us, four 201 us).
+  else if (few_each(a, 8))
+    decode_up_wide<FMT, WHOLE, 2>(a, stream);
   else if (few_each(a, 16))
     decode_up_wide<FMT, WHOLE, 3>(a, stream);
   else
     decode_up_wide<FMT, WHOLE, 4>(a, stream);
 }
 
-template <int FMT, bool WHOLE, int ROWS>
+template <int FMT, bool WHOLE>
 static void decode_down_rows(const DecodeArgs& a, hipStream_t stream) {
-  constexpr int waves = 8, tile = Walk<FMT, 1, ROWS <= 2 ? 4 : 16, WHOLE, kDownAhead<FMT>>::kLds;
-  hipLaunchKernelGGL((decode_down_kernel<FMT, WHOLE, ROWS>), dim3(a.hidden / 16), dim3(64 * waves),
+  constexpr int waves = 8, tile = Walk<FMT, 1, 16, WHOLE, kDownAhead<FMT>>::kLds;
+  hipLaunchKernelGGL((decode_down_kernel<FMT, WHOLE>), dim3(a.hidden / 16), dim3(64 * waves),
                      (size_t)waves * (a.tokens * 64 + tile), stream, a, tile);
 }
 
-template <int FMT, bool WHOLE, int TILES, int NT>
+template <int FMT, bool WHOLE>
 static void decode_down_wide(DecodeArgs a, hipStream_t stream) {
+  constexpr int NT = 2;
   const int chunks = (a.tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk;
-  typedef WideWalk<FMT, NT, TILES, WHOLE, 1> Wk;
+  typedef WideWalk<FMT, NT, kDownTiles, WHOLE, 1> Wk;
   a.slots = decode_slots(a.tokens, a.topk, a.experts);
-  hipLaunchKernelGGL((decode_down_wide_kernel<FMT, WHOLE, TILES, NT>),
+  hipLaunchKernelGGL((decode_down_wide_kernel<FMT, WHOLE, NT>),
                      dim3((a.hidden + 64 * NT - 1) / (64 * NT), a.slots * a.splits, chunks), dim3(256),
                      (size_t)(Wk::kShared + 4 * Wk::Wt::kLds), stream, a);
 }
 
 template <int FMT, bool WHOLE>
 static void decode_down_go(const DecodeArgs& a, hipStream_t stream) {
-  if (a.splits == 0 && a.tokens <= 2) return decode_down_rows<FMT, WHOLE, 2>(a, stream);
-  if (a.splits == 0) return decode_down_rows<FMT, WHOLE, 16>(a, stream);
-  // three row tiles hold the 24 entries that few experts pass where 16 are the mean
-  if (few_each(a, 16))
-    decode_down_wide<FMT, WHOLE, 6, 2>(a, stream);
-  else
-    decode_down_wide<FMT, WHOLE, (FMT == WF_MXFP4 && !WHOLE) ? 6 : 8, 2>(a, stream);   // (8 would spill there)
+  if (a.splits == 0) return decode_down_rows<FMT, WHOLE>(a, stream);
+  decode_down_wide<FMT, WHOLE>(a, stream);
   hipLaunchKernelGGL(decode_sum_kernel, dim3((a.hidden / 4 + 63) / 64, a.tokens), dim3(256), 0, stream, a);
 }
 
