@@ -727,8 +727,8 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
  * Rows of x do not mix: an infinity or NaN in one row stays in that row. Sums
  * have one order for a given shape, so results repeat bit for bit. m or n zero
  * is a no-op. Errors: MX_EINVAL (null pointers, y_dtype), MX_ESHAPE (negative
- * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EWORKSPACE, MX_EUNSUPPORTED
- * (m > 65536, n > 2^30, k or ldx > 2^24), MX_EHIP.
+ * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EWORKSPACE,
+ * MX_EUNSUPPORTED (m > 65536, n > 2^30, k or ldx > 2^24), MX_EHIP.
  */
 MX_API mx_status mx_gemv_sizes(int64_t m, int64_t n, int64_t k, size_t* workspace);
 MX_API mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
@@ -803,8 +803,10 @@ MX_API mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_we
  *            dprobs of grouped_mlp_bwd): dw[t, j] is then dw[perm[t, j]], and 0
  *            where perm lies outside [0, dw_rows). dw_rows is the number of
  *            elements of dw in both cases.
- *   topk_idx, topk_w, lse   from the forward (lse is read with renormalize 0
- *            only, and may be NULL otherwise).
+ *   topk_idx, topk_w, lse   from the forward, whose experts of one token are
+ *            distinct (of equal ones one is taken as chosen); one outside [0,
+ *            num_experts) is skipped. lse is read with renormalize 0 only, and
+ *            may be NULL otherwise.
  *   dlogits  [tokens, num_experts] of logits_dtype, all of it written; logits
  *            may be NULL with renormalize 1.
  * Both: tokens == 0 is a no-op. Errors: MX_EINVAL (null pointers, dtype),

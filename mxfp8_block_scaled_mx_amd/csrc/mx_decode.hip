@@ -13,6 +13,23 @@
 // expanded exactly to bf16 in registers (an E2M1 or E4M3 element times a power
 // of two, or E2M1 times E4M3, has at most 6 significant bits), and products
 // are summed in fp32 by the 16 x 16 x 32 bf16 MFMA.
+//
+// All of it is bound by reading the weights: a byte of 4-bit codes meets 4
+// operations per row, far below what the MFMA needs to be busy. So a kernel is
+// a way to keep enough whole cache lines of weights on their way: 32 to 64 KiB a
+// compute unit, since a line takes 2 to 3 us when the memory is busy (reading
+// alone reaches 6.9 TB/s on this layout of loads). What the forms reach (weight
+// bytes over time, the calls' other reads not counted):
+//   gemv_kernel       4-bit, 28672 x 4096:  1 row 12.6 us, 5.0 TB/s; 16 rows
+//                     18 to 20 us, 3.3 TB/s (activation tiles pass LDS too);
+//                     1 row, 4096 x 14336: 8.7 us, 3.6 TB/s (3 us are the launch)
+//   gemv_wide_kernel  32 rows 21.2 us, 2.9 TB/s
+//   decode_up_kernel  8 experts of 4096 x 14336, 2 choices: 1 token, 4-bit, 23 us,
+//                     5.4 TB/s; 7 tokens, 8-bit, 135 us, 6.2 TB/s
+//   decode_down_kernel   the same: 13.8 us, 4.5 TB/s; 76 us, 5.5 TB/s
+//   decode_up_wide_kernel, decode_down_wide_kernel   64 tokens, 4-bit: 103 us, 4.8
+//                     TB/s; 89 us, 2.8 TB/s (its activations are twice 16 bits
+//                     of every value, and as many bytes as the weights by way of L2)
 #include <stddef.h>
 
 #include <algorithm>
@@ -540,7 +557,8 @@ __global__ __launch_bounds__(256, 2) void gemv_wide_kernel(GemvArgs a) {
       }
 }
 
-// y = the splits' sums, added in order.
+// y = the splits' sums, added in order (4 us at 57 x 1740, 16 splits, of which 3
+// are the launch).
 template <int FMT>
 __global__ __launch_bounds__(256) void gemv_sum_kernel(GemvArgs a) {
   const int64_t n = a.m * a.n;
@@ -1140,7 +1158,8 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
 // y[t] = the sums of the token's entries and splits; 4 values a thread. The
 // planes of a token (its entries in order, each with its splits) go round the
 // four waves, whose sums are added in wave order. The rows of entries that are
-// in no list were not written.
+// in no list were not written. Bound by the latency of its loads: four in flight
+// of each wave (64 planes of 8 x 192 values: one at a time 8.2 us, four 4.7 us).
 __global__ __launch_bounds__(256) void decode_sum_kernel(DecodeArgs a) {
   __shared__ v4f part[3][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
