@@ -20,10 +20,13 @@
 // compute unit, since a line takes 2 to 3 us when the memory is busy (reading
 // alone reaches 6.9 TB/s on this layout of loads). What the forms reach (weight
 // bytes over time, the calls' other reads not counted):
-//   gemv_kernel       4-bit, 28672 x 4096:  1 row 12.6 us, 5.0 TB/s; 16 rows
-//                     18 to 20 us, 3.3 TB/s (activation tiles pass LDS too);
-//                     1 row, 4096 x 14336: 8.7 us, 3.6 TB/s (3 us are the launch)
-//   gemv_wide_kernel  32 rows 21.2 us, 2.9 TB/s
+//   gemv_kernel       4-bit, 1 row: 28672 x 4096 12.6 us, 5.0 TB/s; 4096 x
+//                     14336 8.6 us, 3.6 TB/s (3 us are the launch); NVFP4, 5
+//                     rows, 14336 x 4096: 11.4 us, 2.9 TB/s (its expansion takes
+//                     twice the instructions)
+//   gemv_wide_kernel  4-bit, 28672 x 4096: 16 rows 17.1 us, 3.6 TB/s; 32 rows 21.2
+//                     us, 2.9 TB/s (the activations take the same path through
+//                     the load unit and LDS as the weights)
 //   decode_up_kernel  8 experts of 4096 x 14336, 2 choices: 1 token, 4-bit, 23 us,
 //                     5.4 TB/s; 7 tokens, 8-bit, 135 us, 6.2 TB/s
 //   decode_down_kernel   the same: 13.8 us, 4.5 TB/s; 76 us, 5.5 TB/s
@@ -624,20 +627,22 @@ static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
 // against two tiles one step ahead: 4096 x 14336 8.7 and 11.6 us, 28672 x 4096
 // 14.2 and 13.2 us); for up to 16 rows, where an activation tile is four times the
 // loads, earlier (one tile, two: 4096 x 14336 14.0 and 16.4 us, 8192 x 4096 9.0 and
-// 7.8 us, 28672 x 4096 24.8 and 20.4 us). The wide form takes 32 rows at a time or
-// 64 (32 rows, 28672 x 4096: 21.2 us, 35.0 us).
+// 7.8 us, 28672 x 4096 24.8 and 20.4 us). The wide form takes 16, 32 or 64 rows at a
+// time (32 rows, 28672 x 4096: 21.2 us as 32, 35.0 us as 64).
 template <int FMT>
 static void gemv_format(const GemvArgs& a, hipStream_t stream) {
-  if (a.m <= 4) {
+  if (a.splits == 0 && a.m <= 4) {
     if (a.n >= 16384)
       gemv_go<FMT, 2, 4, 1>(a, stream);
     else
       gemv_go<FMT, 1, 4, 2>(a, stream);
-  } else if (a.m <= 16) {
+  } else if (a.splits == 0) {
     if (a.n >= 8192)
       gemv_go<FMT, 2, 16, 1>(a, stream);
     else
       gemv_go<FMT, 1, 16, 1>(a, stream);
+  } else if (a.m <= 16) {
+    gemv_wide_go<FMT, 1>(a, stream);
   } else if (a.m <= 32) {
     gemv_wide_go<FMT, 2>(a, stream);
   } else {
@@ -647,9 +652,13 @@ static void gemv_format(const GemvArgs& a, hipStream_t stream) {
 
 // Splits of k of the wide product (0: the narrow one runs): up to 512
 // workgroups, 2 a compute unit, of at least 512 values of k each. (64 x 14336 x
-// 4096: 2 splits 24.2 us, 3 26.7 us; 64 x 28672 x 4096: 1 split 31.7 us.)
+// 4096: 2 splits 24.2 us, 3 26.7 us; 64 x 28672 x 4096: 1 split 31.7 us.) For
+// more than 8 rows it also runs, unsplit, where its workgroups go round the chip
+// at least once: the narrow form's waves load the activations each for itself (16
+// rows, narrow and wide: 28672 x 4096 18.7 and 16.9 us, 20000 x 8192 33.5 and 30.8
+// us, 16384 x 4096 12.5 and 13.7 us; 8 rows, 20000 x 8192: 28.3 and 30.1 us).
 int gemv_splits(int64_t m, int64_t n, int64_t k) {
-  if (m <= 16) return 0;
+  if (m <= 8 || (m <= 16 && n < 18432)) return 0;
   const int64_t groups = (n + 63) / 64 * ((m + 63) / 64);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, k / 512), 512 / groups));
 }

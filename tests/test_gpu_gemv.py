@@ -65,10 +65,11 @@ def test_nvfp4_integers_are_exact(gpu_lib, m, n, k):
         assert torch.equal(out.cpu(), torch.from_numpy(want).to(torch.float32).to(dt))
 
 
-@pytest.mark.parametrize("m,n,k", [(17, 70, 8192), (64, 200, 8192), (100, 65, 8192), (16, 50, 8192)])
+@pytest.mark.parametrize("m,n,k", [(17, 70, 8192), (64, 200, 8192), (100, 65, 8192), (16, 50, 8192), (9, 18433, 288),
+                                   (16, 18432, 512), (13, 20011, 8192), (8, 18500, 96)])
 def test_rows_a_page_apart(gpu_lib, m, n, k):
     """Code rows a multiple of 4096 bytes apart, where workgroups begin at
-    places of their own. Integer rows of at most 4: the products are multiples
+    places of their own, and many weight rows. Integer rows of at most 4: the products are multiples
     of 1/16 of at most 96, so sums below 8192 * 96 < 2^20 are exact."""
     rng = np.random.default_rng(m + n)
     x = _ints(rng, (m, k), 4)
