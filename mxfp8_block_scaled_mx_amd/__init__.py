@@ -961,11 +961,18 @@ def _opt(who, name, t, shape, dtype, dev):
     return None if t is None else _need(who, name, t, shape, dtype, dev)
 
 
+def _on_device(stream, dev):
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+
+
 def _new(shape, dtype, dev, stream):
     """A new tensor that the call fills (or uses) on the given stream."""
     t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None and t.numel():
-        t.record_stream(stream)         # not handed out again before that stream's work is done
+    if stream is not None:
+        _on_device(stream, dev)
+        if t.numel():
+            t.record_stream(stream)     # not handed out again before that stream's work is done
     return t
 
 
@@ -983,6 +990,8 @@ def _call(fn, dev, stream, *args):
     """fn(*args, stream) with the tensors' device current: on its current
     stream, or the given one."""
     index = dev.index
+    if stream is not None:
+        _on_device(stream, dev)
     if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream)
     else:

@@ -86,6 +86,39 @@ def test_long_and_paged_rows(gpu_lib, fmt, T, k, E, H, F):
     _check(gpu_lib, x, idx, rng.uniform(0, 1, size=(T, k)).astype(np.float32), args, w1, w2)
 
 
+def test_two_calls_at_once(gpu_lib):
+    """Calls on two streams, each with what it allocates itself, interleaved."""
+    gen = torch.Generator().manual_seed(22)
+    sizes = [(6, 256, 512, 40, 2), (4, 512, 288, 9, 1)]
+    calls, wants = [], []
+    for E, H, F, T, k in sizes:
+        args, _, _ = _weights(gpu_lib, E, H, F, "mxfp8", gen)
+        x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+        idx = torch.from_numpy(_choices(np.random.default_rng(T), T, k, E)).cuda()
+        calls.append((x, idx, None, *args))
+        wants.append(gpu_lib.grouped_mlp_decode(*calls[-1]))
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    got = [[gpu_lib.grouped_mlp_decode(*c, stream=s) for c, s in zip(calls, streams)] for _ in range(8)]
+    torch.cuda.synchronize()
+    for pair in got:
+        assert all(torch.equal(a, b) for a, b in zip(pair, wants))
+
+
+def test_a_stream_of_another_device_is_refused(gpu_lib):
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    gen = torch.Generator().manual_seed(23)
+    args, _, _ = _weights(gpu_lib, 2, 32, 32, "bf16", gen)
+    x, idx = torch.zeros((1, 32), dtype=torch.bfloat16, device="cuda"), torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    z = torch.zeros((2, 8), device="cuda")
+    for call in (lambda: gpu_lib.grouped_mlp_decode(x, idx, None, *args, stream=Elsewhere()),
+                 lambda: gpu_lib.mx_moe_route(z, 2, stream=Elsewhere())):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_workspace_of_a_call_on_another_stream(gpu_lib):
     """The call's own workspace is not handed out again before the stream that
     it was given has run the call."""
