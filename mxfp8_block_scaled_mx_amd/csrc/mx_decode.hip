@@ -22,7 +22,7 @@
 // bytes over time, the calls' other reads not counted):
 //   gemv_kernel       4-bit, 1 row: 28672 x 4096 12.6 us, 5.0 TB/s; 4096 x
 //                     14336 8.6 us, 3.6 TB/s (3 us are the launch); NVFP4, 5
-//                     rows, 14336 x 4096: 11.4 us, 2.9 TB/s (its expansion takes
+//                     rows, 14336 x 4096: 11.5 us, 2.9 TB/s (its expansion takes
 //                     twice the instructions)
 //   gemv_wide_kernel  4-bit, 28672 x 4096: 16 rows 17.1 us, 3.6 TB/s; 32 rows 21.2
 //                     us, 2.9 TB/s (the activations take the same path through
@@ -268,7 +268,7 @@ struct Weights {
 };
 
 // One wave's part of the products of NT tiles of 16 weight rows with R
-// activation rows (16, or 4 repeated over the MFMA's 16) over the k-steps
+// activation rows (16, or 4 or 8 repeated over the MFMA's 16) over the k-steps
 // [s0, s1). Result: acc[n][0] register r of lane l = activation row
 // (l / 16) * 4 + r, weight row l % 16. The activations go the weights' way.
 // Loads complete in the order of their issue as far as a wave can tell, so both
@@ -627,7 +627,9 @@ static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
 // against two tiles one step ahead: 4096 x 14336 8.7 and 11.6 us, 28672 x 4096
 // 14.2 and 13.2 us); for up to 16 rows, where an activation tile is four times the
 // loads, earlier (one tile, two: 4096 x 14336 14.0 and 16.4 us, 8192 x 4096 9.0 and
-// 7.8 us, 28672 x 4096 24.8 and 20.4 us). The wide form takes 16, 32 or 64 rows at a
+// 7.8 us, 28672 x 4096 24.8 and 20.4 us). Tiles of 8 activation rows save half of
+// those loads (8 rows, tiles of 16 and of 8: 28672 x 4096 15.9 and 14.7 us, 4096 x
+// 14336 12.4 and 11.7 us; 6 rows, 20000 x 8192 27.3 and 24.3 us). The wide form takes 16, 32 or 64 rows at a
 // time (32 rows, 28672 x 4096: 21.2 us as 32, 35.0 us as 64).
 template <int FMT>
 static void gemv_format(const GemvArgs& a, hipStream_t stream) {
@@ -636,6 +638,11 @@ static void gemv_format(const GemvArgs& a, hipStream_t stream) {
       gemv_go<FMT, 2, 4, 1>(a, stream);
     else
       gemv_go<FMT, 1, 4, 2>(a, stream);
+  } else if (a.splits == 0 && a.m <= 8) {
+    if (a.n >= 8192)
+      gemv_go<FMT, 2, 8, 1>(a, stream);
+    else
+      gemv_go<FMT, 1, 8, 1>(a, stream);
   } else if (a.splits == 0) {
     if (a.n >= 8192)
       gemv_go<FMT, 2, 16, 1>(a, stream);
@@ -656,7 +663,7 @@ static void gemv_format(const GemvArgs& a, hipStream_t stream) {
 // more than 8 rows it also runs, unsplit, where its workgroups go round the chip
 // at least once: the narrow form's waves load the activations each for itself (16
 // rows, narrow and wide: 28672 x 4096 18.7 and 16.9 us, 20000 x 8192 33.5 and 30.8
-// us, 16384 x 4096 12.5 and 13.7 us; 8 rows, 20000 x 8192: 28.3 and 30.1 us).
+// us, 16384 x 4096 12.5 and 13.7 us; 20000 x 8192, narrow 6 rows 24 us, wide 8 rows 30 us).
 int gemv_splits(int64_t m, int64_t n, int64_t k) {
   if (m <= 8 || (m <= 16 && n < 18432)) return 0;
   const int64_t groups = (n + 63) / 64 * ((m + 63) / 64);
