@@ -877,6 +877,7 @@ typedef std::integral_constant<int, 1> One;
 typedef std::integral_constant<int, 2> Two;
 typedef std::integral_constant<int, 3> Three;
 typedef std::integral_constant<int, 4> Four;
+typedef std::integral_constant<int, 8> Eight;
 typedef std::integral_constant<int, 16> Sixteen;
 
 // A = w silu(g) u of every entry, [g | u] = W1_e x_t, for at most ROWS (4 or
@@ -942,8 +943,11 @@ __global__ __launch_bounds__(512, 2) void decode_up_kernel(DecodeArgs a, int par
         store_act(a.act + (int64_t)rows.entry[row] * 2 * a.ffn + f0 + (lane & 15), a.ffn, rows.weight[row], g, up);
     }
   };
+  // (8 tokens of one 4-bit expert, 4096 x 14336: 16 rows a tile 19.7 us, 8 18.3 us)
   if (ROWS <= 4 || rows.count <= 4)
     go(Four{});
+  else if (rows.count <= 8)
+    go(Eight{});
   else
     go(Sixteen{});
 }
@@ -1037,7 +1041,7 @@ struct Stretch {
 // y[t] = sum over the token's entries of W2_e . A, for at most 16
 // tokens. A workgroup owns 16 values of h; the k-steps of all named experts,
 // one after the other, are split evenly over its waves. A tile's activation
-// rows are up to 8 (2) entries' leading parts and the same entries' second
+// rows are up to 8 (4, 2) entries' leading parts and the same entries' second
 // parts, whose results are added. Each wave adds its results to a slice of its
 // own in LDS (a token appears once among an expert's entries), and the slices
 // are added in wave order, so the sum has one order whatever the timing.
@@ -1081,6 +1085,11 @@ __global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, in
           if (q >= 2) continue;
           v = acc[0][0][q] + acc[0][0][q + 2];
           row = lane < 16 ? c0 + q : rows;
+        } else if constexpr (R == 8) {
+          const uint32_t b = __float_as_uint(acc[0][0][q]);
+          const u32x2 t = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+          v = __uint_as_float(t.x) + __uint_as_float(t.y);
+          row = lane < 16 ? c0 + q : rows;
         } else {
           v = sum_halves(acc[0][0][q]);
           row = lane < 32 ? c0 + (lane >> 4) * 4 + q : rows;
@@ -1088,8 +1097,11 @@ __global__ __launch_bounds__(8 * 64, 2) void decode_down_kernel(DecodeArgs a, in
         if (row < rows) mine[plan.list[row0 + row] / a.topk * 16 + (lane & 15)] += v;
       }
     };
+    // (4 tokens of one 4-bit expert, 4096 x 14336: 16 rows a tile 11.8 us, 8 10.4 us)
     if (rows <= 2)
       go(Four{}, 0);
+    else if (rows <= 4)
+      go(Eight{}, 0);
     else
       for (int c0 = 0; c0 < rows; c0 += 8) go(Sixteen{}, c0);
   }
@@ -1257,7 +1269,11 @@ static void decode_up_go(const DecodeArgs& a, hipStream_t stream) {
   // x 14336: 23.1 us, 24.2 us).
   if (a.tokens <= 4)
     decode_up_rows<FMT, WHOLE, 4>(a, stream);
-  else if (a.tokens <= 16)
+  // Past 8 tokens, and past 4 entries an expert in the mean, the activations are
+  // worth sharing (4-bit, 16 tokens, 4 choices among 8 experts of 4096 x 14336: narrow
+  // 172 us for the layer, wide 158 us; 2 choices: no difference; 8 tokens of one
+  // expert: 32 us, 35 us).
+  else if (a.tokens <= 8 || (a.tokens <= 16 && a.tokens * a.topk <= 4 * decode_slots(a.tokens, a.topk, a.experts)))
     decode_up_rows<FMT, WHOLE, 16>(a, stream);
   // Most row tiles of a pass: fewer leave LDS for more workgroups (4-bit, 61 tokens, 5
   // choices among 60 experts of 544 x 4288: two 61 us, three 73 us), but a pass
@@ -1313,17 +1329,23 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
 // Splits of the wide second product, 0 where the narrow one runs: for up to 16
 // tokens that can name up to 16 experts (each expert is a stretch of its own of
 // every wave there: 128 experts of 2048 x 768, 16 tokens: narrow 75 us for the
-// layer, wide 66 us; 8 experts of 4096 x 14336, 1 token: narrow 38 us, wide 47
-// us), unless its hidden / 16 workgroups leave half the chip empty and have a
-// long way each (second product alone, 8 bf16 experts of 192 x 8960, 8 tokens:
-// narrow 58 us, wide and sum 14 us; 2048 x 5632, 4 tokens: narrow 27 us, 30 us;
-// two 4-bit ones of 1024 x 4096: narrow 6 us). About six workgroups a compute
-// unit (4 resident at once, 64 tokens of 8 experts: 3 a unit 126 us, 6 a unit 100
-// us), at least 512 values of k each, and no more than 16 planes to add (one 8-bit
-// expert of 2016 x 10432, 58 tokens: 8 splits 34 us, 16 28 us, 20 41 us).
+// layer, wide 66 us; 8 experts of 4096 x 14336, 1 token: narrow 38 us, wide 47 us),
+// and where no expert is likely to have more than the 8 entries of a pass (for the
+// layer, 4-bit, 16 tokens, 2 choices among 8: narrow 175 us, wide 153 us; 8-bit, 12
+// tokens, 4 choices among 16 of 2048 x 4096: 87 us, 77 us; 8-bit, 7 tokens, 2
+// choices among 8: 207 us, 213 us), unless its hidden / 16 workgroups are fewer than
+// the compute units and have a long way each (narrow and wide for the layer: 16 bf16
+// experts of 2048 x 5632 146 and 133 us, 8 of them 62 and 62 us; 4 8-bit ones of
+// 1024 x 8192 31.7 and 27.4 us; one 4-bit of 1024 x 14336 15.2 and 16.5 us; 4 of 256
+// x 4096 12.7 and 13.5 us; second product alone, 8 bf16 ones of 192 x 8960: 58 and
+// 14 us). About six workgroups a compute unit (4 resident at once, 64 tokens of 8
+// experts: 3 a unit 126 us, 6 a unit 100 us), at least 512 values of k each, and no
+// more than 16 planes to add (one 8-bit expert of 2016 x 10432, 58 tokens: 8 splits
+// 34 us, 16 28 us, 20 41 us).
 int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn) {
   const int64_t slots = decode_slots((int)tokens, topk, experts);
-  if (tokens <= 16 && slots <= 16 && tokens * topk <= 4 * slots && (hidden >= 2048 || slots * ffn < 16384)) return 0;
+  const bool long_way = hidden < 4096 && slots * ffn > std::max<int64_t>(16384, 24 * hidden);
+  if (tokens <= 16 && slots <= 16 && (tokens <= 4 || tokens * topk <= 2 * slots) && !long_way) return 0;
   const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
   return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, ffn / 512), 1536 / (groups * slots)));
 }
