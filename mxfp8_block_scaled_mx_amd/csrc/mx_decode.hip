@@ -1124,6 +1124,7 @@ constexpr int kDownTiles = 6;
 template <int FMT, bool WHOLE, int NT>
 __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];         // the shared tiles, the waves' tiles
+  __shared__ int16_t list[kDecodeTokenChunk];             // the expert's entries, one of a token at most
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int split = blockIdx.y / a.slots, slot = blockIdx.y % a.slots, chunk = blockIdx.z;
   const DecodePlan& plan = *(reinterpret_cast<const DecodePlan*>(a.plan) + chunk);
@@ -1132,6 +1133,8 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
   if (slot >= slots) return;
   const int e = __builtin_amdgcn_readfirstlane(expert), row0 = __builtin_amdgcn_readfirstlane(from);
   const int rows = __builtin_amdgcn_readfirstlane(to) - row0;
+  if (tid < rows) list[tid] = plan.list[row0 + tid];
+  __syncthreads();
   const int64_t entry0 = (int64_t)chunk * kDecodeTokenChunk * a.topk;
   const int nb = a.ffn / 32, n0 = (blockIdx.x * 4 + wave) * 16 * NT;
   int64_t first[NT];
@@ -1148,7 +1151,7 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int r = tid >> 4;
-      k.xoff[t] = (uint32_t)(2 * plan.list[row0 + min(c0 + 8 * t + (r & 7), rows - 1)] + (r >> 3)) * (uint32_t)(a.ffn * 2);
+      k.xoff[t] = (uint32_t)(2 * list[min(c0 + 8 * t + (r & 7), rows - 1)] + (r >> 3)) * (uint32_t)(a.ffn * 2);
     }
     v4f acc[NT][MT];
     clear(acc);
@@ -1158,15 +1161,12 @@ __global__ __launch_bounds__(256, 2) void decode_down_wide_kernel(DecodeArgs a) 
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = c0 + 8 * t + (lane >> 4) * 4 + q;
-        const bool ok = lane < 32 && row < rows;
-        float* to = a.sums + ((int64_t)split * a.tokens * a.topk + entry0 + (ok ? plan.list[row0 + row] : 0)) * a.hidden;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float v = sum_halves(acc[n][t][q]);
-          const int h = (int)(first[n] - (int64_t)e * a.hidden) + (lane & 15);
-          if (ok && h >= n0 + 16 * n && h < a.hidden) to[h] = v;
-        }
+        // the lower half wave stores the first tile's sums, the upper half the second's
+        const int row = c0 + 8 * t + ((lane >> 4) & 1) * 4 + q, n = lane >> 5;
+        const float v0 = sum_halves(acc[0][t][q]), v1 = sum_halves(acc[1][t][q]);
+        const int h = (int)((n ? first[1] : first[0]) - (int64_t)e * a.hidden) + (lane & 15);
+        if (row < rows && h >= n0 + 16 * n && h < a.hidden)
+          a.sums[((int64_t)split * a.tokens * a.topk + entry0 + list[row]) * a.hidden + h] = n ? v1 : v0;
       }
   };
   for (int c0 = 0; c0 < rows; c0 += 8 * kDownTiles) {
