@@ -1338,16 +1338,17 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
 // experts of 2048 x 5632 146 and 133 us, 8 of them 62 and 62 us; 4 8-bit ones of
 // 1024 x 8192 31.7 and 27.4 us; one 4-bit of 1024 x 14336 15.2 and 16.5 us; 4 of 256
 // x 4096 12.7 and 13.5 us; second product alone, 8 bf16 ones of 192 x 8960: 58 and
-// 14 us). About six workgroups a compute unit (4 resident at once, 64 tokens of 8
-// experts: 3 a unit 126 us, 6 a unit 100 us), at least 512 values of k each, and no
-// more than 16 planes to add (one 8-bit expert of 2016 x 10432, 58 tokens: 8 splits
-// 34 us, 16 28 us, 20 41 us).
+// 14 us). About four workgroups a compute unit (for the layer, 4-bit, 40 tokens, 4
+// choices among 16 experts of 2048 x 4096: four 65.8 us, six 70.6 us, eight 70.8 us;
+// bf16, 24 tokens of 8, 4096 x 14336: 469, 477 and 484 us), at least 512 values of k
+// each, and no more than 16 planes to add (one 8-bit expert of 2016 x 10432, 58
+// tokens: 8 splits 34 us, 16 28 us, 20 41 us).
 int decode_splits(int64_t tokens, int32_t topk, int32_t experts, int64_t hidden, int64_t ffn) {
   const int64_t slots = decode_slots((int)tokens, topk, experts);
   const bool long_way = hidden < 4096 && slots * ffn > std::max<int64_t>(16384, 24 * hidden);
   if (tokens <= 16 && slots <= 16 && (tokens <= 4 || tokens * topk <= 2 * slots) && !long_way) return 0;
   const int64_t groups = (hidden + 127) / 128 * ((tokens + kDecodeTokenChunk - 1) / kDecodeTokenChunk);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, ffn / 512), 1536 / (groups * slots)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(16, ffn / 512), 1024 / (groups * slots)));
 }
 
 hipError_t launch_decode(int fmt, const DecodeArgs& a, hipStream_t stream) {
