@@ -941,7 +941,10 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
 
 # ---- the few tokens of a decoding step, and the router around the experts.
 # These calls take a few microseconds on the GPU, so their checks are one
-# expression per tensor.
+# expression per tensor. A call that is given a stream runs there, on tensors
+# that are ready there: the caller lets the stream wait for what makes them, and
+# whoever reads the results wait for the stream. What the call allocates itself
+# needs no such wait.
 
 MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
 
@@ -966,20 +969,30 @@ def _on_device(stream, dev):
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
 
 
+def _alloc(shape, dtype, dev, stream):
+    """A new tensor from the memory of the stream that will write it: memory of
+    another stream may still be in use there, by work that is only queued."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _on_device(stream, dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _new(shape, dtype, dev, stream):
-    """A new tensor that the call fills (or uses) on the given stream."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None:
-        _on_device(stream, dev)
-        if t.numel():
-            t.record_stream(stream)     # not handed out again before that stream's work is done
+    """A new tensor that the call fills on the given stream and hands to its
+    caller. The caller's stream is recorded: the memory goes back to the given
+    stream only after what the caller has queued on its own by then."""
+    t = _alloc(shape, dtype, dev, stream)
+    if stream is not None and t.numel():
+        t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
 def _scratch(who, workspace, nbytes, dev, stream):
     """The caller's workspace, or a new one of nbytes (None where none is needed)."""
     if workspace is None:
-        return _new((nbytes,), torch.uint8, dev, stream) if nbytes else None
+        return _alloc((nbytes,), torch.uint8, dev, stream) if nbytes else None
     if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == dev
             and workspace.is_contiguous()):
         raise ValueError(f"{who}: workspace must be a contiguous uint8 tensor on {dev}")

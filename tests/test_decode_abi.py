@@ -112,3 +112,47 @@ def test_binding_refuses_what_does_not_fit():
                  lambda: mx.mx_moe_route_bwd(torch.zeros((2, 8)), idx, w, torch.zeros(2), w)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_what_a_call_allocates_is_memory_of_its_stream(monkeypatch):
+    """A call that is given a stream takes its memory from that stream's pool:
+    a block freed on the caller's stream may have work queued there that writes
+    it still. Results are recorded on the caller's stream, scratch is not."""
+    dev = torch.device("cuda", 0)
+
+    class Stream:
+        device = dev
+
+    class Tensor:
+        def __init__(self, n):
+            self.n, self.pool, self.recorded = n, entered[-1], []
+
+        def numel(self):
+            return self.n
+
+        def record_stream(self, s):
+            self.recorded.append(s)
+
+    class entering:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            entered.append(self.s)
+
+        def __exit__(self, *_):
+            entered.pop()
+
+    caller, side = Stream(), Stream()
+    entered = [caller]
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: Tensor(shape[0]))
+    monkeypatch.setattr(torch.cuda, "stream", entering)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: entered[-1])
+    out = mx._new((8,), torch.float32, dev, side)
+    assert out.pool is side and out.recorded == [caller]
+    ws = mx._scratch("a call", None, 512, dev, side)
+    assert ws.pool is side and ws.recorded == []
+    assert mx._scratch("a call", None, 0, dev, side) is None
+    for t in (mx._new((8,), torch.float32, dev, None), mx._scratch("a call", None, 512, dev, None)):
+        assert t.pool is caller and t.recorded == []
+    assert entered == [caller]

@@ -254,3 +254,57 @@ def test_route_then_decode(gpu_lib):
     parts = sum(np.abs(ref.moe(ref.f64(x), ridx[:, j:j + 1], rw[:, j:j + 1], w1, w2)[0]) for j in range(k))
     assert np.all(np.abs(ref.f64(y) - want) <= bound + 2 * rel * parts)
     assert not y[6].any()
+
+
+@pytest.mark.parametrize("T", [4, 64])
+def test_a_stream_that_does_not_wait_for_the_callers(gpu_lib, T):
+    """Blocks of the sizes that the call allocates were just freed on the
+    caller's stream, whose work on them is still queued when the call runs on
+    another stream: neither side writes the other's memory."""
+    gen = torch.Generator().manual_seed(24)
+    E, H, F, k = 8, 512, 1024, 2
+    args, _, _ = _weights(gpu_lib, E, H, F, "mxfp4", gen)
+    x = torch.randn((T, H), generator=gen).to(torch.bfloat16).cuda()
+    z = torch.randn((T, E), generator=gen).cuda()
+    idx, w, lse = gpu_lib.mx_moe_route(z, k)
+    q, s = args[0][0], args[2][0]                                    # one expert's first matrix, [2F, H]
+    calls = [lambda st: gpu_lib.grouped_mlp_decode(x, idx, w, *args, stream=st),
+             lambda st: gpu_lib.mx_gemv_fp4(x, q, s, out_dtype=torch.float32, stream=st),
+             lambda st: gpu_lib.mx_moe_route_bwd(z, idx, w, lse, w, stream=st),
+             lambda st: gpu_lib.mx_moe_route(z, k, stream=st)]
+    sizes = [gpu_lib.mlp_decode_workspace_bytes(E, T, H, F, k), gpu_lib.gemv_workspace_bytes(T, 2 * F, H), T * H * 2,
+             T * 2 * F * 4, T * k * 4, T * E * 4, T * 4]
+    wants = [c(None) for c in calls]
+    busy = torch.randn((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for _ in range(20):
+            busy = torch.mm(busy, busy).clamp_(-1, 1)
+        held = [torch.full((max(n, 1),), 0x7F, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(2)]
+        del held                                                     # free, and not yet written
+        got = [c(side) for c in calls]
+        torch.cuda.synchronize()
+        for a, b in zip([*got[:3], *got[3]], [*wants[:3], *wants[3]]):
+            assert torch.equal(a, b)
+
+
+def test_results_freed_while_the_callers_stream_reads_them(gpu_lib):
+    """A result that is dropped while the caller's stream has yet to read it is
+    not handed to the stream that made it before that read."""
+    gen = torch.Generator().manual_seed(25)
+    T, E, k = 4096, 64, 8
+    z = [torch.randn((T, E), generator=gen).cuda() for _ in range(2)]
+    want = gpu_lib.mx_moe_route(z[0], k)[1].sum(1)
+    busy = torch.randn((4096, 4096), device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    idx, w, lse = gpu_lib.mx_moe_route(z[0], k, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(20):
+        busy = torch.mm(busy, busy).clamp_(-1, 1)
+    got = w.sum(1)                                                   # queued behind the products
+    del idx, w, lse
+    later = [gpu_lib.mx_moe_route(z[1], k, stream=side) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(later) == 3
