@@ -200,6 +200,35 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# A call that is given a stream runs there, on tensors that are ready there: its
+# caller lets the stream wait for what makes them, and whoever reads the results
+# wait for the stream. What the call allocates itself needs no such wait.
+
+def _on_device(stream, dev):
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+
+
+def _alloc(shape, dtype, dev, stream):
+    """A new tensor from the memory of the stream that will write it: memory of
+    another stream may still be in use there, by work that is only queued."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _on_device(stream, dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _new(shape, dtype, dev, stream):
+    """A new tensor that the call fills on the given stream and hands to its
+    caller. The caller's stream is recorded: the memory goes back to the given
+    stream only after what the caller has queued on its own by then."""
+    t = _alloc(shape, dtype, dev, stream)
+    if stream is not None and t.numel():
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
 def padded_sizes(sizes):
     return [(int(m) + 31) // 32 * 32 for m in sizes]
 
@@ -219,12 +248,12 @@ def quantize(x: torch.Tensor, group_sizes=None, rowwise: bool = True, colwise: b
     dev = x.device
     out = {"q_row": None, "s_row": None, "q_col": None, "s_col": None}
     if rowwise:
-        out["q_row"] = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-        out["s_row"] = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+        out["q_row"] = _new((rows, cols), torch.uint8, dev, stream)
+        out["s_row"] = _new((rows, cols // 32), torch.uint8, dev, stream)
     if colwise:
         P = sum(padded_sizes(group_sizes if group_sizes is not None else [rows]))
-        out["q_col"] = torch.empty((cols, P), dtype=torch.uint8, device=dev)
-        out["s_col"] = torch.empty((cols, P // 32), dtype=torch.uint8, device=dev)
+        out["q_col"] = _new((cols, P), torch.uint8, dev, stream)
+        out["s_col"] = _new((cols, P // 32), torch.uint8, dev, stream)
     gs = None if group_sizes is None else _i64_array(group_sizes)
     ng = 0 if group_sizes is None else len(group_sizes)
     _check(L.mx_quantize(_ptr(x), dt, rows, cols, gs, ng, _ptr(out["q_row"]), _ptr(out["s_row"]),
@@ -248,7 +277,7 @@ def grouped_gemm(mode: int, sizes, a_q, a_s, b_q, b_s, *, N: int, K: int, M: int
     ldb = b_q.shape[-1] if ldb is None else ldb
     if out is None:
         shape = (M, N) if mode == MX_GROUP_M else (G, M, N)
-        out = torch.empty(shape, dtype=out_dtype, device=a_q.device)
+        out = _new(shape, out_dtype, a_q.device, stream)
     cdt = {torch.bfloat16: MX_BF16, torch.float32: MX_F32}[out.dtype]
     if c_group_stride is None:
         c_group_stride = M * N if mode == MX_GROUP_K else 0
@@ -379,9 +408,9 @@ def _mlp_grads(E, R, H, F, dw1=None, dw2=None):
     return [(dw1, (E, 2 * F, H), torch.float32, "dw1", True), (dw2, (E, H, F), torch.float32, "dw2", True)]
 
 
-def _byte_buffer(nbytes: int, device):
+def _byte_buffer(nbytes: int, device, stream=None):
     # 256-byte aligned (the caching allocator aligns to at least 512 bytes)
-    return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+    return _new((max(int(nbytes), 1),), torch.uint8, device, stream)
 
 
 def grouped_mlp_fwd(x, probs, w1, w2, split_sizes, *, training: bool = True, workspace=None,
@@ -397,9 +426,9 @@ def grouped_mlp_fwd(x, probs, w1, w2, split_sizes, *, training: bool = True, wor
     _mlp_inputs(E, R, H, F, split_sizes, x, w1, w2, probs, extra=[(out, (R, H), torch.bfloat16, "out", True)])
     fws, sv, _ = mlp_sizes(E, R, H, F, split_sizes)
     if workspace is None or workspace.numel() < fws:
-        workspace = _byte_buffer(fws, x.device)
-    y = torch.empty((R, H), dtype=torch.bfloat16, device=x.device) if out is None else out
-    saved = _byte_buffer(sv, x.device) if training else None
+        workspace = _byte_buffer(fws, x.device, stream)
+    y = _new((R, H), torch.bfloat16, x.device, stream) if out is None else out
+    saved = _byte_buffer(sv, x.device, stream) if training else None
     _check(L.grouped_mlp_fwd(ctypes.byref(_dims(E, R, H, F)), _i64_array(split_sizes), _ptr(x),
                              _ptr(probs), _ptr(w1), _ptr(w2), _ptr(y), _ptr(saved),
                              0 if saved is None else saved.numel(), _ptr(workspace),
@@ -425,9 +454,9 @@ def grouped_mlp_fwd_gather(x_tokens, row_token, probs, w1, w2, split_sizes, *, t
                        (out, (R, H), torch.bfloat16, "out", True)])
     fws, sv, _ = mlp_sizes(E, R, H, F, split_sizes)
     if workspace is None or workspace.numel() < fws:
-        workspace = _byte_buffer(fws, x_tokens.device)
-    y = torch.empty((R, H), dtype=torch.bfloat16, device=x_tokens.device) if out is None else out
-    saved = _byte_buffer(sv, x_tokens.device) if training else None
+        workspace = _byte_buffer(fws, x_tokens.device, stream)
+    y = _new((R, H), torch.bfloat16, x_tokens.device, stream) if out is None else out
+    saved = _byte_buffer(sv, x_tokens.device, stream) if training else None
     _check(L.grouped_mlp_fwd_gather(ctypes.byref(_dims(E, R, H, F)), _i64_array(split_sizes), _ptr(x_tokens), T,
                                     _ptr(row_token), _ptr(probs), _ptr(w1), _ptr(w2), _ptr(y), _ptr(saved),
                                     0 if saved is None else saved.numel(), _ptr(workspace), workspace.numel(),
@@ -451,15 +480,15 @@ def grouped_mlp_bwd_gather(dy_tokens, row_token, probs, state: MLPState, *, dw1=
                  (probs, (R,), torch.float32, "probs", True)] + _mlp_grads(E, R, H, F, dw1, dw2))
     _, _, bws = mlp_sizes(E, R, H, F, state.split_sizes)
     if workspace is None or workspace.numel() < bws:
-        workspace = _byte_buffer(bws, dy_tokens.device)
+        workspace = _byte_buffer(bws, dy_tokens.device, stream)
     dev = dy_tokens.device
-    dx = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dprobs = torch.empty((R,), dtype=torch.float32, device=dev) if want_dprobs else None
+    dx = _new((R, H), torch.bfloat16, dev, stream)
+    dprobs = _new((R,), torch.float32, dev, stream) if want_dprobs else None
     if dw1 is None:
-        dw1 = torch.empty((E, 2 * F, H), dtype=torch.float32, device=dev)
+        dw1 = _new((E, 2 * F, H), torch.float32, dev, stream)
         accumulate = False if dw2 is None else accumulate
     if dw2 is None:
-        dw2 = torch.empty((E, H, F), dtype=torch.float32, device=dev)
+        dw2 = _new((E, H, F), torch.float32, dev, stream)
     _check(L.grouped_mlp_bwd_gather(ctypes.byref(_dims(E, R, H, F)), _i64_array(state.split_sizes), _ptr(dy_tokens),
                                     T, _ptr(row_token), _ptr(probs), _ptr(state.saved), state.saved.numel(),
                                     _ptr(dx), _ptr(dprobs), _ptr(dw1), _ptr(dw2), int(accumulate), _ptr(workspace),
@@ -478,15 +507,15 @@ def grouped_mlp_bwd(dy, probs, state: MLPState, *, dw1=None, dw2=None, accumulat
                 + _mlp_grads(E, R, H, F, dw1, dw2))
     _, _, bws = mlp_sizes(E, R, H, F, state.split_sizes)
     if workspace is None or workspace.numel() < bws:
-        workspace = _byte_buffer(bws, dy.device)
+        workspace = _byte_buffer(bws, dy.device, stream)
     dev = dy.device
-    dx = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dprobs = torch.empty((R,), dtype=torch.float32, device=dev) if want_dprobs else None
+    dx = _new((R, H), torch.bfloat16, dev, stream)
+    dprobs = _new((R,), torch.float32, dev, stream) if want_dprobs else None
     if dw1 is None:
-        dw1 = torch.empty((E, 2 * F, H), dtype=torch.float32, device=dev)
+        dw1 = _new((E, 2 * F, H), torch.float32, dev, stream)
         accumulate = False if dw2 is None else accumulate
     if dw2 is None:
-        dw2 = torch.empty((E, H, F), dtype=torch.float32, device=dev)
+        dw2 = _new((E, H, F), torch.float32, dev, stream)
     _check(L.grouped_mlp_bwd(ctypes.byref(_dims(E, R, H, F)), _i64_array(state.split_sizes),
                              _ptr(dy), _ptr(probs), _ptr(state.saved), state.saved.numel(),
                              _ptr(dx), _ptr(dprobs), _ptr(dw1), _ptr(dw2), int(accumulate),
@@ -517,9 +546,9 @@ def grouped_mlp_fwd_fp4(x, probs, w1, w2, split_sizes, *, training: bool = True,
     _mlp_inputs(E, R, H, F, split_sizes, x, w1, w2, probs, extra=[(out, (R, H), torch.bfloat16, "out", True)])
     fws, sv, _ = mlp_fp4_sizes(E, R, H, F, split_sizes)
     if workspace is None or workspace.numel() < fws:
-        workspace = _byte_buffer(fws, x.device)
-    y = torch.empty((R, H), dtype=torch.bfloat16, device=x.device) if out is None else out
-    saved = _byte_buffer(sv, x.device) if training else None
+        workspace = _byte_buffer(fws, x.device, stream)
+    y = _new((R, H), torch.bfloat16, x.device, stream) if out is None else out
+    saved = _byte_buffer(sv, x.device, stream) if training else None
     _check(L.grouped_mlp_fwd_fp4(ctypes.byref(_dims(E, R, H, F)), _i64_array(split_sizes), _ptr(x),
                                  _ptr(probs), _ptr(w1), _ptr(w2), _ptr(y), _ptr(saved),
                                  0 if saved is None else saved.numel(), _ptr(workspace),
@@ -539,15 +568,15 @@ def grouped_mlp_bwd_fp4(dy, probs, state: MLPState, *, dw1=None, dw2=None, accum
                 + _mlp_grads(E, R, H, F, dw1, dw2))
     _, _, bws = mlp_fp4_sizes(E, R, H, F, state.split_sizes)
     if workspace is None or workspace.numel() < bws:
-        workspace = _byte_buffer(bws, dy.device)
+        workspace = _byte_buffer(bws, dy.device, stream)
     dev = dy.device
-    dx = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dprobs = torch.empty((R,), dtype=torch.float32, device=dev) if want_dprobs else None
+    dx = _new((R, H), torch.bfloat16, dev, stream)
+    dprobs = _new((R,), torch.float32, dev, stream) if want_dprobs else None
     if dw1 is None:
-        dw1 = torch.empty((E, 2 * F, H), dtype=torch.float32, device=dev)
+        dw1 = _new((E, 2 * F, H), torch.float32, dev, stream)
         accumulate = False if dw2 is None else accumulate
     if dw2 is None:
-        dw2 = torch.empty((E, H, F), dtype=torch.float32, device=dev)
+        dw2 = _new((E, H, F), torch.float32, dev, stream)
     _check(L.grouped_mlp_bwd_fp4(ctypes.byref(_dims(E, R, H, F)), _i64_array(state.split_sizes),
                                  _ptr(dy), _ptr(probs), _ptr(state.saved), state.saved.numel(),
                                  _ptr(dx), _ptr(dprobs), _ptr(dw1), _ptr(dw2), int(accumulate),
@@ -568,13 +597,13 @@ class WeightCache:
     [E,H,F] in both layouts (a caller-owned device buffer filled by
     grouped_mlp_quantize_weights, resp. grouped_mlp_fp4_quantize_weights)."""
 
-    def __init__(self, E: int, H: int, F: int, device="cuda", fmt: str = "mxfp8"):
+    def __init__(self, E: int, H: int, F: int, device="cuda", fmt: str = "mxfp8", stream=None):
         if fmt not in ("mxfp8", "mxfp4"):
             raise ValueError(f"WeightCache: unknown format {fmt!r}")
         self.ehf = (int(E), int(H), int(F))
         self.fmt = fmt
         n = grouped_mlp_weight_cache_bytes(E, H, F) if fmt == "mxfp8" else grouped_mlp_fp4_weight_cache_bytes(E, H, F)
-        self.buf = _byte_buffer(n, device)
+        self.buf = _byte_buffer(n, device, stream)
 
 
 def grouped_mlp_quantize_weights(w1, w2, cache: WeightCache | None = None, stream=None) -> WeightCache:
@@ -587,7 +616,7 @@ def grouped_mlp_quantize_weights(w1, w2, cache: WeightCache | None = None, strea
     F = F2 // 2
     _expect_all([(w1, (E, 2 * F, H), torch.bfloat16, "w1", False), (w2, (E, H, F), torch.bfloat16, "w2", False)])
     if cache is None:
-        cache = WeightCache(E, H, F, device=w1.device)
+        cache = WeightCache(E, H, F, device=w1.device, stream=stream)
     if cache.ehf != (E, H, F) or cache.fmt != "mxfp8":
         raise ValueError(f"weight cache is {cache.fmt} for (E, H, F) = {cache.ehf}, weights are MXFP8 {(E, H, F)}")
     _check(L.grouped_mlp_quantize_weights(ctypes.byref(_dims(E, 0, H, F)), _ptr(w1), _ptr(w2),
@@ -608,9 +637,9 @@ def grouped_mlp_fwd_cached(x, probs, cache: WeightCache, split_sizes, *, trainin
     _mlp_inputs(E, R, H, F, split_sizes, x, probs=probs, extra=[(out, (R, H), torch.bfloat16, "out", True)])
     fws, sv, _ = mlp_sizes(E, R, H, F, split_sizes)
     if workspace is None or workspace.numel() < fws:
-        workspace = _byte_buffer(fws, x.device)
-    y = torch.empty((R, H), dtype=torch.bfloat16, device=x.device) if out is None else out
-    saved = _byte_buffer(sv, x.device) if training else None
+        workspace = _byte_buffer(fws, x.device, stream)
+    y = _new((R, H), torch.bfloat16, x.device, stream) if out is None else out
+    saved = _byte_buffer(sv, x.device, stream) if training else None
     _check(L.grouped_mlp_fwd_cached(ctypes.byref(_dims(E, R, H, F)), _i64_array(split_sizes), _ptr(x),
                                     _ptr(probs), _ptr(cache.buf), cache.buf.numel(), _ptr(y), _ptr(saved),
                                     0 if saved is None else saved.numel(), _ptr(workspace),
@@ -632,15 +661,15 @@ def grouped_mlp_bwd_cached(dy, probs, state: MLPState, cache: WeightCache, *, dw
                 + _mlp_grads(E, R, H, F, dw1, dw2))
     _, _, bws = mlp_sizes(E, R, H, F, state.split_sizes)
     if workspace is None or workspace.numel() < bws:
-        workspace = _byte_buffer(bws, dy.device)
+        workspace = _byte_buffer(bws, dy.device, stream)
     dev = dy.device
-    dx = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dprobs = torch.empty((R,), dtype=torch.float32, device=dev) if want_dprobs else None
+    dx = _new((R, H), torch.bfloat16, dev, stream)
+    dprobs = _new((R,), torch.float32, dev, stream) if want_dprobs else None
     if dw1 is None:
-        dw1 = torch.empty((E, 2 * F, H), dtype=torch.float32, device=dev)
+        dw1 = _new((E, 2 * F, H), torch.float32, dev, stream)
         accumulate = False if dw2 is None else accumulate
     if dw2 is None:
-        dw2 = torch.empty((E, H, F), dtype=torch.float32, device=dev)
+        dw2 = _new((E, H, F), torch.float32, dev, stream)
     _check(L.grouped_mlp_bwd_cached(ctypes.byref(_dims(E, R, H, F)), _i64_array(state.split_sizes),
                                     _ptr(dy), _ptr(probs), _ptr(cache.buf), cache.buf.numel(),
                                     _ptr(state.saved), state.saved.numel(), _ptr(dx), _ptr(dprobs),
@@ -668,7 +697,7 @@ def grouped_mlp_fp4_quantize_weights(w1, w2, cache: WeightCache | None = None, s
     F = F2 // 2
     _expect_all([(w1, (E, 2 * F, H), torch.bfloat16, "w1", False), (w2, (E, H, F), torch.bfloat16, "w2", False)])
     if cache is None:
-        cache = WeightCache(E, H, F, device=w1.device, fmt="mxfp4")
+        cache = WeightCache(E, H, F, device=w1.device, fmt="mxfp4", stream=stream)
     if cache.ehf != (E, H, F) or cache.fmt != "mxfp4":
         raise ValueError(f"weight cache is {cache.fmt} for (E, H, F) = {cache.ehf}, weights are MXFP4 {(E, H, F)}")
     _check(L.grouped_mlp_fp4_quantize_weights(ctypes.byref(_dims(E, 0, H, F)), _ptr(w1), _ptr(w2),
@@ -689,9 +718,9 @@ def grouped_mlp_fwd_fp4_cached(x, probs, cache: WeightCache, split_sizes, *, tra
     _mlp_inputs(E, R, H, F, split_sizes, x, probs=probs, extra=[(out, (R, H), torch.bfloat16, "out", True)])
     fws, sv, _ = mlp_fp4_sizes(E, R, H, F, split_sizes)
     if workspace is None or workspace.numel() < fws:
-        workspace = _byte_buffer(fws, x.device)
-    y = torch.empty((R, H), dtype=torch.bfloat16, device=x.device) if out is None else out
-    saved = _byte_buffer(sv, x.device) if training else None
+        workspace = _byte_buffer(fws, x.device, stream)
+    y = _new((R, H), torch.bfloat16, x.device, stream) if out is None else out
+    saved = _byte_buffer(sv, x.device, stream) if training else None
     _check(L.grouped_mlp_fwd_fp4_cached(ctypes.byref(_dims(E, R, H, F)), _i64_array(split_sizes), _ptr(x),
                                         _ptr(probs), _ptr(cache.buf), cache.buf.numel(), _ptr(y), _ptr(saved),
                                         0 if saved is None else saved.numel(), _ptr(workspace),
@@ -713,15 +742,15 @@ def grouped_mlp_bwd_fp4_cached(dy, probs, state: MLPState, cache: WeightCache, *
                 + _mlp_grads(E, R, H, F, dw1, dw2))
     _, _, bws = mlp_fp4_sizes(E, R, H, F, state.split_sizes)
     if workspace is None or workspace.numel() < bws:
-        workspace = _byte_buffer(bws, dy.device)
+        workspace = _byte_buffer(bws, dy.device, stream)
     dev = dy.device
-    dx = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    dprobs = torch.empty((R,), dtype=torch.float32, device=dev) if want_dprobs else None
+    dx = _new((R, H), torch.bfloat16, dev, stream)
+    dprobs = _new((R,), torch.float32, dev, stream) if want_dprobs else None
     if dw1 is None:
-        dw1 = torch.empty((E, 2 * F, H), dtype=torch.float32, device=dev)
+        dw1 = _new((E, 2 * F, H), torch.float32, dev, stream)
         accumulate = False if dw2 is None else accumulate
     if dw2 is None:
-        dw2 = torch.empty((E, H, F), dtype=torch.float32, device=dev)
+        dw2 = _new((E, H, F), torch.float32, dev, stream)
     _check(L.grouped_mlp_bwd_fp4_cached(ctypes.byref(_dims(E, R, H, F)), _i64_array(state.split_sizes),
                                         _ptr(dy), _ptr(probs), _ptr(cache.buf), cache.buf.numel(),
                                         _ptr(state.saved), state.saved.numel(), _ptr(dx), _ptr(dprobs),
@@ -739,10 +768,10 @@ def mx_quantize_fp4(x: torch.Tensor, colwise: bool = False, stream=None):
         raise ValueError("mx_quantize_fp4: x must be a contiguous 2-D bfloat16 CUDA tensor")
     L = load()
     rows, cols = x.shape
-    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=x.device)
-    s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    qc = torch.empty((cols, rows // 2), dtype=torch.uint8, device=x.device) if colwise else None
-    sc = torch.empty((cols, rows // 32), dtype=torch.uint8, device=x.device) if colwise else None
+    q = _new((rows, cols // 2), torch.uint8, x.device, stream)
+    s = _new((rows, cols // 32), torch.uint8, x.device, stream)
+    qc = _new((cols, rows // 2), torch.uint8, x.device, stream) if colwise else None
+    sc = _new((cols, rows // 32), torch.uint8, x.device, stream) if colwise else None
     _check(L.mx_quantize_fp4(_ptr(x), rows, cols, _ptr(q), _ptr(s), _ptr(qc), _ptr(sc), _stream(stream)))
     return (q, s, qc, sc) if colwise else (q, s)
 
@@ -762,7 +791,7 @@ def mx_gemm_fp4(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, out=None, stream=N
                             or out.dtype not in (torch.bfloat16, torch.float32)):
         raise ValueError("mx_gemm_fp4: out must be a contiguous bf16 or fp32 [m, n] tensor")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a_q.device)
+        out = _new((m, n), out_dtype, a_q.device, stream)
     dt = MX_F32 if out.dtype == torch.float32 else MX_BF16
     _check(L.mx_gemm_fp4(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), m, n, k, _ptr(out), dt, _stream(stream)))
     return out
@@ -783,7 +812,7 @@ def mx_grouped_gemm_fp4(a_q, a_s, b_q, b_s, group_sizes, out_dtype=torch.bfloat1
             or tuple(b_s.shape) != (G, n, k // 32)):
         raise ValueError("mx_grouped_gemm_fp4: operand shapes do not match the group sizes")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a_q.device)
+        out = _new((m, n), out_dtype, a_q.device, stream)
     if tuple(out.shape) != (m, n) or not out.is_contiguous() or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("mx_grouped_gemm_fp4: out must be a contiguous bf16 or fp32 [M, n] tensor")
     dt = MX_F32 if out.dtype == torch.float32 else MX_BF16
@@ -804,11 +833,11 @@ def mx_quantize_nvfp4(x: torch.Tensor, colwise: bool = False, rowwise: bool = Tr
     L = load()
     rows, cols = x.shape
     dev = x.device
-    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev) if rowwise else None
-    s = torch.empty((rows, cols // 16), dtype=torch.uint8, device=dev) if rowwise else None
-    qc = torch.empty((cols, rows // 2), dtype=torch.uint8, device=dev) if colwise else None
-    sc = torch.empty((cols, rows // 16), dtype=torch.uint8, device=dev) if colwise else None
-    amax = torch.empty((1,), dtype=torch.float32, device=dev)
+    q = _new((rows, cols // 2), torch.uint8, dev, stream) if rowwise else None
+    s = _new((rows, cols // 16), torch.uint8, dev, stream) if rowwise else None
+    qc = _new((cols, rows // 2), torch.uint8, dev, stream) if colwise else None
+    sc = _new((cols, rows // 16), torch.uint8, dev, stream) if colwise else None
+    amax = _new((1,), torch.float32, dev, stream)
     _check(L.mx_quantize_nvfp4(_ptr(x), rows, cols, _ptr(q), _ptr(s), _ptr(qc), _ptr(sc), _ptr(amax),
                                _stream(stream)))
     return (q, s, amax, qc, sc) if colwise else (q, s, amax)
@@ -833,7 +862,7 @@ def mx_grouped_gemm_nvfp4(a_q, a_s, a_amax, b_q, b_s, b_amax, group_sizes, out_d
             or tuple(b_s.shape) != (G, n, k // 16)):
         raise ValueError("mx_grouped_gemm_nvfp4: operand shapes do not match the group sizes")
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a_q.device)
+        out = _new((m, n), out_dtype, a_q.device, stream)
     if tuple(out.shape) != (m, n) or not out.is_contiguous() or out.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("mx_grouped_gemm_nvfp4: out must be a contiguous bf16 or fp32 [M, n] tensor")
     dt = MX_F32 if out.dtype == torch.float32 else MX_BF16
@@ -864,8 +893,8 @@ def mx_quantize_fp4_colwise_grouped(x, group_sizes, stream=None):
         raise ValueError(f"mx_quantize_fp4_colwise_grouped: group sizes {sizes} must be >= 0 and sum to {rows}")
     P = sum(padded_sizes(sizes))
     L = load()
-    qc = torch.empty((cols, P // 2), dtype=torch.uint8, device=x.device)
-    sc = torch.empty((cols, P // 32), dtype=torch.uint8, device=x.device)
+    qc = _new((cols, P // 2), torch.uint8, x.device, stream)
+    sc = _new((cols, P // 32), torch.uint8, x.device, stream)
     _check(L.mx_quantize_fp4_colwise_grouped(_ptr(x), rows, cols, _i64_array(sizes), len(sizes), _ptr(qc), _ptr(sc),
                                              _stream(stream)))
     return qc, sc
@@ -886,7 +915,7 @@ def mx_grouped_gemm_fp4_wgrad(a_q, a_s, b_q, b_s, group_sizes, out=None, accumul
     if accumulate and out is None:
         raise ValueError("mx_grouped_gemm_fp4_wgrad: accumulate needs out")
     if out is None:
-        out = torch.empty((G, m, n), dtype=torch.float32, device=a_q.device)
+        out = _new((G, m, n), torch.float32, a_q.device, stream)
     L = load()
     _check(L.mx_grouped_gemm_fp4_wgrad(_ptr(a_q), _ptr(a_s), _ptr(b_q), _ptr(b_s), _i64_array(sizes), G, m, n,
                                        _ptr(out), int(bool(accumulate)), _stream(stream)))
@@ -907,12 +936,12 @@ def mx_moe_dispatch(x, topk_idx, topk_w, num_experts: int, stream=None, gather: 
     _expect_all([(x, (T, H), torch.bfloat16, "x", False), (topk_idx, (T, k), torch.int32, "topk_idx", False),
                  (topk_w, (T, k), torch.float32, "topk_w", True)])
     dev = x.device
-    x_perm = torch.empty((T * k, H), dtype=x.dtype, device=dev) if gather else None
-    probs_perm = torch.empty((T * k,), dtype=torch.float32, device=dev) if topk_w is not None else None
-    perm = torch.empty((T, k), dtype=torch.int32, device=dev)
-    row_token = torch.empty((T * k,), dtype=torch.int32, device=dev)
-    counts = torch.empty((num_experts,), dtype=torch.int64, device=dev)
-    ws = _byte_buffer(L.mx_moe_dispatch_workspace_bytes(T, k, num_experts), dev)
+    x_perm = _new((T * k, H), x.dtype, dev, stream) if gather else None
+    probs_perm = _new((T * k,), torch.float32, dev, stream) if topk_w is not None else None
+    perm = _new((T, k), torch.int32, dev, stream)
+    row_token = _new((T * k,), torch.int32, dev, stream)
+    counts = _new((num_experts,), torch.int64, dev, stream)
+    ws = _byte_buffer(L.mx_moe_dispatch_workspace_bytes(T, k, num_experts), dev, stream)
     _check(L.mx_moe_dispatch(_ptr(x) if gather else None, _ptr(topk_idx), _ptr(topk_w), T, H, k, num_experts,
                              _ptr(x_perm),
                              _ptr(probs_perm), _ptr(perm), _ptr(row_token), _ptr(counts), _ptr(ws), ws.numel(),
@@ -934,17 +963,14 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
     _expect_all([(perm, (T, k), torch.int32, "perm", False),
                  (y_perm, (y_perm.shape[0], H), torch.bfloat16, "y_perm", False),
                  (out, (T, H), torch.bfloat16, "out", True)])
-    y = torch.empty((T, H), dtype=y_perm.dtype, device=y_perm.device) if out is None else out
+    y = _new((T, H), y_perm.dtype, y_perm.device, stream) if out is None else out
     _check(L.mx_moe_combine(_ptr(y_perm), _ptr(perm), T, H, k, _ptr(y), _stream(stream)))
     return y
 
 
 # ---- the few tokens of a decoding step, and the router around the experts.
 # These calls take a few microseconds on the GPU, so their checks are one
-# expression per tensor. A call that is given a stream runs there, on tensors
-# that are ready there: the caller lets the stream wait for what makes them, and
-# whoever reads the results wait for the stream. What the call allocates itself
-# needs no such wait.
+# expression per tensor.
 
 MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
 
@@ -962,31 +988,6 @@ def _need(who, name, t, shape, dtype, dev):
 
 def _opt(who, name, t, shape, dtype, dev):
     return None if t is None else _need(who, name, t, shape, dtype, dev)
-
-
-def _on_device(stream, dev):
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-
-
-def _alloc(shape, dtype, dev, stream):
-    """A new tensor from the memory of the stream that will write it: memory of
-    another stream may still be in use there, by work that is only queued."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _on_device(stream, dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _new(shape, dtype, dev, stream):
-    """A new tensor that the call fills on the given stream and hands to its
-    caller. The caller's stream is recorded: the memory goes back to the given
-    stream only after what the caller has queued on its own by then."""
-    t = _alloc(shape, dtype, dev, stream)
-    if stream is not None and t.numel():
-        t.record_stream(torch.cuda.current_stream(dev))
-    return t
 
 
 def _scratch(who, workspace, nbytes, dev, stream):
@@ -1234,7 +1235,7 @@ class MLPRunner:
         """Fill this runner's weight cache (allocated on first use) from w1, w2."""
         E, _, H, F = self.dims
         if getattr(self, "cache", None) is None:
-            self.cache = WeightCache(E, H, F, device=self.y.device)
+            self.cache = WeightCache(E, H, F, device=self.y.device, stream=stream)
         grouped_mlp_quantize_weights(w1, w2, self.cache, stream=stream)
         return self.cache
 
