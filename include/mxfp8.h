@@ -728,7 +728,7 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
  * have one order for a given shape, so results repeat bit for bit. m or n zero
  * is a no-op. Errors: MX_EINVAL (null pointers, y_dtype), MX_ESHAPE (negative
  * sizes, k not a positive multiple of 32, ldx), MX_EALIGN, MX_EWORKSPACE,
- * MX_EUNSUPPORTED (m > 65536, n > 2^30, k or ldx > 2^24), MX_EHIP.
+ * MX_EUNSUPPORTED (m > 65536, n > 2^30 - 64, k or ldx > 2^24), MX_EHIP.
  */
 MX_API mx_status mx_gemv_sizes(int64_t m, int64_t n, int64_t k, size_t* workspace);
 MX_API mx_status mx_gemv_fp4(const void* x, int64_t ldx, const uint8_t* w, const uint8_t* w_s, int64_t m, int64_t n,
@@ -812,7 +812,7 @@ MX_API mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_we
  * Both: tokens == 0 is a no-op. Errors: MX_EINVAL (null pointers, dtype),
  * MX_ESHAPE (negative sizes, topk outside 1 .. num_experts, dw_rows not
  * tokens * topk without perm), MX_EALIGN, MX_EUNSUPPORTED (num_experts >
- * MX_MAX_GROUPS, topk > MX_ROUTE_MAX_TOPK, tokens > 2^27), MX_EHIP.
+ * MX_MAX_GROUPS, topk > MX_ROUTE_MAX_TOPK, tokens > 2^27 - 8), MX_EHIP.
  */
 #define MX_ROUTE_MAX_TOPK 16
 MX_API mx_status mx_moe_route(const void* logits, mx_dtype logits_dtype, const float* bias, int64_t tokens,

@@ -1833,13 +1833,19 @@ mx_status grouped_mlp_bwd_fp4_cached(const mx_mlp_dims* dims, const int64_t* spl
 
 namespace {
 
+// Most weight rows of a few-row product and most tokens of a router call: a
+// launch has fewer than 2^32 threads along x, and these are 256 threads for 64
+// weight rows or 8 tokens.
+constexpr int64_t kGemvMaxN = ((int64_t)1 << 30) - 64;
+constexpr int64_t kRouteMaxTokens = ((int64_t)1 << 27) - 8;
+
 // Sizes of a few-row product: MX_OK and its workspace, the planes of sums of a
 // product that splits k over workgroups.
 mx_status gemv_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes, const char* who) {
   if (m < 0 || n < 0 || k <= 0 || k % 32)
     return fail(MX_ESHAPE, "%s: need m, n >= 0 and k a positive multiple of 32", who);
-  if (m > 65536 || n > ((int64_t)1 << 30) || k > ((int64_t)1 << 24))
-    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30 and k <= 2^24", who);
+  if (m > 65536 || n > kGemvMaxN || k > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: need m <= 65536, n <= 2^30 - 64 and k <= 2^24", who);
   const int splits = m > 0 && n > 0 ? mx::gemv_splits(m, n, k) : 0;
   *bytes = splits > 1 ? (size_t)splits * m * n * 4 : 0;
   return MX_OK;
@@ -1908,7 +1914,7 @@ mx_status route_checks(const char* who, mx_dtype dt, int64_t tokens, int32_t E, 
   if (E < 1 || topk < 1 || topk > E) return fail(MX_ESHAPE, "%s: need 1 <= topk <= num_experts", who);
   if (E > mx::kMaxGroups) return fail(MX_EUNSUPPORTED, "%s: %d experts exceeds the maximum %d", who, E, mx::kMaxGroups);
   if (topk > MX_ROUTE_MAX_TOPK) return fail(MX_EUNSUPPORTED, "%s: topk %d exceeds the maximum %d", who, topk, MX_ROUTE_MAX_TOPK);
-  if (tokens > ((int64_t)1 << 27)) return fail(MX_EUNSUPPORTED, "%s: more than 2^27 tokens", who);
+  if (tokens > kRouteMaxTokens) return fail(MX_EUNSUPPORTED, "%s: more than 2^27 - 8 tokens", who);
   return MX_OK;
 }
 

@@ -156,3 +156,19 @@ def test_what_a_call_allocates_is_memory_of_its_stream(monkeypatch):
     for t in (mx._new((8,), torch.float32, dev, None), mx._scratch("a call", None, 512, dev, None)):
         assert t.pool is caller and t.recorded == []
     assert entered == [caller]
+
+
+def test_sizes_whose_launch_would_pass_the_thread_limit_are_refused(L):
+    """A launch has fewer than 2^32 threads along x: 256 of them take 64 weight
+    rows (wide products) or 8 tokens (more than 64 experts)."""
+    n = ctypes.c_size_t()
+    most = (1 << 30) - 64
+    for m in (1, 9, 64):
+        assert L.mx_gemv_sizes(m, most, 32, ctypes.byref(n)) == OK
+        for over in (most + 1, 1 << 30):
+            assert L.mx_gemv_sizes(m, over, 32, ctypes.byref(n)) == EUNSUPPORTED
+            assert L.mx_gemv_fp4(FAKE, 32, FAKE, FAKE, m, over, 32, FAKE, 0, None, 0, None) == EUNSUPPORTED
+    for over in ((1 << 27) - 7, 1 << 27):
+        assert L.mx_moe_route(FAKE, 0, None, over, 128, 2, 1, FAKE, FAKE, FAKE, None) == EUNSUPPORTED
+        assert L.mx_moe_route_bwd(FAKE, 0, None, FAKE, FAKE, FAKE, FAKE, over * 2, None, over, 128, 2, 1, FAKE,
+                                  None) == EUNSUPPORTED
