@@ -975,6 +975,11 @@ def mx_moe_combine(y_perm, perm, out=None, stream=None):
 MX_W_BF16, MX_W_MXFP8, MX_W_MXFP4 = 0, 1, 2
 
 
+def _i32(n):
+    """A count as the C ABI's int32: one that passes it is refused there, not cut."""
+    return min(n, 2 ** 31 - 1)
+
+
 def _need(who, name, t, shape, dtype, dev):
     """The address of t, a contiguous tensor of that shape, dtype and device."""
     try:
@@ -1072,8 +1077,8 @@ def mx_gemv_nvfp4(x, w_q, w_s, w_amax, out_dtype=torch.bfloat16, out=None, works
 @functools.lru_cache(maxsize=4096)
 def _decode_dims(E, T, H, F, k):
     """The dims of a decode call and its workspace's bytes."""
-    dims, nbytes = ctypes.byref(_Dims(E, T, H, F)), ctypes.c_size_t()
-    _check(load().grouped_mlp_decode_sizes(dims, k, ctypes.byref(nbytes)))
+    dims, nbytes = ctypes.byref(_Dims(_i32(E), T, H, F)), ctypes.c_size_t()
+    _check(load().grouped_mlp_decode_sizes(dims, _i32(k), ctypes.byref(nbytes)))
     return dims, nbytes.value
 
 
@@ -1139,11 +1144,11 @@ def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=
     T, E = logits.shape
     dev = logits.device
     b = _opt("mx_moe_route", "bias", bias, (E,), torch.float32, dev)
-    k = topk if topk > 0 else 0
+    k = topk if 0 < topk <= E else 0        # 0 is refused by the call, and allocates nothing
     idx = _new((T, k), torch.int32, dev, stream)
     w = _new((T, k), torch.float32, dev, stream)
     lse = _new((T,), torch.float32, dev, stream)
-    _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, b, T, E, topk, 1 if renormalize else 0,
+    _call(load().mx_moe_route, dev, stream, logits.data_ptr(), dt, b, T, _i32(E), k, 1 if renormalize else 0,
           idx.data_ptr(), w.data_ptr(), lse.data_ptr())
     return idx, w, lse
 
@@ -1167,7 +1172,7 @@ def mx_moe_route_bwd(logits, topk_idx, topk_w, lse, dw, perm=None, bias=None, re
             _need(who, "dw", dw, (T, k) if perm is None else dw.shape, torch.float32, dev), dw.numel(),
             _opt(who, "perm", perm, (T, k), torch.int32, dev))
     dlogits = _new((T, E), logits.dtype, dev, stream)
-    _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, *args, T, E, k, 1 if renormalize else 0,
+    _call(load().mx_moe_route_bwd, dev, stream, logits.data_ptr(), dt, *args, T, _i32(E), _i32(k), 1 if renormalize else 0,
           dlogits.data_ptr())
     return dlogits
 

@@ -172,3 +172,9 @@ def test_sizes_whose_launch_would_pass_the_thread_limit_are_refused(L):
         assert L.mx_moe_route(FAKE, 0, None, over, 128, 2, 1, FAKE, FAKE, FAKE, None) == EUNSUPPORTED
         assert L.mx_moe_route_bwd(FAKE, 0, None, FAKE, FAKE, FAKE, FAKE, over * 2, None, over, 128, 2, 1, FAKE,
                                   None) == EUNSUPPORTED
+
+
+def test_counts_past_32_bits_are_refused_not_cut(L):
+    for E, k in ((4, 2 ** 32 + 2), (2 ** 32 + 4, 2), (4, 2 ** 31)):
+        with pytest.raises(mx.MXError):
+            mx.mlp_decode_workspace_bytes(E, 3, 64, 96, k)

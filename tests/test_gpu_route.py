@@ -212,3 +212,13 @@ def test_training_chain(gpu_lib):
     want, bound = ref.route_bwd(ref.f64(z), None, idx.cpu().numpy(), ref.f64(w), ref.f64(lse), dw, True)
     assert np.all(np.abs(ref.f64(dz) - want) <= bound + 1e-37)
     assert np.abs(want).max() > 0
+
+
+def test_topk_out_of_range_is_refused_before_anything_is_allocated(gpu_lib):
+    z = torch.zeros((64, 8), device="cuda")
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.max_memory_allocated()
+    for k in (0, -1, 9, 10 ** 9, 2 ** 32 + 2):
+        with pytest.raises(gpu_lib.MXError):
+            gpu_lib.mx_moe_route(z, k)
+    assert torch.cuda.max_memory_allocated() - before <= 4096
