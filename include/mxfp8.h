@@ -705,8 +705,14 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
 /*
  * The few tokens of a decoding step. The calls below read every weight once
  * for a handful of rows; the activations stay bf16 and only the weights are
- * block-scaled, so each weight is expanded exactly (an E2M1 or E4M3 element
- * times its scale fits bf16) and products are summed in fp32.
+ * block-scaled. Each weight is expanded to bf16 and products are summed in
+ * fp32. The expansion is exact wherever bf16 reaches (an element times its
+ * scale has at most 6 significant bits): for every NVFP4 weight, MXFP4 under
+ * scale codes 0 .. 252, MXFP8 under scale codes 3 .. 246, and for whatever
+ * mx_quantize and mx_quantize_fp4 make of finite bf16 weights. Under other
+ * scale codes a magnitude from 2^128 on becomes infinite, and what lies below
+ * bf16's last step, 2^-133, is rounded to a neighbouring step. Scale code 255
+ * and the E4M3 NaN codes are outside the contract.
  *
  * mx_gemv_fp4 / mx_gemv_nvfp4 -- y[m, n] = x[m, k] . W[n, k]^T with W in the
  * rowwise layout of mx_quantize_fp4 (one E8M0 scale per 32 values) or

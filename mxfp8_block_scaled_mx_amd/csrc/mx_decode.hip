@@ -10,9 +10,11 @@
 //     bf16, MXFP8 or MXFP4 weights.
 //
 // The activations stay bf16 (weight-only quantization): every weight is
-// expanded exactly to bf16 in registers (an E2M1 or E4M3 element times a power
-// of two, or E2M1 times E4M3, has at most 6 significant bits), and products
-// are summed in fp32 by the 16 x 16 x 32 bf16 MFMA.
+// expanded to bf16 in registers, exactly between bf16's last step, 2^-133, and
+// 2^128 (an E2M1 or E4M3 element times a power of two, or E2M1 times E4M3, has at
+// most 6 significant bits; E4M3 reaches below 2^-133 under scale codes 0 .. 2 and
+// past 2^128 from code 247 on), and products are summed in fp32 by the 16 x 16 x
+// 32 bf16 MFMA.
 //
 // All of it is bound by reading the weights: a byte of 4-bit codes meets 4
 // operations per row, far below what the MFMA needs to be busy. So a kernel is

@@ -308,3 +308,80 @@ def test_results_freed_while_the_callers_stream_reads_them(gpu_lib):
     later = [gpu_lib.mx_moe_route(z[1], k, stream=side) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(later) == 3
+
+
+# All E8M0 scale codes, each with 8 groups of 32 E4M3 codes. NaN codes and values
+# from 2^128 on are left out (they would spread over their row): zero instead.
+def _all_mxfp8():
+    codes = np.tile(np.arange(256, dtype=np.uint8).reshape(8, 32), (255, 1))          # [255 * 8, 32]
+    scales = np.repeat(np.arange(255, dtype=np.uint8), 8)[:, None]
+    with np.errstate(invalid="ignore"):
+        codes[~(np.abs(ref.mxfp8(codes, scales)) < 2.0 ** 128)] = 0
+    assert (codes[24:247 * 8] == 0).sum() == (247 - 3) * (1 + 2)                      # codes 3 .. 246: zero and the two NaNs
+    return codes, scales, ref.mxfp8(codes, scales)
+
+
+def _check_expanded(got, want):
+    """Exact where bf16 has the value: any multiple of 2^-133, its last step
+    (under scale codes from 3 on every one is); within that step otherwise."""
+    exact = np.ldexp(want, 133) % 1.0 == 0
+    assert exact[24:].all() and not exact[:24].all()
+    assert np.array_equal(got[exact], want[exact])
+    assert np.all(np.abs(got - want) < 2.0 ** -133)
+
+
+def test_every_mxfp8_code_and_scale_in_the_second_product(gpu_lib):
+    """Tokens and experts that make A a unit matrix pick single weights: token t
+    has g = 32 and u = 1 at f = t only, and weight 2^-5 (silu(32) is 32 in fp32,
+    silu(0) is 0)."""
+    codes, scales, want = _all_mxfp8()
+    H, F = 2048, 32
+    w2, s2 = np.zeros((1, H, F), dtype=np.uint8), np.full((1, H, 1), 127, dtype=np.uint8)
+    w2[0, :2040], s2[0, :2040] = codes, scales
+    w1 = np.zeros((1, 2 * F, H), dtype=np.uint8)
+    w1[0, np.arange(F), np.arange(F)], w1[0, F + np.arange(F), np.arange(F)] = 0x60, 0x38       # 32 and 1
+    s1 = np.full((1, 2 * F, H // 32), 127, dtype=np.uint8)
+    put = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    x = torch.eye(F, H).to(torch.bfloat16).cuda()
+    idx, wt = torch.zeros((F, 1), dtype=torch.int32, device="cuda"), torch.full((F, 1), 2.0 ** -5, device="cuda")
+    for T in (4, 16, 32):
+        y = gpu_lib.grouped_mlp_decode(x[:T], idx[:T], wt[:T], put(w1), put(w2), put(s1), put(s2))
+        if T == 32:
+            _check_expanded(ref.f64(y).T[:2040], want)
+        else:
+            full = gpu_lib.grouped_mlp_decode(x, idx, wt, put(w1), put(w2), put(s1), put(s2))
+            assert torch.equal(y, full[:T])
+
+
+def test_every_mxfp8_code_and_scale_in_the_first_product(gpu_lib):
+    """The codes as rows of u, g = 32 everywhere, W2 a unit matrix: y[t, f] is
+    expert t / 32's weight f under the unit token t % 32."""
+    codes, scales, want = _all_mxfp8()
+    H = F = 32
+    put = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    E = 32
+    x = torch.eye(H).repeat(E, 1).to(torch.bfloat16).cuda()
+    idx = torch.arange(E, dtype=torch.int32).repeat_interleave(H)[:, None].contiguous().cuda()
+    wt = torch.full((E * H, 1), 2.0 ** -5, device="cuda")
+    w2, s2 = np.tile((np.eye(H) * 0x38).astype(np.uint8), (E, 1, 1)), np.full((E, H, 1), 127, dtype=np.uint8)
+    got = np.zeros_like(want)
+    for r0 in (0, 2040 - E * F):
+        w1 = np.full((E, 2 * F, H), 0x60, dtype=np.uint8)
+        s1 = np.full((E, 2 * F, 1), 127, dtype=np.uint8)
+        w1[:, F:], s1[:, F:] = codes[r0:r0 + E * F].reshape(E, F, H), scales[r0:r0 + E * F].reshape(E, F, 1)
+        y = ref.f64(gpu_lib.grouped_mlp_decode(x, idx, wt, put(w1), put(w2), put(s1), put(s2)))
+        got[r0:r0 + E * F] = y.reshape(E, H, F).transpose(0, 2, 1).reshape(E * F, H)
+    _check_expanded(got, want)
+
+
+def test_weights_that_the_cast_makes_of_bf16_are_exact(gpu_lib):
+    """bf16 weights down to its last subnormal, cast to MXFP8: every value that
+    the cast makes is a multiple of 2^-133 below 2^128."""
+    rng = np.random.default_rng(26)
+    bits = rng.integers(0, 2 ** 16, size=(512, 256)).astype(np.uint16)
+    bits[:256] &= 0x81FF                                             # magnitudes below 2^-123
+    bits[256:384] = (bits[256:384] & 0x80FF) | 0x7E00                # magnitudes from 2^125 on
+    bits[(bits & 0x7F80) == 0x7F80] = 0                              # no infinities, no NaN
+    d = gpu_lib.quantize(torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16), colwise=False)
+    v = ref.mxfp8(d["q_row"].cpu().numpy(), d["s_row"].cpu().numpy())
+    assert np.all(np.abs(v) < 2.0 ** 128) and np.all(np.ldexp(v, 133) % 1.0 == 0)

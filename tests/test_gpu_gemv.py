@@ -196,3 +196,16 @@ def test_repeats_bit_for_bit_on_streams_and_in_graphs(gpu_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager), i
+
+
+def test_every_nvfp4_code_and_scale(gpu_lib):
+    """Unit rows pick single weights: all 16 codes under every E4M3 scale, the
+    subnormal ones and 448 among them, exactly (amax 2688: tensor scale 1)."""
+    scales = np.arange(127, dtype=np.uint8)
+    q = np.tile(np.tile(np.arange(16, dtype=np.uint8), 2)[0::2] | (np.tile(np.arange(16, dtype=np.uint8), 2)[1::2] << 4), (127, 1))
+    s = np.repeat(scales[:, None], 2, axis=1)
+    want = ref.nvfp4(q, s, 2688.0).T
+    for m in (4, 8, 16, 32):
+        got = gpu_lib.mx_gemv_nvfp4(_bf16(np.eye(32)[:m]), _u8(q), _u8(s), torch.tensor([2688.0], device="cuda"),
+                                    out_dtype=torch.float32)
+        assert np.array_equal(ref.f64(got), want[:m])
