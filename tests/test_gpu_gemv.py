@@ -209,3 +209,45 @@ def test_every_nvfp4_code_and_scale(gpu_lib):
         got = gpu_lib.mx_gemv_nvfp4(_bf16(np.eye(32)[:m]), _u8(q), _u8(s), torch.tensor([2688.0], device="cuda"),
                                     out_dtype=torch.float32)
         assert np.array_equal(ref.f64(got), want[:m])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("m,n,k", [(40, 300, 4096), (64, 129, 7200), (17, 70, 8192)])
+def test_split_products_repeat_in_a_workspace_of_their_size(gpu_lib, fmt, m, n, k):
+    """Products that split k over workgroups: the caller's workspace of exactly
+    the size asked for, full of NaN before each call; other streams, two graphs
+    that share it, replays with new rows and eager work in between."""
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    x = torch.randn((m, k), generator=gen, device="cuda").to(torch.bfloat16)
+    w = torch.randn((n, k), generator=gen, device="cuda").to(torch.bfloat16)
+    gemv, weight = ((gpu_lib.mx_gemv_fp4, gpu_lib.mx_quantize_fp4(w)) if fmt == "mxfp4" else
+                    (gpu_lib.mx_gemv_nvfp4, gpu_lib.mx_quantize_nvfp4(w)))
+    nbytes = gpu_lib.gemv_workspace_bytes(m, n, k)
+    assert nbytes > 0 and nbytes % (m * n * 4) == 0
+    buf, ws = guarded((nbytes,))
+    side = torch.cuda.Stream()
+    outs, graphs = [torch.empty((m, n), dtype=dt, device="cuda") for dt in (torch.float32, torch.bfloat16)], []
+    wants = [gemv(x, *weight, out_dtype=o.dtype) for o in outs]
+    for o, want in zip(outs, wants):
+        for stream in (None, side):
+            ws.fill_(0xFF)
+            o.zero_()
+            torch.cuda.synchronize()
+            gemv(x, *weight, out=o, workspace=ws, stream=stream)
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and canaries_intact(buf)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            gemv(x, *weight, out=o, workspace=ws)
+        graphs.append(g)
+    with pytest.raises(gpu_lib.MXError):
+        gemv(x, *weight, out=outs[0], workspace=ws[:-1])
+    for i in range(4):
+        x.copy_(torch.randn((m, k), generator=gen, device="cuda"))
+        eager = [gemv(x, *weight, out_dtype=o.dtype) for o in outs]
+        ws.fill_(0xFF)
+        for g, o, want in zip(graphs, outs, eager):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and canaries_intact(buf), i
