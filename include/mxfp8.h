@@ -721,13 +721,15 @@ MX_API mx_status mx_moe_dispatch_noalloc(const void* x, const int32_t* topk_idx,
  * training with native PyTorch training loop" (Quantized Training), for one
  * row or a few. mx_gemm_fp4 / mx_gemm_nvfp4 take 4-bit rows x as well and are
  * the calls for many rows; these two are made for m up to 64 and read W again
- * for every further 64 rows.
+ * for every further 64 rows (28672 x 4096, MXFP4: 64 rows 38 us, 128 rows 69 us;
+ * casting x and mx_gemm_fp4: 45 and 49 us).
  *   x        bf16 [m, k], consecutive rows ldx elements apart (ldx >= k where
  *            m > 1, ldx % 8 == 0), 16-byte aligned.
  *   w, w_s   codes [n, k/2], scales [n, k/32] (E8M0, codes 0 .. 254) or
  *            [n, k/16] (E4M3); w 16-byte, NVFP4 scales 2-byte aligned.
  *   w_amax   device fp32, the weight's amax from mx_quantize_nvfp4.
- *   y        [m, n] row-major, bf16 (rounded once, to nearest even) or fp32.
+ *   y        [m, n] row-major, bf16 (rounded once, to nearest even) or fp32, not
+ *            overlapping x.
  *   workspace  mx_gemv_sizes bytes (0 for m <= 16 and for many shapes above;
  *            then it may be NULL), 256-byte aligned.
  * Rows of x do not mix: an infinity or NaN in one row stays in that row. Sums
@@ -767,7 +769,10 @@ MX_API mx_status mx_gemv_nvfp4(const void* x, int64_t ldx, const uint8_t* w, con
  *   topk_w     f32 [tokens, topk] or NULL (all 1).
  *   workspace  grouped_mlp_decode_sizes bytes, 256-byte aligned.
  * Requires H % 32 == 0 and F % 32 == 0. Only weights of experts that a token
- * names are read. Results repeat bit for bit. tokens == 0 is a no-op.
+ * names are read, again for every further 64 tokens (2 choices of 8 experts of
+ * 4096 x 14336, MXFP4: 64 tokens 173 us, 128 tokens 342 us; mx_moe_dispatch,
+ * grouped_mlp_fwd_fp4_cached and mx_moe_combine: 300 and 311 us). Results repeat
+ * bit for bit. tokens == 0 is a no-op.
  * Errors: MX_EINVAL, MX_ESHAPE, MX_EALIGN (x, w1, w2, y 16-byte, topk_idx and
  * topk_w 4-byte, workspace 256-byte), MX_EWORKSPACE, MX_EUNSUPPORTED (more
  * than MX_MAX_GROUPS experts, topk, too many entries, H or F above 2^19),
@@ -797,7 +802,8 @@ MX_API mx_status grouped_mlp_decode(const mx_mlp_dims* dims, int32_t topk, mx_we
  *                the dispatch drops) with weight 0.
  *   topk_w       f32 [tokens, topk].
  *   lse          f32 [tokens]: log of the sum of exp(logit) over the open
- *                experts (-inf if none), for the backward and for a z-loss.
+ *                experts (-inf if none), for the backward, which takes the
+ *                gradient of the weights and none of lse.
  * Logits of +inf are outside the contract (weights are then unspecified, the
  * choices are not).
  *

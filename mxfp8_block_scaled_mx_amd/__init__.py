@@ -13,6 +13,8 @@ training for biological foundation models", Key technical approaches item 3).
 For decoding steps: mx_gemv_fp4 / mx_gemv_nvfp4 (a few rows times 4-bit
 weights) and grouped_mlp_decode (the MoE MLP of a few tokens); for routers:
 mx_moe_route / mx_moe_route_bwd, and MoERoute, an autograd Function over them.
+GroupedMLP and MoERoute alone take part in autograd: what the other calls return
+has no history, also where an input requires a gradient.
 """
 from __future__ import annotations
 
@@ -1063,7 +1065,8 @@ def _gemv(who, fn, group, x, w_q, w_s, amax, out_dtype, out, workspace, stream):
 def mx_gemv_fp4(x, w_q, w_s, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """y [m, n] = x . W^T (mx_gemv_fp4): x bf16 [m, k] (its rows may be apart,
     by a multiple of 8 elements), W rowwise MXFP4 as mx_quantize_fp4 makes it
-    (w_q [n, k/2], w_s [n, k/32]). Made for m up to 64; bf16 or fp32.
+    (w_q [n, k/2], w_s [n, k/32]). Made for m up to 64; bf16 or fp32, without
+    autograd history.
     workspace: uint8, gemv_workspace_bytes(m, n, k) (allocated when None)."""
     return _gemv("mx_gemv_fp4", load().mx_gemv_fp4, 32, x, w_q, w_s, None, out_dtype, out, workspace, stream)
 
@@ -1093,7 +1096,7 @@ def grouped_mlp_decode(x, topk_idx, topk_w, w1, w2, w1_s=None, w2_s=None, *, out
     fp32 [T, k] or None (all 1) -> y bf16 [T, H]. Weights: bf16 w1 [E, 2F, H]
     and w2 [E, H, F]; or rowwise codes with scales w1_s [E, 2F, H/32] and w2_s
     [E, H, F/32]: uint8 w1 [E, 2F, H], w2 [E, H, F] (MXFP8) or w1 [E, 2F, H/2],
-    w2 [E, H, F/2] (MXFP4). T * k <= 1024."""
+    w2 [E, H, F/2] (MXFP4). T * k <= 1024. No autograd history."""
     who = "grouped_mlp_decode"
     if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda):
         raise ValueError(f"{who}: x must be a [T, H] CUDA tensor")
@@ -1139,7 +1142,8 @@ def mx_moe_route(logits, topk: int, bias=None, renormalize: bool = True, stream=
     """The router's choice (mx_moe_route): logits [T, E] bf16 or fp32, bias
     fp32 [E] (for the choice only) or None -> (topk_idx int32 [T, topk],
     topk_w fp32 [T, topk], lse fp32 [T]), as mx_moe_dispatch and
-    grouped_mlp_decode take them."""
+    grouped_mlp_decode take them. No autograd history (MoERoute has one, for
+    topk_w)."""
     dt = _logits_dtype("mx_moe_route", logits)
     T, E = logits.shape
     dev = logits.device

@@ -21,19 +21,21 @@
 // a way to keep enough whole cache lines of weights on their way: 32 to 64 KiB a
 // compute unit, since a line takes 2 to 3 us when the memory is busy (reading
 // alone reaches 6.9 TB/s on this layout of loads). What the forms reach (weight
-// bytes over time, the calls' other reads not counted):
-//   gemv_kernel       4-bit, 1 row: 28672 x 4096 12.6 us, 5.0 TB/s; 4096 x
-//                     14336 8.6 us, 3.6 TB/s (3 us are the launch); NVFP4, 5
-//                     rows, 14336 x 4096: 11.5 us, 2.9 TB/s (its expansion takes
-//                     twice the instructions)
-//   gemv_wide_kernel  4-bit, 28672 x 4096: 16 rows 17.1 us, 3.6 TB/s; 32 rows 21.2
-//                     us, 2.9 TB/s (the activations take the same path through
-//                     the load unit and LDS as the weights)
-//   decode_up_kernel  8 experts of 4096 x 14336, 2 choices: 1 token, 4-bit, 23 us,
-//                     5.4 TB/s; 7 tokens, 8-bit, 135 us, 6.2 TB/s
-//   decode_down_kernel   the same: 13.8 us, 4.5 TB/s; 76 us, 5.5 TB/s
-//   decode_up_wide_kernel, decode_down_wide_kernel   64 tokens, 4-bit: 103 us, 4.8
-//                     TB/s; 89 us, 2.8 TB/s (its activations are twice 16 bits
+// bytes over time, the calls' other reads not counted; 12 inputs in turn, means):
+//   gemv_kernel       4-bit, 1 row: 28672 x 4096 13.9 us, 4.5 TB/s; 4096 x
+//                     14336 8.7 us, 3.6 TB/s (3 us are the launch); NVFP4, 5
+//                     rows, 14336 x 4096: 12.1 us, 2.7 TB/s (vector units 22% busy,
+//                     load unit 20%, LDS 12%: a wave's load, expansion, LDS and
+//                     MFMA follow each other)
+//   gemv_wide_kernel  4-bit, 28672 x 4096: 16 rows 18.5 us, 3.4 TB/s; 32 rows 21.8
+//                     us, 2.9 TB/s; 64 rows 36.7 us, 1.7 TB/s (the activations take
+//                     the same path through the load unit and LDS as the weights:
+//                     LDS 41% busy at 64 rows, no other unit above 26%)
+//   decode_up_kernel  8 experts of 4096 x 14336, 2 choices: 1 token, 4-bit, 22.8 us,
+//                     5.5 TB/s; 7 tokens, 8-bit, 131 us, 6.2 TB/s
+//   decode_down_kernel   the same: 14.1 us, 4.4 TB/s; 71.6 us, 5.7 TB/s
+//   decode_up_wide_kernel, decode_down_wide_kernel   64 tokens, 4-bit: 109 us, 4.5
+//                     TB/s; 87 us, 2.8 TB/s (its activations are twice 16 bits
 //                     of every value, and as many bytes as the weights by way of L2)
 #include <stddef.h>
 
@@ -136,9 +138,11 @@ __device__ __forceinline__ int part_start(int nb, int i, int n) {
 // The MFMA's lane layout (lane l holds row l % 16) makes neighbouring lanes
 // read different rows, which costs the load path one cache line per lane. So
 // rows are loaded as whole pieces (consecutive lanes, consecutive 16-byte
-// chunks) and the tile's chunks are swizzled so that neither its writes nor its
-// reads conflict on banks. Scales come 1 KiB (G steps) at a time. No barrier:
-// the tile is the wave's own.
+// chunks) and the tile's chunks are swizzled. That leaves bank conflicts: the
+// rows of a 4-bit or 8-bit tile are 128 bytes, so rows r and r + 8 of a read share
+// their banks, and scales are read byte by byte. Conflicts are 17 to 44% of the
+// LDS's busy cycles, and those 12 to 42% of a kernel's. Scales come 1 KiB (G
+// steps) at a time. No barrier: the tile is the wave's own.
 //
 // WHOLE: k is a multiple of the step, and scale rows of 16 bytes. Otherwise
 // blocks past the end repeat the last one and count as zero.
@@ -608,6 +612,11 @@ static void gemv_go(const GemvArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((gemv_kernel<FMT, NT, R, false, D>), grid, dim3(64 * waves), lds, stream, a, parts);
 }
 
+// One tile of weight rows a wave. Two feed each activation fragment to two MFMAs
+// but halve the workgroups: better for more than 32 rows only (one and two, 28672
+// x 4096, 4-bit: 16 rows 16.1 and 17.0 us, 32 rows 20.5 and 19.9 us, 64 rows 36.0
+// and 29.4 us; NVFP4: 18.8 and 19.9, 23.2 and 24.4, 38.3 and 34.8 us; 64 x 4096 x
+// 14336, 4-bit: 26.5 and 24.2 us).
 template <int FMT, int MT>
 static void gemv_wide_go(const GemvArgs& a, hipStream_t stream) {
   constexpr int NT = 1, D = 1;
@@ -690,7 +699,7 @@ namespace {
 // Entries are taken in groups of whole tokens, at most 64 entries. stage() puts
 // them into LDS for the workgroup, so that what follows waits for memory once
 // (61 tokens, 5 choices among 60 experts of 544 x 4288, 4-bit, first product:
-// BEFORE us reading them from memory, AFTER us).
+// 88 us reading them from memory, 76 us).
 struct Entries {
   const int32_t* idx;               // the chunk's entries
   int n, topk, per;                 // entries, choices per token, entries per group (topk * floor(64 / topk))
@@ -865,7 +874,9 @@ struct ExpertRows {
 };
 
 // A = w silu(g) u of one value, kept as the sum of two bf16 numbers (16 bits),
-// since the second product takes bf16. to: the entry's row, ffn further the second part.
+// since the second product takes bf16 (0.1 to 0.3% of the layer's bf16 results then
+// differ from the rounded exact ones, 0.1 to 0.2% where A stays fp32; a third
+// number would be half as many activations and MFMAs again). to: the entry's row, ffn further the second part.
 __device__ __forceinline__ void store_act(uint16_t* to, int ffn, float w, float g, float u) {
   const float v = w * (g / (1.0f + expf(-g))) * u;
   const __bf16 hi = (__bf16)v;
@@ -1336,11 +1347,20 @@ static hipError_t decode_go(const DecodeArgs& a, hipStream_t stream) {
 // layer, 4-bit, 16 tokens, 2 choices among 8: narrow 175 us, wide 153 us; 8-bit, 12
 // tokens, 4 choices among 16 of 2048 x 4096: 87 us, 77 us; 8-bit, 7 tokens, 2
 // choices among 8: 207 us, 213 us), unless its hidden / 16 workgroups are fewer than
-// the compute units and have a long way each (narrow and wide for the layer: 16 bf16
-// experts of 2048 x 5632 146 and 133 us, 8 of them 62 and 62 us; 4 8-bit ones of
-// 1024 x 8192 31.7 and 27.4 us; one 4-bit of 1024 x 14336 15.2 and 16.5 us; 4 of 256
-// x 4096 12.7 and 13.5 us; second product alone, 8 bf16 ones of 192 x 8960: 58 and
-// 14 us). About four workgroups a compute unit (for the layer, 4-bit, 40 tokens, 4
+// the compute units and have a long way each, slots * ffn values of k (16 bf16
+// experts of 2048 x 5632, 16 tokens, narrow and wide for the layer: 146 and 133 us).
+// The wide form adds a launch and its planes, which take longer the more hidden
+// there is, so the way has two bounds, where 4-bit weights break even. One token,
+// narrow and wide for the layer, 4 choices of 4 experts:
+//   hidden 256:  way 16384, 4-bit 14.5 and 14.6 us, 8-bit 17.2 and 16.0, bf16 21.3
+//     and 17.3; way 24576, 17.3 and 15.6, 21.9 and 17.1, 27.4 and 19.0 us
+//   hidden 1024: way 24576 (24 hidden), 19.2 and 19.1, 27.4 and 24.1, 41.8 and 38.5
+//     us; way 49152, 31.6 and 27.6, 48.4 and 39.8, 76.9 and 61.8 us
+//   hidden 2048: way 49152 (24 hidden), 39.6 and 41.0, 63.4 and 64.4, 115 and 109
+//     us; way 98304, 69.7 and 66.1, 119 and 108, 226 and 193 us
+// Wider weights would go over earlier (bf16 from a way of about 12288 on: up to 28%
+// at hidden 64 and 256, 14% above); past the bounds the worst is 4-bit at hidden
+// 3584, way 98304, 97.8 and 104.0 us. About four workgroups a compute unit (for the layer, 4-bit, 40 tokens, 4
 // choices among 16 experts of 2048 x 4096: four 65.8 us, six 70.6 us, eight 70.8 us;
 // bf16, 24 tokens of 8, 4096 x 14336: 469, 477 and 484 us), at least 512 values of k
 // each, and no more than 16 planes to add (one 8-bit expert of 2016 x 10432, 58
