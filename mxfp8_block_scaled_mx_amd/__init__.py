@@ -225,8 +225,10 @@ def _new(shape, dtype, dev, stream):
     """A new tensor that the call fills on the given stream and hands to its
     caller. The caller's stream is recorded: the memory goes back to the given
     stream only after what the caller has queued on its own by then."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
     t = _alloc(shape, dtype, dev, stream)
-    if stream is not None and t.numel():
+    if t.numel():
         t.record_stream(torch.cuda.current_stream(dev))
     return t
 
