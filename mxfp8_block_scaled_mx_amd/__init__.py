@@ -203,11 +203,13 @@ def _stream(stream=None):
 
 
 # A call that is given a stream runs there, on tensors that are ready there: its
-# caller lets the stream wait for what makes them, and whoever reads the results
-# wait for the stream. What the call allocates itself needs no such wait.
+# caller lets the stream wait for what makes them, keeps them until the stream has
+# run the call (or records the stream on them), and lets whoever reads the results
+# wait for the stream. What the call allocates itself needs none of this.
 
 def _on_device(stream, dev):
-    if stream.device != dev:
+    dev = torch.device(dev)                 # ("cuda" without a number is any stream's)
+    if stream.device.type != dev.type or dev.index not in (None, stream.device.index):
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
 
 
@@ -229,7 +231,7 @@ def _new(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
     t = _alloc(shape, dtype, dev, stream)
     if t.numel():
-        t.record_stream(torch.cuda.current_stream(dev))
+        t.record_stream(torch.cuda.current_stream(stream.device))
     return t
 
 

@@ -33,6 +33,24 @@ def test_every_allocation_of_a_call_names_its_stream():
     assert seen > 60
 
 
+def test_the_streams_device_is_checked():
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    for dev in ("cuda", "cuda:1", torch.device("cuda"), torch.device("cuda", 1)):
+        mx._on_device(Stream(), dev)
+    for dev in ("cuda:0", torch.device("cuda", 0), "cpu", torch.device("cpu")):
+        with pytest.raises(ValueError):
+            mx._on_device(Stream(), dev)
+
+
+@pytest.mark.gpu
+def test_weight_cache_of_a_stream(gpu_lib):
+    side = torch.cuda.Stream()
+    cache = gpu_lib.WeightCache(2, 128, 128, stream=side)
+    assert cache.buf.device == side.device and cache.buf.numel() == gpu_lib.grouped_mlp_weight_cache_bytes(2, 128, 128)
+
+
 @pytest.mark.gpu
 def test_streams_that_do_not_wait_for_the_callers(gpu_lib):
     """Blocks of the sizes that the calls allocate were just freed on the
