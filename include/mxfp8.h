@@ -836,6 +836,136 @@ MX_API mx_status mx_moe_route_bwd(const void* logits, mx_dtype logits_dtype, con
                                   int32_t topk, int32_t renormalize, void* dlogits, void* stream);
 
 /*
+ * The balance loss of a router's choices, so that training keeps the experts'
+ * load even (the article's Dense vs. MoE scaling: each token activates a few
+ * experts, GroupedLinear takes what falls to each). For the tokens of one
+ * sequence, n of them, with p the softmax of a token's logits over its open
+ * experts as mx_moe_route defines them (0 for shut ones):
+ *     counts_e    = how often topk_idx names expert e
+ *     mean_prob_e = 1/n sum over t of p_te
+ *     loss        = num_experts / (topk n) sum over e of counts_e mean_prob_e
+ * which is 1 for an even load. Weighting the losses and adding them up is left
+ * to the caller, as is a loss of counts summed over several devices: its
+ * gradient for mean_prob goes in as dmean_prob.
+ *   logits, bias  as in mx_moe_route.
+ *   topk_idx      int32 [tokens, topk]; entries outside [0, num_experts) count
+ *                 nowhere.
+ *   segments      int32 [sequences + 1] on the device: sequence s is tokens
+ *                 [segments[s], segments[s + 1]); offsets do not fall, and
+ *                 equal ones make an empty sequence (loss and means 0). Tokens
+ *                 before the first and behind the last offset (padding) take no
+ *                 part. Offsets outside 0 .. tokens are cut there. NULL with
+ *                 sequences == 1: all tokens.
+ *   loss          f32 [sequences];  counts int64 [sequences, num_experts] (with
+ *                 one sequence the split_sizes that mx_moe_dispatch returns);
+ *                 mean_prob f32 [sequences, num_experts].
+ *   workspace     mx_moe_balance_sizes bytes (0 for short calls; then it may be
+ *                 NULL), 256-byte aligned.
+ * Sums are kept in 64 bits, in one order for a given shape, so results repeat
+ * bit for bit. Logits of +inf are outside the contract.
+ *
+ * mx_moe_balance_bwd -- gradient for the logits:
+ *     A_e = dloss num_experts counts_e / (topk n) + dmean_prob_e
+ *     dlogits_te = add_te + p_te / n (A_e - sum over j of p_tj A_j)
+ *   dloss         f32 [sequences], or NULL (then counts may be NULL too).
+ *   counts        of the forward; dmean_prob f32 [sequences, num_experts] or NULL.
+ *   add           [tokens, num_experts] of logits_dtype or NULL: a gradient to add
+ *                 to, such as mx_moe_route_bwd's; dlogits itself may be given.
+ *   dlogits       [tokens, num_experts] of logits_dtype, rounded once, all of it
+ *                 written: tokens outside the sequences get add, or 0. It does not
+ *                 overlap the other arrays, nor add in part.
+ * tokens == 0: the forward writes zeros, the backward is a no-op. Errors:
+ * MX_EINVAL (null pointers, dtype), MX_ESHAPE (negative sizes, topk outside 1 ..
+ * num_experts, sequences < 1, more than one without segments), MX_EALIGN,
+ * MX_EWORKSPACE, MX_EUNSUPPORTED (as mx_moe_route; sequences > MX_MAX_SEQUENCES),
+ * MX_EHIP.
+ */
+#define MX_MAX_SEQUENCES 65534
+MX_API mx_status mx_moe_balance_sizes(int64_t tokens, int32_t num_experts, int32_t sequences, size_t* workspace);
+MX_API mx_status mx_moe_balance(const void* logits, mx_dtype logits_dtype, const float* bias, const int32_t* topk_idx,
+                                const int32_t* segments, int32_t sequences, int64_t tokens, int32_t num_experts,
+                                int32_t topk, float* loss, int64_t* counts, float* mean_prob, void* workspace,
+                                size_t workspace_bytes, void* stream);
+MX_API mx_status mx_moe_balance_bwd(const void* logits, mx_dtype logits_dtype, const float* bias,
+                                    const int64_t* counts, const float* dloss, const float* dmean_prob,
+                                    const int32_t* segments, int32_t sequences, int64_t tokens, int32_t num_experts,
+                                    int32_t topk, const void* add, void* dlogits, void* stream);
+
+/*
+ * 8-bit integers with one scale per row: per token for activations, per output
+ * channel for weights. The plainest 8-bit format beside the block-scaled ones
+ * above, for serving weights that were made for it.
+ *
+ * mx_quantize_int8 -- with a = max(max |x| of the row, 2^-100):
+ *     q = the integer nearest to 127 x / a (the exact quotient; ties to even),
+ *     s = a / 127, times row_weight where given (fp32, rounded each time);
+ *   a value is q s. A NaN or infinity makes its row's scale NaN or infinite, and
+ *   no other row's.
+ *   x           bf16 or f32 [x_rows, cols], rows ldx values apart (ldx >= cols
+ *               where x_rows > 1; a multiple of 16 bytes), 16-byte aligned.
+ *   row_index   int32 [rows]: row r is made from row row_index[r] of x (the
+ *               dispatch's row_token); an index outside [0, x_rows) makes a row
+ *               of zeros. NULL: row r of x, rows == x_rows.
+ *   row_weight  f32 [rows] or NULL (the routing weights of the rows: what follows
+ *               is linear in a row, so its weight can ride on its scale).
+ *   q           int8 [rows, cols] in -127 .. 127;  s  f32 [rows].
+ * Requires cols % 16 == 0. Weights [E, n, k] are cast as [E n, k].
+ * Errors: MX_EINVAL, MX_ESHAPE, MX_EALIGN (x, q 16-byte), MX_EUNSUPPORTED (rows
+ * >= 2^24, x_rows >= 2^31, cols or ldx > 2^24), MX_EHIP.
+ *
+ * mx_gemm_int8 / mx_grouped_gemm_int8 -- C[m, n] = a_s[m] b_s[n] sum over k of
+ * A[m, k] B[n, k] (GroupedLinear over split_sizes, article item 1). The sum is
+ * exact in 32 bits, so a result does not depend on how the work is split.
+ *   a, a_s  int8 [m, k] (-128 .. 127), f32 [m];  b, b_s  int8 [n, k], f32 [n]
+ *           (grouped: [groups, n, k], [groups, n]).
+ *   group_sizes  int64 [groups]: rows of A per group, in order, summing to m. On
+ *           the host; or for the _device_split call on the device, read when the
+ *           kernel runs: a count below 0 reads as 0, one that would take the
+ *           running sum past m is cut there, and rows of C behind the last group
+ *           are not written.
+ *   c       [m, n] row-major, bf16 (rounded to nearest even) or fp32.
+ * m or n zero is a no-op. Errors: MX_EINVAL (null pointers, dtype, groups < 1),
+ * MX_ESHAPE (negative sizes, k not a positive multiple of 16), MX_EALIGN (a, b
+ * 16-byte, others by element), MX_EUNSUPPORTED (groups > MX_MAX_GROUPS, m or n >
+ * 2^30, k > 131071, too many tiles), MX_EHIP.
+ *
+ * grouped_mlp_fwd_int8 -- the MoE MLP (article item 3) for inference on int8
+ * weights: for expert e and its rows, w the row's routing weight,
+ *     [g | u] = W1_e Q(x);  A = silu(g) u (fp32);  y = w W2_e Q(A)
+ * with Q the cast above (of X inside the call, of A with w on its scales).
+ *   dims         num_experts, rows (routed), hidden, ffn (multiples of 32).
+ *   split_sizes / split_sizes_dev  rows per expert on the host, or on the device
+ *                (as _device_split above; rows of y behind the last expert's are
+ *                not written); exactly one of them.
+ *   x            bf16 [rows, H], or with row_token (int32 [rows]) [tokens, H] as
+ *                in grouped_mlp_fwd_gather.
+ *   probs        f32 [rows] or NULL (all 1).
+ *   w1, w1_s     int8 [E, 2F, H] (gate rows, then up rows), f32 [E, 2F];
+ *   w2, w2_s     int8 [E, H, F], f32 [E, H].
+ *   y            bf16 [rows, H], rounded once.
+ *   workspace    grouped_mlp_int8_sizes bytes, 256-byte aligned.
+ * Errors as above, and MX_EWORKSPACE.
+ */
+MX_API mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_rows, int64_t cols, int64_t ldx,
+                                  const int32_t* row_index, int64_t rows, const float* row_weight, int8_t* q,
+                                  float* s, void* stream);
+MX_API mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m,
+                              int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* stream);
+MX_API mx_status mx_grouped_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
+                                      const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n, int64_t k,
+                                      void* c, mx_dtype c_dtype, void* stream);
+MX_API mx_status mx_grouped_gemm_int8_device_split(const int8_t* a, const float* a_s, const int8_t* b,
+                                                   const float* b_s, const int64_t* group_sizes, int32_t groups,
+                                                   int64_t m, int64_t n, int64_t k, void* c, mx_dtype c_dtype,
+                                                   void* stream);
+MX_API mx_status grouped_mlp_int8_sizes(const mx_mlp_dims* dims, size_t* workspace);
+MX_API mx_status grouped_mlp_fwd_int8(const mx_mlp_dims* dims, const int64_t* split_sizes,
+                                      const int64_t* split_sizes_dev, const void* x, int64_t tokens,
+                                      const int32_t* row_token, const float* probs, const int8_t* w1,
+                                      const float* w1_s, const int8_t* w2, const float* w2_s, void* y,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * mx_set_stage_events -- optional per-stage timing of the fused MLP calls
  * (observability only; the results are the same). While events are set, the
  * fused MLP calls run every stage on the caller's stream in order, without

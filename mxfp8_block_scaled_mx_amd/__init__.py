@@ -12,9 +12,12 @@ ScaledSwiGLU -> GroupedLinear with routing-weight scaling: "Efficient MoE
 training for biological foundation models", Key technical approaches item 3).
 For decoding steps: mx_gemv_fp4 / mx_gemv_nvfp4 (a few rows times 4-bit
 weights) and grouped_mlp_decode (the MoE MLP of a few tokens); for routers:
-mx_moe_route / mx_moe_route_bwd, and MoERoute, an autograd Function over them.
-GroupedMLP and MoERoute alone take part in autograd: what the other calls return
-has no history, also where an input requires a gradient.
+mx_moe_route / mx_moe_route_bwd, and MoERoute, an autograd Function over them,
+and likewise for the balance loss mx_moe_balance / mx_moe_balance_bwd and
+MoEBalance. On weights in 8-bit integers: mx_quantize_int8, mx_gemm_int8,
+mx_grouped_gemm_int8 and grouped_mlp_fwd_int8.
+GroupedMLP, MoERoute and MoEBalance alone take part in autograd: what the other
+calls return has no history, also where an input requires a gradient.
 """
 from __future__ import annotations
 
@@ -30,7 +33,9 @@ __all__ = [
     "grouped_mlp_fwd", "grouped_mlp_bwd", "GroupedMLP", "MLPState", "MLPRunner",
     "set_stage_events", "FWD_STAGES", "BWD_STAGES", "mx_quantize_fp4", "mx_gemm_fp4", "mx_grouped_gemm_fp4",
     "mx_gemv_fp4", "mx_gemv_nvfp4", "gemv_workspace_bytes", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
-    "mx_moe_route", "mx_moe_route_bwd", "MoERoute",
+    "mx_moe_route", "mx_moe_route_bwd", "MoERoute", "mx_moe_balance", "mx_moe_balance_bwd", "MoEBalance",
+    "moe_balance_workspace_bytes", "mx_quantize_int8", "mx_gemm_int8", "mx_grouped_gemm_int8", "grouped_mlp_fwd_int8",
+    "mlp_int8_workspace_bytes",
 ]
 
 FWD_STAGES = ("quantize_x", "quantize_w1", "quantize_w2", "gemm1_swiglu", "gemm2")
@@ -175,6 +180,24 @@ def load() -> ctypes.CDLL:
     L.mx_moe_route.argtypes = [vp, i32, vp, i64, i32, i32, i32, vp, vp, vp, vp]
     L.mx_moe_route_bwd.restype = ctypes.c_int
     L.mx_moe_route_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, vp, i64, i32, i32, i32, vp, vp]
+    L.mx_moe_balance_sizes.restype = ctypes.c_int
+    L.mx_moe_balance_sizes.argtypes = [i64, i32, i32, ctypes.POINTER(sz)]
+    L.mx_moe_balance.restype = ctypes.c_int
+    L.mx_moe_balance.argtypes = [vp, i32, vp, vp, vp, i32, i64, i32, i32, vp, vp, vp, vp, sz, vp]
+    L.mx_moe_balance_bwd.restype = ctypes.c_int
+    L.mx_moe_balance_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, vp]
+    L.mx_quantize_int8.restype = ctypes.c_int
+    L.mx_quantize_int8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp]
+    L.mx_gemm_int8.restype = ctypes.c_int
+    L.mx_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.mx_grouped_gemm_int8.restype = ctypes.c_int
+    L.mx_grouped_gemm_int8.argtypes = [vp, vp, vp, vp, p64, i32, i64, i64, i64, vp, i32, vp]
+    L.mx_grouped_gemm_int8_device_split.restype = ctypes.c_int
+    L.mx_grouped_gemm_int8_device_split.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i32, vp]
+    L.grouped_mlp_int8_sizes.restype = ctypes.c_int
+    L.grouped_mlp_int8_sizes.argtypes = [ctypes.POINTER(_Dims), ctypes.POINTER(sz)]
+    L.grouped_mlp_fwd_int8.restype = ctypes.c_int
+    L.grouped_mlp_fwd_int8.argtypes = [ctypes.POINTER(_Dims), p64, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.mx_device_copy.restype = ctypes.c_int
     L.mx_device_copy.argtypes = [vp, vp, i64, vp]
     L.mx_set_stage_events.restype = ctypes.c_int
@@ -1185,6 +1208,234 @@ def mx_moe_route_bwd(logits, topk_idx, topk_w, lse, dw, perm=None, bias=None, re
     return dlogits
 
 
+# ---- the balance loss of the router's choices
+
+@functools.lru_cache(maxsize=4096)
+def moe_balance_workspace_bytes(T: int, E: int, sequences: int = 1) -> int:
+    """Bytes of the workspace of mx_moe_balance (0: none)."""
+    nbytes = ctypes.c_size_t()
+    _check(load().mx_moe_balance_sizes(T, _i32(E), _i32(sequences), ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+def _sequences(who, segments, dev):
+    """The number of sequences and the address of their offsets."""
+    if segments is None:
+        return 1, None
+    if not (isinstance(segments, torch.Tensor) and segments.dim() == 1):
+        raise ValueError(f"{who}: segments must be an int32 [sequences + 1] tensor")
+    return segments.shape[0] - 1, _need(who, "segments", segments, segments.shape, torch.int32, dev)
+
+
+def mx_moe_balance(logits, topk_idx, bias=None, segments=None, workspace=None, stream=None):
+    """The balance loss of a router's choices (mx_moe_balance): logits [T, E] bf16
+    or fp32 and bias as in mx_moe_route, topk_idx int32 [T, k] its choices,
+    segments int32 [S + 1] the sequences' token offsets or None (S = 1, all
+    tokens) -> (loss fp32 [S], counts int64 [S, E], mean_prob fp32 [S, E]). No
+    autograd history (MoEBalance has one, for loss and mean_prob)."""
+    who = "mx_moe_balance"
+    dt = _logits_dtype(who, logits)
+    T, E = logits.shape
+    dev = logits.device
+    if not (isinstance(topk_idx, torch.Tensor) and topk_idx.dim() == 2):
+        raise ValueError(f"{who}: topk_idx must be [T, k]")
+    k = topk_idx.shape[1]
+    b, idx = _opt(who, "bias", bias, (E,), torch.float32, dev), _need(who, "topk_idx", topk_idx, (T, k), torch.int32, dev)
+    S, seg = _sequences(who, segments, dev)
+    nbytes = moe_balance_workspace_bytes(T, E, S)
+    if nbytes or workspace is not None:
+        workspace = _scratch(who, workspace, nbytes, dev, stream)
+    loss = _new((S,), torch.float32, dev, stream)
+    counts = _new((S, E), torch.int64, dev, stream)
+    mean_prob = _new((S, E), torch.float32, dev, stream)
+    _call(load().mx_moe_balance, dev, stream, logits.data_ptr(), dt, b, idx, seg, S, T, _i32(E), _i32(k), loss.data_ptr(),
+          counts.data_ptr(), mean_prob.data_ptr(), None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel())
+    return loss, counts, mean_prob
+
+
+def mx_moe_balance_bwd(logits, counts, topk: int, dloss=None, dmean_prob=None, bias=None, segments=None, add=None,
+                       out=None, stream=None):
+    """Gradient of mx_moe_balance's loss and mean_prob with respect to the logits
+    (mx_moe_balance_bwd): dloss fp32 [S] or None, dmean_prob fp32 [S, E] or None,
+    counts the forward's (or None without dloss) -> dlogits [T, E] of the logits'
+    dtype, added to `add` (a gradient such as mx_moe_route_bwd's, which may be
+    `out` too). topk, bias and segments as in the forward."""
+    who = "mx_moe_balance_bwd"
+    dt = _logits_dtype(who, logits)
+    T, E = logits.shape
+    dev = logits.device
+    S, seg = _sequences(who, segments, dev)
+    if dloss is not None and counts is None:
+        raise ValueError(f"{who}: the gradient of the loss needs the counts")
+    args = (_opt(who, "bias", bias, (E,), torch.float32, dev), _opt(who, "counts", counts, (S, E), torch.int64, dev),
+            _opt(who, "dloss", dloss, (S,), torch.float32, dev),
+            _opt(who, "dmean_prob", dmean_prob, (S, E), torch.float32, dev), seg)
+    base = _opt(who, "add", add, (T, E), logits.dtype, dev)
+    if out is None:
+        out = _new((T, E), logits.dtype, dev, stream)
+        dz = out.data_ptr()
+    else:
+        dz = _need(who, "out", out, (T, E), logits.dtype, dev)
+    _call(load().mx_moe_balance_bwd, dev, stream, logits.data_ptr(), dt, *args, S, T, _i32(E), _i32(topk), base, dz)
+    return out
+
+
+# ---- 8-bit integers with a scale per row
+
+def mx_quantize_int8(x, row_index=None, row_weight=None, stream=None):
+    """8-bit integers of bf16 or fp32 x [rows, cols] with a scale per row
+    (mx_quantize_int8; its rows may be apart by a multiple of 16 bytes) ->
+    (q int8 [rows, cols], s fp32 [rows]). row_index int32 [n]: the n rows
+    x[row_index] instead (zeros where an index lies outside x); row_weight fp32:
+    a factor for each scale. Weights x [E, rows, cols] (contiguous, without
+    row_index) -> q [E, rows, cols], s [E, rows]."""
+    who = "mx_quantize_int8"
+    if not (isinstance(x, torch.Tensor) and x.dtype in (torch.bfloat16, torch.float32) and x.dim() in (2, 3) and x.is_cuda):
+        raise ValueError(f"{who}: x must be a 2-D or 3-D bfloat16 or float32 CUDA tensor")
+    shape, dev = x.shape, x.device
+    if x.dim() == 3:
+        if row_index is not None or not x.is_contiguous():
+            raise ValueError(f"{who}: a 3-D x must be contiguous and goes without row_index")
+        x = x.view(shape[0] * shape[1], shape[2])
+    rows, cols = x.shape
+    ldx, inner = x.stride()
+    if inner != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{who}: the elements of a row of x must be consecutive")
+    idx, n = None, rows
+    if row_index is not None:
+        if not (isinstance(row_index, torch.Tensor) and row_index.dim() == 1):
+            raise ValueError(f"{who}: row_index must be an int32 [n] tensor")
+        n = row_index.shape[0]
+        idx = _need(who, "row_index", row_index, (n,), torch.int32, dev)
+    weight = _opt(who, "row_weight", row_weight, (n,), torch.float32, dev)
+    q = _new((n, cols), torch.int8, dev, stream)
+    s = _new((n,), torch.float32, dev, stream)
+    _call(load().mx_quantize_int8, dev, stream, x.data_ptr(), MX_F32 if x.dtype is torch.float32 else MX_BF16, rows, cols,
+          ldx if rows > 1 else (cols + 7) // 8 * 8, idx, n, weight, q.data_ptr(), s.data_ptr())
+    return (q, s) if len(shape) == 2 else (q.view(shape), s.view(shape[:2]))
+
+
+def _out_tensor(who, out, out_dtype, shape, dev, stream):
+    """The result of a product, given or new: (tensor, its address, its dtype's code)."""
+    if out is not None:
+        out_dtype = out.dtype if isinstance(out, torch.Tensor) else None
+    if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+        raise ValueError(f"{who}: the output is bfloat16 or float32")
+    if out is None:
+        out = _new(shape, out_dtype, dev, stream)
+        at = out.data_ptr()
+    else:
+        at = _need(who, "out", out, shape, out_dtype, dev)
+    return out, at, MX_F32 if out_dtype is torch.float32 else MX_BF16
+
+
+def _int8_rows(who, a_q, a_s):
+    if not (isinstance(a_q, torch.Tensor) and a_q.dim() == 2 and a_q.is_cuda):
+        raise ValueError(f"{who}: a_q must be an int8 [m, k] CUDA tensor")
+    return (_need(who, "a_q", a_q, a_q.shape, torch.int8, a_q.device),
+            _need(who, "a_s", a_s, a_q.shape[:1], torch.float32, a_q.device))
+
+
+def mx_gemm_int8(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, out=None, stream=None):
+    """C [m, n] = A . B^T in 8-bit integers (mx_gemm_int8): a_q int8 [m, k] with
+    a_s fp32 [m] (a scale per token), b_q int8 [n, k] with b_s fp32 [n] (a scale
+    per channel), as mx_quantize_int8 makes them; bf16 or fp32."""
+    who = "mx_gemm_int8"
+    a, sa = _int8_rows(who, a_q, a_s)
+    if not (isinstance(b_q, torch.Tensor) and b_q.dim() == 2):
+        raise ValueError(f"{who}: b_q must be [n, k]")
+    (m, k), n, dev = a_q.shape, b_q.shape[0], a_q.device
+    b, sb = _need(who, "b_q", b_q, (n, k), torch.int8, dev), _need(who, "b_s", b_s, (n,), torch.float32, dev)
+    out, c, dt = _out_tensor(who, out, out_dtype, (m, n), dev, stream)
+    _call(load().mx_gemm_int8, dev, stream, a, sa, b, sb, m, n, k, c, dt)
+    return out
+
+
+def _sizes_arg(who, sizes, groups, rows, dev):
+    """Rows per group: (host array, device address), one of them None."""
+    if isinstance(sizes, torch.Tensor) and sizes.is_cuda:
+        return None, _need(who, "the sizes", sizes, (groups,), torch.int64, dev)
+    sizes = [int(v) for v in sizes]
+    if len(sizes) != groups or sum(sizes) != rows or (sizes and min(sizes) < 0):
+        raise ValueError(f"{who}: sizes {sizes} must be {groups} counts >= 0 that sum to {rows}")
+    return (ctypes.c_int64 * max(1, groups))(*sizes), None
+
+
+def mx_grouped_gemm_int8(a_q, a_s, b_q, b_s, group_sizes, out_dtype=torch.bfloat16, out=None, stream=None):
+    """Grouped mx_gemm_int8 over split_sizes: rows of group g of A (a_q int8
+    [M, k], a_s fp32 [M]) times B_g^T (b_q int8 [G, n, k], b_s fp32 [G, n]) -> C
+    [M, n]. group_sizes: a list that sums to M, or an int64 [G] CUDA tensor
+    (mx_moe_dispatch's counts), which is read on the device; rows of C behind its
+    last group are then not written."""
+    who = "mx_grouped_gemm_int8"
+    a, sa = _int8_rows(who, a_q, a_s)
+    if not (isinstance(b_q, torch.Tensor) and b_q.dim() == 3):
+        raise ValueError(f"{who}: b_q must be [G, n, k]")
+    (m, k), (G, n, _), dev = a_q.shape, b_q.shape, a_q.device
+    b, sb = _need(who, "b_q", b_q, (G, n, k), torch.int8, dev), _need(who, "b_s", b_s, (G, n), torch.float32, dev)
+    host, counts = _sizes_arg(who, group_sizes, G, m, dev)
+    out, c, dt = _out_tensor(who, out, out_dtype, (m, n), dev, stream)
+    if counts is None:
+        _call(load().mx_grouped_gemm_int8, dev, stream, a, sa, b, sb, host, _i32(G), m, n, k, c, dt)
+    else:
+        _call(load().mx_grouped_gemm_int8_device_split, dev, stream, a, sa, b, sb, counts, _i32(G), m, n, k, c, dt)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_mlp_dims(E, R, H, F):
+    """The dims of an int8 MLP call and its workspace's bytes."""
+    dims, nbytes = ctypes.byref(_Dims(_i32(E), R, H, F)), ctypes.c_size_t()
+    _check(load().grouped_mlp_int8_sizes(dims, ctypes.byref(nbytes)))
+    return dims, nbytes.value
+
+
+def mlp_int8_workspace_bytes(E: int, R: int, H: int, F: int) -> int:
+    """Bytes of the workspace of grouped_mlp_fwd_int8."""
+    return _int8_mlp_dims(E, R, H, F)[1]
+
+
+def grouped_mlp_fwd_int8(x, probs, w1, w1_s, w2, w2_s, split_sizes, *, row_token=None, out=None, workspace=None,
+                         stream=None):
+    """The MoE MLP for inference on int8 weights (grouped_mlp_fwd_int8): w1 int8
+    [E, 2F, H] and w2 [E, H, F] with scales w1_s fp32 [E, 2F] and w2_s [E, H], as
+    mx_quantize_int8 makes them; x bf16 [R, H] routed rows, or with row_token
+    int32 [R] (of mx_moe_dispatch) the tokens' rows [T, H]; probs fp32 [R] or
+    None. split_sizes: a list that sums to R, or mx_moe_dispatch's counts on the
+    device (rows of y behind the last expert's are then not written).
+    Returns y bf16 [R, H]; no autograd history."""
+    who = "grouped_mlp_fwd_int8"
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2 and x.is_cuda):
+        raise ValueError(f"{who}: x must be a 2-D CUDA tensor")
+    if not (isinstance(w1, torch.Tensor) and w1.dim() == 3):
+        raise ValueError(f"{who}: w1 must be [E, 2F, H]")
+    dev = x.device
+    T, H = x.shape
+    E, F2, _ = w1.shape
+    F = F2 // 2
+    R, idx = T, None
+    if row_token is not None:
+        if not (isinstance(row_token, torch.Tensor) and row_token.dim() == 1):
+            raise ValueError(f"{who}: row_token must be an int32 [R] tensor")
+        R = row_token.shape[0]
+        idx = _need(who, "row_token", row_token, (R,), torch.int32, dev)
+    host, counts = _sizes_arg(who, split_sizes, E, R, dev)
+    args = (_need(who, "x", x, (T, H), torch.bfloat16, dev), T, idx, _opt(who, "probs", probs, (R,), torch.float32, dev),
+            _need(who, "w1", w1, (E, 2 * F, H), torch.int8, dev), _need(who, "w1_s", w1_s, (E, 2 * F), torch.float32, dev),
+            _need(who, "w2", w2, (E, H, F), torch.int8, dev), _need(who, "w2_s", w2_s, (E, H), torch.float32, dev))
+    dims, nbytes = _int8_mlp_dims(E, R, H, F)
+    workspace = _scratch(who, workspace, nbytes, dev, stream)
+    if out is None:
+        out = _new((R, H), torch.bfloat16, dev, stream)
+        y = out.data_ptr()
+    else:
+        y = _need(who, "out", out, (R, H), torch.bfloat16, dev)
+    _call(load().grouped_mlp_fwd_int8, dev, stream, dims, host, counts, *args, y,
+          None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel())
+    return out
+
+
 _event_arrays = []   # keeps the handle arrays alive while the library holds them
 
 
@@ -1408,3 +1659,31 @@ class MoERoute(torch.autograd.Function):
     def backward(ctx, _, dw):
         logits, bias, idx, w, lse = ctx.saved_tensors
         return mx_moe_route_bwd(logits, idx, w, lse, dw.contiguous(), bias=bias, renormalize=ctx.renormalize), None, None, None
+
+
+class MoEBalance(torch.autograd.Function):
+    """loss, counts, mean_prob = MoEBalance.apply(logits, topk_idx, bias, segments):
+    the balance loss of a router's choices with the gradient of loss and mean_prob
+    for the logits (once: the gradient has none of its own). For a training step
+    that is captured into a graph the same holds as for MoERoute."""
+
+    @staticmethod
+    def forward(ctx, logits, topk_idx, bias=None, segments=None):
+        logits = logits.contiguous()
+        loss, counts, mean_prob = mx_moe_balance(logits, topk_idx.contiguous(), bias=bias, segments=segments)
+        ctx.save_for_backward(logits, bias, segments, counts)
+        ctx.topk = topk_idx.shape[1]
+        ctx.mark_non_differentiable(counts)
+        ctx.set_materialize_grads(False)
+        return loss, counts, mean_prob
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss, _, dmean_prob):
+        if dloss is None and dmean_prob is None:
+            return None, None, None, None
+        logits, bias, segments, counts = ctx.saved_tensors
+        dz = mx_moe_balance_bwd(logits, counts, ctx.topk, dloss=None if dloss is None else dloss.contiguous(),
+                                dmean_prob=None if dmean_prob is None else dmean_prob.contiguous(), bias=bias,
+                                segments=segments)
+        return dz, None, None, None

@@ -2040,3 +2040,286 @@ mx_status mx_moe_route_bwd(const void* logits, mx_dtype logits_dtype, const floa
 }
 
 }  // extern "C"
+
+namespace {
+
+mx_status balance_checks(const char* who, mx_dtype dt, int64_t tokens, int32_t E, int32_t topk, int32_t sequences,
+                         const int32_t* segments) {
+  mx_status st = route_checks(who, dt, tokens, E, topk);
+  if (st != MX_OK) return st;
+  if (sequences < 1 || (!segments && sequences != 1))
+    return fail(MX_ESHAPE, "%s: need at least one sequence, and exactly one without segments", who);
+  if (sequences > MX_MAX_SEQUENCES) return fail(MX_EUNSUPPORTED, "%s: %d sequences exceed the maximum %d", who, sequences, MX_MAX_SEQUENCES);
+  return MX_OK;
+}
+
+struct BalanceLayout {
+  size_t prob, count, total;
+  int parts;
+};
+BalanceLayout balance_layout(int64_t tokens, int32_t E, int32_t sequences) {
+  BalanceLayout L;
+  L.parts = mx::balance_parts(tokens, sequences);
+  const size_t n = L.parts > 1 ? (size_t)sequences * L.parts * E : 0;
+  size_t cur = 0;
+  L.prob = take(cur, n * 8);
+  L.count = take(cur, n * 4);
+  L.total = cur;
+  return L;
+}
+
+// Sizes and the group mode of an int8 product; the arrays are checked by the callers.
+constexpr int64_t kInt8MaxK = 131071;        // 2^14 k < 2^31: sums of products of -128 .. 127
+constexpr int64_t kInt8MaxDim = (int64_t)1 << 30;
+constexpr int64_t kInt8MaxRows = ((int64_t)1 << 24) - 1;   // of a cast: 256 threads a row
+
+mx_status int8_groups(const char* who, const int64_t* sizes, bool device, int32_t groups, int64_t m, mx::Int8GemmArgs* a) {
+  if (groups < 1) return fail(MX_EINVAL, "%s: need at least one group", who);
+  if (groups > mx::kMaxGroups) return fail(MX_EUNSUPPORTED, "%s: %d groups exceed the maximum %d", who, groups, mx::kMaxGroups);
+  if (m < 0) return fail(MX_ESHAPE, "%s: negative rows", who);
+  if (m > kInt8MaxDim) return fail(MX_EUNSUPPORTED, "%s: more than 2^30 rows", who);
+  if (!sizes) return fail(MX_EINVAL, "%s: null group sizes", who);
+  a->groups = groups;
+  a->M = (int32_t)m;
+  a->sizes_dev = device ? sizes : nullptr;
+  a->split = device ? mx::kInt8DeviceSizes : mx::kInt8HostSizes;
+  if (device) return aligned(sizes, 8) ? MX_OK : fail(MX_EALIGN, "%s: group sizes must be 8-byte aligned", who);
+  mx_status st = check_groups(sizes, groups, m, who);
+  if (st != MX_OK) return st;
+  for (int g = 0; g < groups; ++g) a->sizes[g] = (int32_t)sizes[g];
+  return MX_OK;
+}
+
+mx_status int8_shape(const char* who, int result, int64_t n, int64_t k, mx::Int8GemmArgs* a, mx::Int8Plan* plan) {
+  if (n < 0 || k <= 0 || k % 16) return fail(MX_ESHAPE, "%s: need n >= 0 and k a positive multiple of 16", who);
+  if (n > kInt8MaxDim || k > kInt8MaxK)
+    return fail(MX_EUNSUPPORTED, "%s: need n <= 2^30 and k <= %lld (sums of 32 bits)", who, (long long)kInt8MaxK);
+  a->N = (int32_t)n;
+  a->K = (int32_t)k;
+  *plan = mx::Int8Plan{};
+  if (a->M > 0 && n > 0) *plan = mx::plan_gemm_int8(result, *a);
+  if (plan->tiles > mx::kInt8MaxTiles) return fail(MX_EUNSUPPORTED, "%s: too many output tiles", who);
+  return MX_OK;
+}
+
+mx_status gemm_int8_impl(const char* who, const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
+                         mx::Int8GemmArgs* g, int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+  if (c_dtype != MX_BF16 && c_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad output dtype %d", who, (int)c_dtype);
+  const int result = c_dtype == MX_F32 ? mx::kInt8ToF32 : mx::kInt8ToBf16;
+  mx::Int8Plan plan;
+  mx_status st = int8_shape(who, result, n, k, g, &plan);
+  if (st != MX_OK) return st;
+  if (g->M == 0 || n == 0) return MX_OK;
+  if (!a || !a_s || !b || !b_s || !c) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(c, c_dtype == MX_F32 ? 4 : 2))
+    return fail(MX_EALIGN, "%s: a and b must be 16-byte aligned, scales and c to their elements", who);
+  g->a = a; g->a_s = a_s; g->b = b; g->b_s = b_s; g->c = c;
+  hipError_t e = mx::launch_gemm_int8(result, *g, plan, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+// The int8 MLP: the cast rows of X, the activations in fp32 and their cast.
+struct Int8MlpLayout {
+  size_t xq, xs, act, aq, as, total;
+};
+mx_status int8_mlp_layout(const char* who, const mx_mlp_dims* d, Int8MlpLayout* L) {
+  if (!d) return fail(MX_EINVAL, "%s: null dims", who);
+  if (d->num_experts < 1) return fail(MX_EINVAL, "%s: need at least one expert", who);
+  if (d->num_experts > mx::kMaxGroups)
+    return fail(MX_EUNSUPPORTED, "%s: %d experts exceeds the maximum %d", who, d->num_experts, mx::kMaxGroups);
+  if (d->rows < 0 || d->hidden <= 0 || d->hidden % 32 || d->ffn <= 0 || d->ffn % 32)
+    return fail(MX_ESHAPE, "%s: need rows >= 0, hidden and ffn positive multiples of 32", who);
+  if (d->rows > kInt8MaxRows || d->hidden > kInt8MaxK || d->ffn > kInt8MaxK)
+    return fail(MX_EUNSUPPORTED, "%s: need rows < 2^24, hidden and ffn <= %lld", who, (long long)kInt8MaxK);
+  size_t cur = 0;
+  L->xq = take(cur, (size_t)(d->rows * d->hidden));
+  L->xs = take(cur, (size_t)(d->rows * 4));
+  L->act = take(cur, (size_t)(d->rows * d->ffn * 4));
+  L->aq = take(cur, (size_t)(d->rows * d->ffn));
+  L->as = take(cur, (size_t)(d->rows * 4));
+  L->total = cur;
+  return MX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+mx_status mx_moe_balance_sizes(int64_t tokens, int32_t num_experts, int32_t sequences, size_t* workspace) {
+  g_err[0] = 0;
+  static const int32_t one[2] = {0, 0};
+  mx_status st = balance_checks("mx_moe_balance_sizes", MX_F32, tokens, num_experts, 1, sequences, one);
+  if (st != MX_OK) return st;
+  if (workspace) *workspace = balance_layout(tokens, num_experts, sequences).total;
+  return MX_OK;
+}
+
+mx_status mx_moe_balance(const void* logits, mx_dtype logits_dtype, const float* bias, const int32_t* topk_idx,
+                         const int32_t* segments, int32_t sequences, int64_t tokens, int32_t num_experts, int32_t topk,
+                         float* loss, int64_t* counts, float* mean_prob, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_moe_balance";
+  mx_status st = balance_checks(who, logits_dtype, tokens, num_experts, topk, sequences, segments);
+  if (st != MX_OK) return st;
+  if (!loss || !counts || !mean_prob || (tokens > 0 && (!logits || !topk_idx)))
+    return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(logits, logits_dtype == MX_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_idx, 4) ||
+      !aligned(segments, 4) || !aligned(loss, 4) || !aligned(counts, 8) || !aligned(mean_prob, 4))
+    return fail(MX_EALIGN, "%s: arrays must be aligned to their elements", who);
+  const BalanceLayout L = balance_layout(tokens, num_experts, sequences);
+  if (L.total > 0 && !workspace) return fail(MX_EINVAL, "%s: null workspace", who);
+  if (!aligned(workspace, 256)) return fail(MX_EALIGN, "%s: workspace must be 256-byte aligned", who);
+  if (workspace_bytes < L.total)
+    return fail(MX_EWORKSPACE, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, L.total);
+  mx::BalanceArgs a;
+  a.logits = logits; a.f32 = logits_dtype == MX_F32; a.bias = bias; a.topk_idx = topk_idx; a.segments = segments;
+  a.tokens = tokens; a.experts = num_experts; a.topk = topk; a.sequences = sequences; a.parts = L.parts;
+  a.part_prob = reinterpret_cast<double*>(reinterpret_cast<uint8_t*>(workspace) + L.prob);
+  a.part_count = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(workspace) + L.count);
+  a.loss = loss; a.counts = counts; a.mean_prob = mean_prob;
+  hipError_t e = mx::launch_balance(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+mx_status mx_moe_balance_bwd(const void* logits, mx_dtype logits_dtype, const float* bias, const int64_t* counts,
+                             const float* dloss, const float* dmean_prob, const int32_t* segments, int32_t sequences,
+                             int64_t tokens, int32_t num_experts, int32_t topk, const void* add, void* dlogits,
+                             void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_moe_balance_bwd";
+  mx_status st = balance_checks(who, logits_dtype, tokens, num_experts, topk, sequences, segments);
+  if (st != MX_OK) return st;
+  if (tokens == 0) return MX_OK;
+  if (!logits || !dlogits || (dloss && !counts)) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  const int el = logits_dtype == MX_F32 ? 4 : 2;
+  if (!aligned(logits, el) || !aligned(dlogits, el) || !aligned(add, el) || !aligned(bias, 4) || !aligned(counts, 8) ||
+      !aligned(dloss, 4) || !aligned(dmean_prob, 4) || !aligned(segments, 4))
+    return fail(MX_EALIGN, "%s: arrays must be aligned to their elements", who);
+  mx::BalanceBwdArgs a;
+  a.logits = logits; a.f32 = logits_dtype == MX_F32; a.bias = bias; a.counts = counts; a.dloss = dloss;
+  a.dmean_prob = dmean_prob; a.segments = segments; a.add = add; a.tokens = tokens; a.experts = num_experts;
+  a.topk = topk; a.sequences = sequences; a.dlogits = dlogits;
+  hipError_t e = mx::launch_balance_bwd(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_rows, int64_t cols, int64_t ldx,
+                           const int32_t* row_index, int64_t rows, const float* row_weight, int8_t* q, float* s,
+                           void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_quantize_int8";
+  if (x_dtype != MX_BF16 && x_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad dtype %d", who, (int)x_dtype);
+  if (x_rows < 0 || rows < 0 || (!row_index && rows != x_rows) || cols <= 0 || cols % 16)
+    return fail(MX_ESHAPE, "%s: need rows >= 0 (those of x without an index) and cols a positive multiple of 16", who);
+  const int64_t per = x_dtype == MX_F32 ? 4 : 8;             // values of 16 bytes
+  if (ldx % per || (x_rows > 1 && ldx < cols))
+    return fail(MX_ESHAPE, "%s: ldx %lld must be a multiple of %lld and at least cols", who, (long long)ldx, (long long)per);
+  if (rows > kInt8MaxRows || x_rows > kI32Max || cols > ((int64_t)1 << 24) || ldx > ((int64_t)1 << 24))
+    return fail(MX_EUNSUPPORTED, "%s: need rows < 2^24, rows of x below 2^31, cols and ldx <= 2^24", who);
+  if (rows == 0) return MX_OK;
+  if ((!x && x_rows > 0) || !q || !s) return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4) || !aligned(row_index, 4) || !aligned(row_weight, 4))
+    return fail(MX_EALIGN, "%s: x and q must be 16-byte aligned, the others to their elements", who);
+  mx::QuantInt8Args a;
+  a.x = x; a.f32 = x_dtype == MX_F32; a.rows = rows; a.cols = (int32_t)cols; a.ldx = ldx; a.row_index = row_index;
+  a.index_rows = x_rows; a.row_weight = row_weight; a.q = q; a.s = s;
+  hipError_t e = mx::launch_quantize_int8(a, reinterpret_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m, int64_t n,
+                       int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_gemm_int8";
+  mx::Int8GemmArgs g{};
+  mx_status st = int8_groups(who, &m, false, 1, m, &g);
+  if (st != MX_OK) return st;
+  g.split = mx::kInt8OneGroup;
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+}
+
+mx_status mx_grouped_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
+                               const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n, int64_t k, void* c,
+                               mx_dtype c_dtype, void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_grouped_gemm_int8";
+  mx::Int8GemmArgs g{};
+  mx_status st = int8_groups(who, group_sizes, false, groups, m, &g);
+  if (st != MX_OK) return st;
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+}
+
+mx_status mx_grouped_gemm_int8_device_split(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
+                                            const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n,
+                                            int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+  g_err[0] = 0;
+  const char* who = "mx_grouped_gemm_int8_device_split";
+  mx::Int8GemmArgs g{};
+  mx_status st = int8_groups(who, group_sizes, true, groups, m, &g);
+  if (st != MX_OK) return st;
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+}
+
+mx_status grouped_mlp_int8_sizes(const mx_mlp_dims* dims, size_t* workspace) {
+  g_err[0] = 0;
+  Int8MlpLayout L;
+  mx_status st = int8_mlp_layout("grouped_mlp_int8_sizes", dims, &L);
+  if (st != MX_OK) return st;
+  if (workspace) *workspace = L.total;
+  return MX_OK;
+}
+
+mx_status grouped_mlp_fwd_int8(const mx_mlp_dims* dims, const int64_t* split_sizes, const int64_t* split_sizes_dev,
+                               const void* x, int64_t tokens, const int32_t* row_token, const float* probs,
+                               const int8_t* w1, const float* w1_s, const int8_t* w2, const float* w2_s, void* y,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "grouped_mlp_fwd_int8";
+  Int8MlpLayout L;
+  mx_status st = int8_mlp_layout(who, dims, &L);
+  if (st != MX_OK) return st;
+  if ((split_sizes != nullptr) == (split_sizes_dev != nullptr))
+    return fail(MX_EINVAL, "%s: need split_sizes on the host or on the device, one of them", who);
+  const int64_t R = dims->rows, H = dims->hidden, F = dims->ffn;
+  mx::Int8GemmArgs g{};
+  st = int8_groups(who, split_sizes != nullptr ? split_sizes : split_sizes_dev, split_sizes == nullptr,
+                   dims->num_experts, R, &g);
+  if (st != MX_OK) return st;
+  mx::Int8GemmArgs g2 = g;
+  mx::Int8Plan p1, p2;
+  if ((st = int8_shape(who, mx::kInt8ToSwiglu, 2 * F, H, &g, &p1)) != MX_OK) return st;
+  if ((st = int8_shape(who, mx::kInt8ToBf16, H, F, &g2, &p2)) != MX_OK) return st;
+  if (tokens < 0) return fail(MX_ESHAPE, "%s: negative tokens", who);
+  if (tokens > kI32Max) return fail(MX_EUNSUPPORTED, "%s: need tokens below 2^31", who);
+  if (R == 0) return MX_OK;
+  const int64_t x_rows = row_token != nullptr ? tokens : R;
+  if ((!x && x_rows > 0) || !w1 || !w1_s || !w2 || !w2_s || !y || !workspace)
+    return fail(MX_EINVAL, "%s: null pointer argument", who);
+  if (!aligned(x, 16) || !aligned(w1, 16) || !aligned(w2, 16) || !aligned(y, 16) || !aligned(w1_s, 4) ||
+      !aligned(w2_s, 4) || !aligned(row_token, 4) || !aligned(probs, 4) || !aligned(workspace, 256))
+    return fail(MX_EALIGN, "%s: x, w1, w2 and y must be 16-byte, workspace 256-byte aligned, the others to their elements", who);
+  if (workspace_bytes < L.total)
+    return fail(MX_EWORKSPACE, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, L.total);
+  uint8_t* const ws = reinterpret_cast<uint8_t*>(workspace);
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  mx::QuantInt8Args q;
+  q.x = x; q.f32 = 0; q.rows = R; q.cols = (int32_t)H; q.ldx = H; q.row_index = row_token; q.index_rows = x_rows;
+  q.row_weight = nullptr; q.q = reinterpret_cast<int8_t*>(ws + L.xq); q.s = reinterpret_cast<float*>(ws + L.xs);
+  hipError_t e = mx::launch_quantize_int8(q, s);
+  if (e != hipSuccess) return hip_fail(e, who);
+  g.a = q.q; g.a_s = q.s; g.b = w1; g.b_s = w1_s; g.c = ws + L.act;
+  if ((e = mx::launch_gemm_int8(mx::kInt8ToSwiglu, g, p1, s)) != hipSuccess) return hip_fail(e, who);
+  q.x = ws + L.act; q.f32 = 1; q.cols = (int32_t)F; q.ldx = F; q.row_index = nullptr; q.index_rows = R;
+  q.row_weight = probs; q.q = reinterpret_cast<int8_t*>(ws + L.aq); q.s = reinterpret_cast<float*>(ws + L.as);
+  if ((e = mx::launch_quantize_int8(q, s)) != hipSuccess) return hip_fail(e, who);
+  g2.a = q.q; g2.a_s = q.s; g2.b = w2; g2.b_s = w2_s; g2.c = y;
+  if ((e = mx::launch_gemm_int8(mx::kInt8ToBf16, g2, p2, s)) != hipSuccess) return hip_fail(e, who);
+  return MX_OK;
+}
+
+}  // extern "C"

@@ -351,6 +351,81 @@ struct RouteBwdArgs {
 };
 hipError_t launch_route_bwd(const RouteBwdArgs& a, hipStream_t stream);
 
+// Balance loss of the router's choices over sequences of tokens (mx_route.hip).
+struct BalanceArgs {
+  const void* logits;               // bf16 or fp32 [tokens, experts]
+  int32_t f32;
+  const float* bias;                // [experts] or null
+  const int32_t* topk_idx;          // [tokens, topk]
+  const int32_t* segments;          // [sequences + 1] token offsets, or null (one sequence)
+  int64_t tokens;
+  int32_t experts, topk, sequences;
+  int32_t parts;                    // of balance_parts
+  double* part_prob;                // [sequences, parts, experts] (parts > 1)
+  int32_t* part_count;
+  float* loss;                      // [sequences]
+  int64_t* counts;                  // [sequences, experts]
+  float* mean_prob;                 // [sequences, experts]
+  int32_t vec;                      // as in RouteArgs
+};
+int balance_parts(int64_t tokens, int32_t sequences);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
+struct BalanceBwdArgs {
+  const void* logits;
+  int32_t f32;
+  const float* bias;
+  const int64_t* counts;            // [sequences, experts] (with dloss)
+  const float* dloss;               // [sequences] or null
+  const float* dmean_prob;          // [sequences, experts] or null
+  const int32_t* segments;
+  const void* add;                  // [tokens, experts] of the logits' type, or null
+  int64_t tokens;
+  int32_t experts, topk, sequences;
+  void* dlogits;                    // may be `add`
+  int32_t vec;                      // as in RouteArgs
+};
+hipError_t launch_balance_bwd(const BalanceBwdArgs& a, hipStream_t stream);
+
+// 8-bit integers with a scale per row (mx_int8.hip).
+struct QuantInt8Args {
+  const void* x;                    // bf16 or fp32, rows ldx values apart
+  int32_t f32;
+  int64_t rows;                     // rows made
+  int32_t cols;                     // a multiple of 16
+  int64_t ldx;
+  const int32_t* row_index;         // [rows]: the row of x of each row made, or null
+  int64_t index_rows;               // rows of x
+  const float* row_weight;          // [rows] factor of the scales, or null
+  int8_t* q;                        // [rows, cols]
+  float* s;                         // [rows]
+};
+hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream);
+// Groups of an int8 product: one of all rows, sizes in the arguments, or sizes
+// in device memory (clamped there: below 0 reads as 0, cut where the running sum
+// would pass M; rows behind the last group are left alone).
+enum Int8Split : int { kInt8OneGroup = 0, kInt8HostSizes = 1, kInt8DeviceSizes = 2 };
+struct Int8GemmArgs {
+  const int8_t* a;                  // [M, K]
+  const float* a_s;                 // [M]
+  const int8_t* b;                  // [groups, N, K]
+  const float* b_s;                 // [groups, N]
+  void* c;                          // [M, N]; SwiGLU: fp32 [M, N / 2]
+  int32_t M, N, K, groups, split;
+  const int64_t* sizes_dev;
+  int32_t sizes[kMaxGroups];
+  int32_t n_tiles;                  // set by the launch
+};
+enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2 };
+// How a product runs: the tile shape, and its workgroups (at most kInt8MaxTiles:
+// a launch has fewer than 2^32 threads along x).
+struct Int8Plan {
+  int32_t shape;
+  int64_t n_tiles, tiles;
+};
+constexpr int64_t kInt8MaxTiles = ((int64_t)1 << 24) - 1;
+Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a);
+hipError_t launch_gemm_int8(int result, const Int8GemmArgs& a, const Int8Plan& p, hipStream_t stream);
+
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 constexpr int kTileK = 128;

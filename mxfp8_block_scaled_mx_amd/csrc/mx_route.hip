@@ -17,6 +17,8 @@
 // TB/s), so what they save is latency: maxima and sums go over the lanes by DPP and
 // permlane moves (through LDS: 6.2 us for the 33 tokens), and the gradient's
 // picks are scattered through LDS (a loop over the picks in every lane: 8.0 us).
+#include <algorithm>
+
 #include "mx_device.h"
 #include "mx_internal.h"
 
@@ -76,6 +78,34 @@ __device__ __forceinline__ void load_values(const void* p, int64_t at, int left,
                    : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p)[at + i] << 16);
     }
   }
+}
+
+// The other way round: V values to element `at` of such a row.
+template <int V, bool F32>
+__device__ __forceinline__ void store_values(void* p, int64_t at, int left, bool vec, const float (&v)[V]) {
+  if (V == 4 && vec) {
+    if constexpr (F32) {
+      v4f o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i & 3] = v[i];
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(p) + at) = o;
+    } else {
+      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      bf16x4 o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i & 3] = (__bf16)v[i];
+      *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(p) + at) = o;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < left) {
+      if (F32)
+        reinterpret_cast<float*>(p)[at + i] = v[i];
+      else
+        reinterpret_cast<__bf16*>(p)[at + i] = (__bf16)v[i];
+    }
 }
 
 // The lane's V logits (experts at or past E are shut), and the keys that
@@ -203,30 +233,224 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
     if (!a.renorm && z[v] > kShut) dz[v] -= expf(z[v] - lse) * dot;
   }
   if (!live || e0 >= a.experts) return;
-  const int64_t at = t * a.experts + e0;
-  if (V == 4 && a.vec) {
-    if constexpr (F32) {
-      v4f o;
+  store_values<V, F32>(a.dlogits, t * a.experts + e0, a.experts - e0, a.vec, dz);
+}
+
+// ---- the balance loss
+//
+// For the tokens of one sequence (n of them, k choices each):
+//     c_e = choices that name expert e,   P_e = 1/n sum_t p_te,
+//     loss = E / (k n) sum_e c_e P_e
+// with p the softmax over the open experts, made again from the logits here (a
+// row sits in registers, so this costs two reductions and no memory). Its
+// gradient, and that of the means P themselves, is
+//     dz_te = p_te / n (A_e - sum_j p_tj A_j),   A_e = dloss E c_e / (k n) + dP_e.
+
+// The tokens [begin, end) of sequence s; offsets outside 0 .. tokens, or that
+// fall, are cut so that no token outside the arrays is named.
+struct Span {
+  int64_t begin, end;
+};
+__device__ __forceinline__ Span span_of(const int32_t* segments, int s, int64_t tokens) {
+  if (segments == nullptr) return Span{0, tokens};
+  const int64_t b = min(max((int64_t)segments[s], (int64_t)0), tokens);
+  return Span{b, min(max((int64_t)segments[s + 1], b), tokens)};
+}
+
+// The row's softmax over the open experts (0 for shut ones, and for all where
+// none is open).
+template <int G, int V>
+__device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) {
+  float zm = z[0];
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v & 3] = dz[v];
-      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.dlogits) + at) = o;
-    } else {
-      typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-      bf16x4 o;
+  for (int v = 1; v < V; ++v) zm = fmaxf(zm, z[v]);
+  zm = group_max<G>(zm);
+  float sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) o[v & 3] = (__bf16)dz[v];
-      *reinterpret_cast<bf16x4*>(reinterpret_cast<__bf16*>(a.dlogits) + at) = o;
-    }
-    return;
+  for (int v = 0; v < V; ++v) {
+    p[v] = z[v] > kShut ? expf(z[v] - zm) : 0.f;
+    sum += p[v];
+  }
+  sum = group_sum<G>(sum);
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[v] *= inv;
+}
+
+// What a sequence's sums make: counts, means and (by the first wave, in 64 bits)
+// the loss. prob and count are the sums in LDS.
+__device__ __forceinline__ void balance_results(const BalanceArgs& a, int s, int64_t n, const double* prob, const int* count) {
+  const double len = n > 0 ? (double)n : 1.0;
+  double part = 0.0;
+  for (int e = threadIdx.x; e < a.experts; e += blockDim.x) {
+    const int64_t at = (int64_t)s * a.experts + e;
+    a.counts[at] = count[e];
+    a.mean_prob[at] = (float)(prob[e] / len);
+  }
+  if (threadIdx.x < 64) {
+    for (int e = threadIdx.x; e < a.experts; e += 64) part += (double)count[e] * prob[e];
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) part += __shfl_xor(part, m, 64);
+    if (threadIdx.x == 0) a.loss[s] = (float)(part * a.experts / ((double)a.topk * len * len));
+  }
+}
+
+// Part blockIdx.x of sequence blockIdx.y: sums over its tokens, straight to the
+// results where a sequence is one part, else to the workspace. The sums are kept
+// in 64 bits: in 32 they would stand still past 2^24 tokens, and the few adds a
+// token hide behind its loads.
+template <int G, int V, bool F32>
+__global__ __launch_bounds__(256) void balance_kernel(BalanceArgs a) {
+  constexpr int N = 256 / G;                              // tokens at a time
+  __shared__ double probs[N][G * V];
+  __shared__ double prob[G * V];
+  __shared__ int count[G * V];
+  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y, tid = threadIdx.x;
+  const Span sp = span_of(a.segments, s, a.tokens);
+  const int64_t n = sp.end - sp.begin, parts = gridDim.x;
+  const int64_t t0 = sp.begin + n * blockIdx.x / parts, t1 = sp.begin + n * (blockIdx.x + 1) / parts;
+  if (tid < G * V) count[tid] = 0;
+  __syncthreads();
+  for (int64_t i = t0 * a.topk + tid; i < t1 * a.topk; i += 256) {
+    const int e = a.topk_idx[i];
+    if (e >= 0 && e < a.experts) atomicAdd(&count[e], 1); // integers: any order gives the same sum
+  }
+  double acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.0;
+  for (int64_t t = t0 + tid / G; t < t1; t += N) {
+    float z[V], key[V], p[V];
+    load_row<V, F32>(a.logits, a.bias, t, a.experts, e0, a.vec, z, key);
+    row_softmax<G, V>(z, p);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] += (double)p[v];
   }
 #pragma unroll
-  for (int v = 0; v < V; ++v)
-    if (e0 + v < a.experts) {
-      if (F32)
-        reinterpret_cast<float*>(a.dlogits)[at + v] = dz[v];
-      else
-        reinterpret_cast<__bf16*>(a.dlogits)[at + v] = (__bf16)dz[v];
+  for (int v = 0; v < V; ++v) probs[tid / G][e0 + v] = acc[v];
+  __syncthreads();
+  if (tid < G * V) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += probs[i][tid];
+    prob[tid] = sum;
+  }
+  __syncthreads();
+  if (parts == 1) {
+    balance_results(a, s, n, prob, count);
+  } else if (tid < a.experts) {
+    const int64_t at = ((int64_t)s * parts + blockIdx.x) * a.experts + tid;
+    a.part_prob[at] = prob[tid];
+    a.part_count[at] = count[tid];
+  }
+}
+
+// The parts of sequence blockIdx.x added up in order, 8 strands of them at once.
+__global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a) {
+  __shared__ double probs[8][128];
+  __shared__ int counts[8][128];
+  __shared__ double prob[128];
+  __shared__ int count[128];
+  const int e = threadIdx.x & 127, strand = threadIdx.x >> 7, s = blockIdx.x;
+  double ps = 0.0;
+  int cs = 0;
+  if (e < a.experts) {
+    const int64_t base = (int64_t)s * a.parts * a.experts + e;
+#pragma unroll 8
+    for (int i = strand; i < a.parts; i += 8) {
+      ps += a.part_prob[base + (int64_t)i * a.experts];
+      cs += a.part_count[base + (int64_t)i * a.experts];
     }
+  }
+  probs[strand][e] = ps;
+  counts[strand][e] = cs;
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    double sum = 0.0;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum += probs[i][e];
+      c += counts[i][e];
+    }
+    prob[e] = sum;
+    count[e] = c;
+  }
+  __syncthreads();
+  const Span sp = span_of(a.segments, s, a.tokens);
+  balance_results(a, s, sp.end - sp.begin, prob, count);
+}
+
+// Part blockIdx.x of sequence blockIdx.y; the last blockIdx.y of a call with
+// offsets takes the tokens before the first sequence and behind the last, whose
+// gradient is `add` alone.
+// A is made once a workgroup, in 64 bits, less its mean over the experts: since
+// the p of a row sum to 1 the gradient does not see the shift, and the
+// difference A_e - sum p A loses fewer bits.
+template <int G, int V, bool F32>
+__global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
+  constexpr int N = 256 / G;
+  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y;
+  const bool gap = s >= a.sequences;
+  Span sp;
+  int64_t n, skip = 0, skip_at = 0;                       // the gap: token u, or past skip_at, u + skip
+  if (gap) {
+    const int64_t first = min(max((int64_t)a.segments[0], (int64_t)0), a.tokens);
+    const int64_t last = min(max((int64_t)a.segments[a.sequences], first), a.tokens);
+    sp = Span{0, first + a.tokens - last};
+    skip_at = first;
+    skip = last - first;
+    n = sp.end;
+  } else {
+    sp = span_of(a.segments, s, a.tokens);
+    n = sp.end - sp.begin;
+    skip_at = a.tokens;
+  }
+  const int64_t u0 = sp.begin + n * blockIdx.x / gridDim.x, u1 = sp.begin + n * (blockIdx.x + 1) / gridDim.x;
+  if (u0 >= u1) return;
+  float A[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) A[v] = 0.f;
+  if (!gap) {
+    double w[V], sum = 0.0;
+    const double f = a.dloss != nullptr ? (double)a.dloss[s] * a.experts / ((double)a.topk * (double)n) : 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      w[v] = 0.0;
+      if (e0 + v < a.experts) {
+        const int64_t at = (int64_t)s * a.experts + e0 + v;
+        if (a.dloss != nullptr) w[v] = f * (double)a.counts[at];
+        if (a.dmean_prob != nullptr) w[v] += (double)a.dmean_prob[at];
+      }
+      sum += w[v];
+    }
+    const double mean = (double)(group_sum<G>((float)sum) / (float)a.experts);
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = e0 + v < a.experts ? (float)((w[v] - mean) / (double)n) : 0.f;
+  }
+  // whole passes of N tokens, so that every lane takes part in the reductions
+  for (int64_t u = u0; u < u1; u += N) {
+    const int64_t mine = u + threadIdx.x / G;
+    const bool live = mine < u1;
+    const int64_t uc = live ? mine : u1 - 1;
+    const int64_t t = uc < skip_at ? uc : uc + skip;
+    float z[V], key[V], p[V], base[V];
+    if (!gap) {
+      load_row<V, F32>(a.logits, a.bias, t, a.experts, e0, a.vec, z, key);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) base[v] = 0.f;
+    if (a.add != nullptr && e0 < a.experts) load_values<V, F32>(a.add, t * a.experts + e0, a.experts - e0, a.vec, base);
+    if (!gap) {
+      row_softmax<G, V>(z, p);
+      float dot = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v) dot += p[v] * A[v];
+      dot = group_sum<G>(dot);
+#pragma unroll
+      for (int v = 0; v < V; ++v) base[v] += p[v] * (A[v] - dot);
+    }
+    if (live && e0 < a.experts) store_values<V, F32>(a.dlogits, t * a.experts + e0, a.experts - e0, a.vec, base);
+  }
 }
 
 // Whether rows of `experts` values can be read and written four at a time.
@@ -275,6 +499,49 @@ hipError_t launch_route_bwd(const RouteBwdArgs& args, hipStream_t stream) {
       hipLaunchKernelGGL((route_bwd_kernel<G, V, true>), grid, dim3(256), 0, stream, a);
     else
       hipLaunchKernelGGL((route_bwd_kernel<G, V, false>), grid, dim3(256), 0, stream, a);
+  });
+  return hipGetLastError();
+}
+
+// Parts of a sequence: enough for two workgroups a compute unit where sequences
+// are equally long, at least 64 tokens each if one holds them all, and no more
+// than 16384 (the sequences' lengths are not known here, and one may hold nearly
+// all tokens) as long as that takes at most 4096 workgroups.
+int balance_parts(int64_t tokens, int32_t sequences) {
+  const auto cdiv = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  const int64_t parts = std::max(cdiv(512, sequences), std::min(cdiv(tokens, 16384), cdiv(4096, sequences)));
+  return (int)std::max<int64_t>(1, std::min(cdiv(tokens, 64), parts));
+}
+
+hipError_t launch_balance(const BalanceArgs& args, hipStream_t stream) {
+  BalanceArgs a = args;
+  a.vec = by_fours(a.experts, a.f32, a.logits);
+  by_shape(a.experts, [&](auto g_, auto v_) {
+    constexpr int G = decltype(g_)::value, V = decltype(v_)::value;
+    const dim3 grid((unsigned)a.parts, (unsigned)a.sequences);
+    if (a.f32)
+      hipLaunchKernelGGL((balance_kernel<G, V, true>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((balance_kernel<G, V, false>), grid, dim3(256), 0, stream, a);
+  });
+  if (a.parts > 1)
+    hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)a.sequences), dim3(1024), 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_bwd(const BalanceBwdArgs& args, hipStream_t stream) {
+  BalanceBwdArgs a = args;
+  a.vec = by_fours(a.experts, a.f32, a.logits) && by_fours(a.experts, a.f32, a.dlogits) &&
+          by_fours(a.experts, a.f32, a.add);
+  const int rows = a.sequences + (a.segments != nullptr ? 1 : 0);
+  by_shape(a.experts, [&](auto g_, auto v_) {
+    constexpr int G = decltype(g_)::value, V = decltype(v_)::value, per = 256 / G;
+    const int64_t parts = std::max<int64_t>(1, std::min((a.tokens + per - 1) / per, (int64_t)((2048 + rows - 1) / rows)));
+    const dim3 grid((unsigned)parts, (unsigned)rows);
+    if (a.f32)
+      hipLaunchKernelGGL((balance_bwd_kernel<G, V, true>), grid, dim3(256), 0, stream, a);
+    else
+      hipLaunchKernelGGL((balance_bwd_kernel<G, V, false>), grid, dim3(256), 0, stream, a);
   });
   return hipGetLastError();
 }
