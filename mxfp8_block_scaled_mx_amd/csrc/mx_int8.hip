@@ -321,6 +321,202 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a)
 #endif
 }
 
+// As vgpr_hop, for the integer sums.
+__device__ __forceinline__ int hop(int x) { return __builtin_amdgcn_mov_dpp(x, 0xE4, 0xF, 0xF, false); }
+
+// The tile of 256 x 256 for many rows: four waves of 128 x 128, one a SIMD, so
+// that the 256 sums of a lane have their registers. The stages and their swizzle
+// are those of the kernel above; what differs is the order of things. A step of
+// 128 k is four substeps of 32. In each, the fragments of the next substep are
+// read while the products of this one run, and the last one begins with the
+// barrier: by then every wave holds its last fragments of the stage, so the loads
+// of the step after next go into it at once, and have nearly a whole step to
+// land, while the first fragments of the next stage are read behind the last
+// products of this one. So neither the barrier nor a fragment's latency leaves the
+// matrix cores idle.
+// The MFMA takes B first: a lane holds one row m and runs of 4 columns n, which
+// go through LDS (16-byte chunk c of row r at c ^ (r & 15)) and leave as whole
+// cache lines.
+template <int EPI>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_int8_big_kernel(Int8GemmArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool kPair = EPI == kInt8ToSwiglu;
+  constexpr int BM = 256, BN = 256;
+  __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sA1[BM * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sB0[BN * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sB1[BN * kBK];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, l32 = lane & 31;
+  const int ntn = a.n_tiles;
+  GroupSpan g;
+  const int64_t id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  if (!find_group<BM>(a, id / ntn, &g)) return;
+  const int local = (int)(id - (int64_t)g.tile0 * ntn);
+  // bands of 8 m-tiles: the 32 tiles that run at once on one XCD are 8 x 4
+  const int band = local / (8 * ntn), in_band = local - band * 8 * ntn, height = min(8, g.tiles - 8 * band);
+  const int mt = 8 * band + in_band % height, nt = in_band / height;
+  const int64_t row0 = g.row0 + (int64_t)mt * BM;
+  const int rows = min(BM, g.rows - mt * BM);
+  const int K = a.K, nk = __builtin_amdgcn_readfirstlane((K + kBK - 1) / kBK);
+  const int nrows = kPair ? a.N / 2 : a.N;
+  constexpr int kTileRows = kPair ? BN / 2 : BN;
+  const int n0 = nt * kTileRows, ncols = min(kTileRows, nrows - n0);
+  const int8_t* const bg = a.b + (int64_t)g.group * a.N * K;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.a + row0 * K, (int64_t)rows * K);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(bg + (int64_t)n0 * K, (int64_t)ncols * K);
+  const __amdgpu_buffer_rsrc_t ru = make_rsrc(bg + (int64_t)(nrows + n0) * K, kPair ? (int64_t)ncols * K : 0);
+  const int lch = (lane & 7) ^ (lane >> 4) ^ (4 * (wave & 1));
+  const uint32_t voff = (uint32_t)(lane >> 3) * K + lch * 16;
+  // Block p of this wave's eight of A and of B of step kt. Steps past the last
+  // are out of bounds for every lane: zeros, and no memory is read.
+  auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
+    const int k0 = __builtin_amdgcn_readfirstlane(kt * kBK);
+    const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u, va = k0 < K ? voff : 0x80000000u;
+    const int blk = 4 * p + wave;
+    const uint32_t so = (uint32_t)(8 * blk) * K + k0;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, va, so, 0, 0);
+    if constexpr (kPair) {
+      const uint32_t sp = (uint32_t)((p / 2) * 32 + 8 * wave) * K + k0;    // 32-row block p: gate and up in turn
+      if (p & 1)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, sp, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, sp, 0, 0);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
+    }
+  };
+  v16i acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+  v4i fa[2][4], fb[2][4];
+  const int sw = (l32 >> 1) & 7;               // of every row 32 x + l32
+  auto frag = [&](const uint8_t* base, int r32, int ks) __attribute__((always_inline)) -> v4i {
+    return *reinterpret_cast<const v4i*>(base + (r32 * 32 + l32) * kBK + (((2 * ks + h) ^ sw) << 4));
+  };
+  // Step kt from stage (cA, cB); (nA, nB) holds step kt + 1. Half of a step's blocks
+  // are loaded in the last substep of the step two before, half in the next one.
+  auto step = [&](int kt, uint8_t* cA, uint8_t* cB, uint8_t* nA, uint8_t* nB) __attribute__((always_inline)) {
+    static_for<0, 4>([&](auto ks_) __attribute__((always_inline)) {
+      constexpr int ks = decltype(ks_)::value, cur = ks & 1, nxt = cur ^ 1;
+      if constexpr (ks == 3) {
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+        __syncthreads();
+      }
+      static_for<0, 4>([&](auto i_) __attribute__((always_inline)) {
+        constexpr int i = decltype(i_)::value;
+        const uint8_t* const rA = ks == 3 ? nA : cA;
+        const uint8_t* const rB = ks == 3 ? nB : cB;
+        constexpr int ns = (ks + 1) & 3;
+        if constexpr (i < 2) {
+          fb[nxt][2 * i] = frag(rB, wn * 4 + 2 * i, ns);
+          fb[nxt][2 * i + 1] = frag(rB, wn * 4 + 2 * i + 1, ns);
+        } else {
+          fa[nxt][2 * i - 4] = frag(rA, wm * 4 + 2 * i - 4, ns);
+          fa[nxt][2 * i - 3] = frag(rA, wm * 4 + 2 * i - 3, ns);
+        }
+        if constexpr (ks == 3) load(kt + 2, cA, cB, i);
+        if constexpr (ks == 0) load(kt + 1, nA, nB, 4 + i);
+        static_for<0, 4>([&](auto j_) __attribute__((always_inline)) {
+          constexpr int j = decltype(j_)::value;
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+    });
+  };
+#pragma unroll
+  for (int p = 0; p < 8; ++p) load(0, sA0, sB0, p);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) load(1, sA1, sB1, p);
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    fb[0][x] = frag(sB0, wn * 4 + x, 0);
+    fa[0][x] = frag(sA0, wm * 4 + x, 0);
+  }
+  int kt = 0;
+  for (; kt + 1 < nk; kt += 2) {
+    step(kt, sA0, sB0, sA1, sB1);
+    step(kt + 1, sA1, sB1, sA0, sB0);
+  }
+  if (kt < nk) step(kt, sA0, sB0, sA1, sB1);
+  // Sums to results. Lane: row 32 i + l32 of the wave's 128, columns 32 j + 8 q +
+  // 4 h + 0 .. 3 of its 128; by 32 rows through the wave's own 16 KiB of LDS.
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+  uint8_t* const stage = (wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1);
+  constexpr int kBytes = EPI == kInt8ToBf16 ? 2 : 4, kCols = kPair ? 64 : 128, kRowBytes = kCols * kBytes;
+  constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes;
+  const int cn0 = n0 + wn * kCols;             // the wave's first column of C
+  const int64_t ldc = nrows;
+  const float* const bs = a.b_s + (int64_t)g.group * a.N;
+  const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m0 = wm * 128 + 32 * i;
+    if (m0 >= rows) break;
+    const float sa = a.a_s[row0 + min(m0 + l32, rows - 1)];
+#pragma unroll
+    for (int j = 0; j < 4; j += kPair ? 2 : 1) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = 32 * (kPair ? j / 2 : j) + 8 * q + 4 * h;
+        float y[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int n = min(cn0 + col + v, nrows - 1);
+          y[v] = (float)hop(acc[i][j][4 * q + v]) * sa * bs[n];
+          if constexpr (kPair) {
+            const float up = (float)hop(acc[i][j + 1][4 * q + v]) * sa * bs[nrows + n];
+            y[v] = y[v] / (1.f + __expf(-y[v])) * up;
+          }
+        }
+        const int chunk = col / kPer;
+        uint8_t* const at = stage + l32 * kRowBytes + ((chunk ^ (l32 & (kChunks - 1) & 15)) << 4);
+        if constexpr (kBytes == 4) {
+          *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+        } else {
+          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+        }
+      }
+    }
+    // the wave's own LDS: its writes are done before its reads (no barrier)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < 32 * kChunks / 64; ++u) {
+        const int r = (u * 64 + lane) / kChunks, c = (u * 64 + lane) % kChunks, n = cn0 + c * kPer;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((c ^ (r & (kChunks - 1) & 15)) << 4));
+        if (m0 + r < rows && n < nrows)
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.c) + ((row0 + m0 + r) * ldc + n) * kBytes) = w;
+      }
+    } else {
+      for (int u = lane; u < 32 * kCols; u += 64) {
+        const int r = u / kCols, c = u % kCols, n = cn0 + c;
+        const uint8_t* const from = stage + r * kRowBytes + (((c / kPer) ^ (r & (kChunks - 1) & 15)) << 4) + c % kPer * kBytes;
+        if (m0 + r < rows && n < nrows) {
+          const int64_t at = (row0 + m0 + r) * ldc + n;
+          if constexpr (kBytes == 4) reinterpret_cast<float*>(a.c)[at] = *reinterpret_cast<const float*>(from);
+          else reinterpret_cast<uint16_t*>(a.c)[at] = *reinterpret_cast<const uint16_t*>(from);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+#endif
+}
+
 template <int WM, int WN, int MI, int NI>
 struct Shape {
   static constexpr int kWM = WM, kWN = WN, kMI = MI, kNI = NI, kBM = 32 * MI * WM, kBN = 32 * NI * WN;
@@ -386,7 +582,14 @@ hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan
     using S = decltype(s);
     constexpr int WM = S::kWM, WN = S::kWN, MI = S::kMI, NI = S::kNI;
     const dim3 grid((unsigned)p.tiles), block(64 * WM * WN);
-    if (result == kInt8ToBf16)
+    if constexpr (S::kBM == 256) {
+      if (result == kInt8ToBf16)
+        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToBf16>), grid, block, 0, stream, a);
+      else if (result == kInt8ToF32)
+        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToF32>), grid, block, 0, stream, a);
+      else
+        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToSwiglu>), grid, block, 0, stream, a);
+    } else if (result == kInt8ToBf16)
       hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, MI, NI, kInt8ToBf16>), grid, block, 0, stream, a);
     else if (result == kInt8ToF32)
       hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, MI, NI, kInt8ToF32>), grid, block, 0, stream, a);
