@@ -924,9 +924,11 @@ MX_API mx_status mx_moe_balance_bwd(const void* logits, mx_dtype logits_dtype, c
  *           running sum past m is cut there, and rows of C behind the last group
  *           are not written.
  *   c       [m, n] row-major, bf16 (rounded to nearest even) or fp32.
+ *   workspace  mx_gemm_int8_sizes bytes (groups 1 for mx_gemm_int8; 0 for many
+ *           shapes, then it may be NULL), 256-byte aligned.
  * m or n zero is a no-op. Errors: MX_EINVAL (null pointers, dtype, groups < 1),
  * MX_ESHAPE (negative sizes, k not a positive multiple of 16), MX_EALIGN (a, b
- * 16-byte, others by element), MX_EUNSUPPORTED (groups > MX_MAX_GROUPS, m or n >
+ * 16-byte, others by element), MX_EWORKSPACE, MX_EUNSUPPORTED (groups > MX_MAX_GROUPS, m or n >
  * 2^30, k > 131071, too many tiles), MX_EHIP.
  *
  * grouped_mlp_fwd_int8 -- the MoE MLP (article item 3) for inference on int8
@@ -944,20 +946,23 @@ MX_API mx_status mx_moe_balance_bwd(const void* logits, mx_dtype logits_dtype, c
  *   w2, w2_s     int8 [E, H, F], f32 [E, H].
  *   y            bf16 [rows, H], rounded once.
  *   workspace    grouped_mlp_int8_sizes bytes, 256-byte aligned.
- * Errors as above, and MX_EWORKSPACE.
+ * Errors as above.
  */
 MX_API mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_rows, int64_t cols, int64_t ldx,
                                   const int32_t* row_index, int64_t rows, const float* row_weight, int8_t* q,
                                   float* s, void* stream);
+MX_API mx_status mx_gemm_int8_sizes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t* workspace);
 MX_API mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m,
-                              int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* stream);
+                              int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream);
 MX_API mx_status mx_grouped_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
                                       const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n, int64_t k,
-                                      void* c, mx_dtype c_dtype, void* stream);
+                                      void* c, mx_dtype c_dtype, void* workspace, size_t workspace_bytes,
+                                      void* stream);
 MX_API mx_status mx_grouped_gemm_int8_device_split(const int8_t* a, const float* a_s, const int8_t* b,
                                                    const float* b_s, const int64_t* group_sizes, int32_t groups,
                                                    int64_t m, int64_t n, int64_t k, void* c, mx_dtype c_dtype,
-                                                   void* stream);
+                                                   void* workspace, size_t workspace_bytes, void* stream);
 MX_API mx_status grouped_mlp_int8_sizes(const mx_mlp_dims* dims, size_t* workspace);
 MX_API mx_status grouped_mlp_fwd_int8(const mx_mlp_dims* dims, const int64_t* split_sizes,
                                       const int64_t* split_sizes_dev, const void* x, int64_t tokens,

@@ -35,7 +35,7 @@ __all__ = [
     "mx_gemv_fp4", "mx_gemv_nvfp4", "gemv_workspace_bytes", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
     "mx_moe_route", "mx_moe_route_bwd", "MoERoute", "mx_moe_balance", "mx_moe_balance_bwd", "MoEBalance",
     "moe_balance_workspace_bytes", "mx_quantize_int8", "mx_gemm_int8", "mx_grouped_gemm_int8", "grouped_mlp_fwd_int8",
-    "mlp_int8_workspace_bytes",
+    "gemm_int8_workspace_bytes", "mlp_int8_workspace_bytes",
 ]
 
 FWD_STAGES = ("quantize_x", "quantize_w1", "quantize_w2", "gemm1_swiglu", "gemm2")
@@ -188,12 +188,14 @@ def load() -> ctypes.CDLL:
     L.mx_moe_balance_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, i64, i32, i32, vp, vp, vp]
     L.mx_quantize_int8.restype = ctypes.c_int
     L.mx_quantize_int8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp]
+    L.mx_gemm_int8_sizes.restype = ctypes.c_int
+    L.mx_gemm_int8_sizes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(sz)]
     L.mx_gemm_int8.restype = ctypes.c_int
-    L.mx_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]
+    L.mx_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp, sz, vp]
     L.mx_grouped_gemm_int8.restype = ctypes.c_int
-    L.mx_grouped_gemm_int8.argtypes = [vp, vp, vp, vp, p64, i32, i64, i64, i64, vp, i32, vp]
+    L.mx_grouped_gemm_int8.argtypes = [vp, vp, vp, vp, p64, i32, i64, i64, i64, vp, i32, vp, sz, vp]
     L.mx_grouped_gemm_int8_device_split.restype = ctypes.c_int
-    L.mx_grouped_gemm_int8_device_split.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i32, vp]
+    L.mx_grouped_gemm_int8_device_split.argtypes = [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, i32, vp, sz, vp]
     L.grouped_mlp_int8_sizes.restype = ctypes.c_int
     L.grouped_mlp_int8_sizes.argtypes = [ctypes.POINTER(_Dims), ctypes.POINTER(sz)]
     L.grouped_mlp_fwd_int8.restype = ctypes.c_int
@@ -1337,18 +1339,35 @@ def _int8_rows(who, a_q, a_s):
             _need(who, "a_s", a_s, a_q.shape[:1], torch.float32, a_q.device))
 
 
-def mx_gemm_int8(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, out=None, stream=None):
+@functools.lru_cache(maxsize=4096)
+def gemm_int8_workspace_bytes(m: int, n: int, k: int, groups: int = 1) -> int:
+    """Bytes of the workspace of mx_gemm_int8 and mx_grouped_gemm_int8 (0: none)."""
+    nbytes = ctypes.c_size_t()
+    _check(load().mx_gemm_int8_sizes(m, n, k, _i32(groups), ctypes.byref(nbytes)))
+    return nbytes.value
+
+
+def _int8_scratch(who, workspace, nbytes, dev, stream):
+    """(workspace, its address, its bytes); none is held where none is needed."""
+    if nbytes or workspace is not None:
+        workspace = _scratch(who, workspace, nbytes, dev, stream)
+    return workspace, None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel()
+
+
+def mx_gemm_int8(a_q, a_s, b_q, b_s, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """C [m, n] = A . B^T in 8-bit integers (mx_gemm_int8): a_q int8 [m, k] with
     a_s fp32 [m] (a scale per token), b_q int8 [n, k] with b_s fp32 [n] (a scale
-    per channel), as mx_quantize_int8 makes them; bf16 or fp32."""
+    per channel), as mx_quantize_int8 makes them; bf16 or fp32.
+    workspace: uint8, gemm_int8_workspace_bytes(m, n, k) (allocated when None)."""
     who = "mx_gemm_int8"
     a, sa = _int8_rows(who, a_q, a_s)
     if not (isinstance(b_q, torch.Tensor) and b_q.dim() == 2):
         raise ValueError(f"{who}: b_q must be [n, k]")
     (m, k), n, dev = a_q.shape, b_q.shape[0], a_q.device
     b, sb = _need(who, "b_q", b_q, (n, k), torch.int8, dev), _need(who, "b_s", b_s, (n,), torch.float32, dev)
+    workspace, ws, nbytes = _int8_scratch(who, workspace, gemm_int8_workspace_bytes(m, n, k), dev, stream)
     out, c, dt = _out_tensor(who, out, out_dtype, (m, n), dev, stream)
-    _call(load().mx_gemm_int8, dev, stream, a, sa, b, sb, m, n, k, c, dt)
+    _call(load().mx_gemm_int8, dev, stream, a, sa, b, sb, m, n, k, c, dt, ws, nbytes)
     return out
 
 
@@ -1362,12 +1381,13 @@ def _sizes_arg(who, sizes, groups, rows, dev):
     return (ctypes.c_int64 * max(1, groups))(*sizes), None
 
 
-def mx_grouped_gemm_int8(a_q, a_s, b_q, b_s, group_sizes, out_dtype=torch.bfloat16, out=None, stream=None):
+def mx_grouped_gemm_int8(a_q, a_s, b_q, b_s, group_sizes, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """Grouped mx_gemm_int8 over split_sizes: rows of group g of A (a_q int8
     [M, k], a_s fp32 [M]) times B_g^T (b_q int8 [G, n, k], b_s fp32 [G, n]) -> C
     [M, n]. group_sizes: a list that sums to M, or an int64 [G] CUDA tensor
     (mx_moe_dispatch's counts), which is read on the device; rows of C behind its
-    last group are then not written."""
+    last group are then not written. workspace: uint8, gemm_int8_workspace_bytes(M,
+    n, k, G) (allocated when None)."""
     who = "mx_grouped_gemm_int8"
     a, sa = _int8_rows(who, a_q, a_s)
     if not (isinstance(b_q, torch.Tensor) and b_q.dim() == 3):
@@ -1375,11 +1395,13 @@ def mx_grouped_gemm_int8(a_q, a_s, b_q, b_s, group_sizes, out_dtype=torch.bfloat
     (m, k), (G, n, _), dev = a_q.shape, b_q.shape, a_q.device
     b, sb = _need(who, "b_q", b_q, (G, n, k), torch.int8, dev), _need(who, "b_s", b_s, (G, n), torch.float32, dev)
     host, counts = _sizes_arg(who, group_sizes, G, m, dev)
+    workspace, ws, nbytes = _int8_scratch(who, workspace, gemm_int8_workspace_bytes(m, n, k, G), dev, stream)
     out, c, dt = _out_tensor(who, out, out_dtype, (m, n), dev, stream)
     if counts is None:
-        _call(load().mx_grouped_gemm_int8, dev, stream, a, sa, b, sb, host, _i32(G), m, n, k, c, dt)
+        _call(load().mx_grouped_gemm_int8, dev, stream, a, sa, b, sb, host, _i32(G), m, n, k, c, dt, ws, nbytes)
     else:
-        _call(load().mx_grouped_gemm_int8_device_split, dev, stream, a, sa, b, sb, counts, _i32(G), m, n, k, c, dt)
+        _call(load().mx_grouped_gemm_int8_device_split, dev, stream, a, sa, b, sb, counts, _i32(G), m, n, k, c, dt, ws,
+              nbytes)
     return out
 
 

@@ -2098,12 +2098,13 @@ mx_status int8_shape(const char* who, int result, int64_t n, int64_t k, mx::Int8
   a->K = (int32_t)k;
   *plan = mx::Int8Plan{};
   if (a->M > 0 && n > 0) *plan = mx::plan_gemm_int8(result, *a);
-  if (plan->tiles > mx::kInt8MaxTiles) return fail(MX_EUNSUPPORTED, "%s: too many output tiles", who);
+  if (plan->tiles * plan->parts > mx::kInt8MaxTiles) return fail(MX_EUNSUPPORTED, "%s: too many output tiles", who);
   return MX_OK;
 }
 
 mx_status gemm_int8_impl(const char* who, const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
-                         mx::Int8GemmArgs* g, int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+                         mx::Int8GemmArgs* g, int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* workspace,
+                         size_t workspace_bytes, void* stream) {
   if (c_dtype != MX_BF16 && c_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad output dtype %d", who, (int)c_dtype);
   const int result = c_dtype == MX_F32 ? mx::kInt8ToF32 : mx::kInt8ToBf16;
   mx::Int8Plan plan;
@@ -2113,15 +2114,19 @@ mx_status gemm_int8_impl(const char* who, const int8_t* a, const float* a_s, con
   if (!a || !a_s || !b || !b_s || !c) return fail(MX_EINVAL, "%s: null pointer argument", who);
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_s, 4) || !aligned(b_s, 4) || !aligned(c, c_dtype == MX_F32 ? 4 : 2))
     return fail(MX_EALIGN, "%s: a and b must be 16-byte aligned, scales and c to their elements", who);
+  if (plan.workspace > 0 && !workspace) return fail(MX_EINVAL, "%s: null workspace", who);
+  if (!aligned(workspace, 256)) return fail(MX_EALIGN, "%s: workspace must be 256-byte aligned", who);
+  if (workspace_bytes < plan.workspace)
+    return fail(MX_EWORKSPACE, "%s: workspace %zu bytes < required %zu", who, workspace_bytes, plan.workspace);
   g->a = a; g->a_s = a_s; g->b = b; g->b_s = b_s; g->c = c;
-  hipError_t e = mx::launch_gemm_int8(result, *g, plan, reinterpret_cast<hipStream_t>(stream));
+  hipError_t e = mx::launch_gemm_int8(result, *g, plan, workspace, reinterpret_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, who);
   return MX_OK;
 }
 
 // The int8 MLP: the cast rows of X, the activations in fp32 and their cast.
 struct Int8MlpLayout {
-  size_t xq, xs, act, aq, as, total;
+  size_t xq, xs, act, aq, as, planes, total;
 };
 mx_status int8_mlp_layout(const char* who, const mx_mlp_dims* d, Int8MlpLayout* L) {
   if (!d) return fail(MX_EINVAL, "%s: null dims", who);
@@ -2138,6 +2143,14 @@ mx_status int8_mlp_layout(const char* who, const mx_mlp_dims* d, Int8MlpLayout* 
   L->act = take(cur, (size_t)(d->rows * d->ffn * 4));
   L->aq = take(cur, (size_t)(d->rows * d->ffn));
   L->as = take(cur, (size_t)(d->rows * 4));
+  static const int64_t unread = 0;
+  mx::Int8GemmArgs g{};
+  mx::Int8Plan p1, p2;
+  mx_status st = int8_groups(who, &unread, true, d->num_experts, d->rows, &g);
+  if (st == MX_OK) st = int8_shape(who, mx::kInt8ToSwiglu, 2 * d->ffn, d->hidden, &g, &p1);
+  if (st == MX_OK) st = int8_shape(who, mx::kInt8ToBf16, d->hidden, d->ffn, &g, &p2);
+  if (st != MX_OK) return st;
+  L->planes = take(cur, std::max(p1.workspace, p2.workspace));
   L->total = cur;
   return MX_OK;
 }
@@ -2232,37 +2245,51 @@ mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_rows, int6
   return MX_OK;
 }
 
+mx_status mx_gemm_int8_sizes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t* workspace) {
+  g_err[0] = 0;
+  const char* who = "mx_gemm_int8_sizes";
+  static const int64_t unread = 0;             // how k is shared out goes by the sizes below alone
+  mx::Int8GemmArgs g{};
+  mx::Int8Plan plan;
+  mx_status st = int8_groups(who, &unread, true, groups, m, &g);
+  if (st == MX_OK) st = int8_shape(who, mx::kInt8ToBf16, n, k, &g, &plan);
+  if (st != MX_OK) return st;
+  if (workspace) *workspace = plan.workspace;
+  return MX_OK;
+}
+
 mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m, int64_t n,
-                       int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+                       int64_t k, void* c, mx_dtype c_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
   const char* who = "mx_gemm_int8";
   mx::Int8GemmArgs g{};
   mx_status st = int8_groups(who, &m, false, 1, m, &g);
   if (st != MX_OK) return st;
   g.split = mx::kInt8OneGroup;
-  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, workspace, workspace_bytes, stream);
 }
 
 mx_status mx_grouped_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
                                const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n, int64_t k, void* c,
-                               mx_dtype c_dtype, void* stream) {
+                               mx_dtype c_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
   const char* who = "mx_grouped_gemm_int8";
   mx::Int8GemmArgs g{};
   mx_status st = int8_groups(who, group_sizes, false, groups, m, &g);
   if (st != MX_OK) return st;
-  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, workspace, workspace_bytes, stream);
 }
 
 mx_status mx_grouped_gemm_int8_device_split(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s,
                                             const int64_t* group_sizes, int32_t groups, int64_t m, int64_t n,
-                                            int64_t k, void* c, mx_dtype c_dtype, void* stream) {
+                                            int64_t k, void* c, mx_dtype c_dtype, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
   g_err[0] = 0;
   const char* who = "mx_grouped_gemm_int8_device_split";
   mx::Int8GemmArgs g{};
   mx_status st = int8_groups(who, group_sizes, true, groups, m, &g);
   if (st != MX_OK) return st;
-  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, stream);
+  return gemm_int8_impl(who, a, a_s, b, b_s, &g, n, k, c, c_dtype, workspace, workspace_bytes, stream);
 }
 
 mx_status grouped_mlp_int8_sizes(const mx_mlp_dims* dims, size_t* workspace) {
@@ -2313,12 +2340,12 @@ mx_status grouped_mlp_fwd_int8(const mx_mlp_dims* dims, const int64_t* split_siz
   hipError_t e = mx::launch_quantize_int8(q, s);
   if (e != hipSuccess) return hip_fail(e, who);
   g.a = q.q; g.a_s = q.s; g.b = w1; g.b_s = w1_s; g.c = ws + L.act;
-  if ((e = mx::launch_gemm_int8(mx::kInt8ToSwiglu, g, p1, s)) != hipSuccess) return hip_fail(e, who);
+  if ((e = mx::launch_gemm_int8(mx::kInt8ToSwiglu, g, p1, ws + L.planes, s)) != hipSuccess) return hip_fail(e, who);
   q.x = ws + L.act; q.f32 = 1; q.cols = (int32_t)F; q.ldx = F; q.row_index = nullptr; q.index_rows = R;
   q.row_weight = probs; q.q = reinterpret_cast<int8_t*>(ws + L.aq); q.s = reinterpret_cast<float*>(ws + L.as);
   if ((e = mx::launch_quantize_int8(q, s)) != hipSuccess) return hip_fail(e, who);
   g2.a = q.q; g2.a_s = q.s; g2.b = w2; g2.b_s = w2_s; g2.c = y;
-  if ((e = mx::launch_gemm_int8(mx::kInt8ToBf16, g2, p2, s)) != hipSuccess) return hip_fail(e, who);
+  if ((e = mx::launch_gemm_int8(mx::kInt8ToBf16, g2, p2, ws + L.planes, s)) != hipSuccess) return hip_fail(e, who);
   return MX_OK;
 }
 

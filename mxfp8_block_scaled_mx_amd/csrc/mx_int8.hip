@@ -7,6 +7,7 @@
 // order. (GroupedLinear over split_sizes: "Efficient MoE training for biological
 // foundation models", Key technical approaches items 1 and 3.)
 #include <algorithm>
+#include <cmath>
 
 #include "mx_device.h"
 #include "mx_internal.h"
@@ -135,17 +136,22 @@ __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantInt8Args a) {
 
 constexpr int kBK = 128;                     // k values of a step: one cache line of a row
 
-// Where a workgroup's tile lies: its group, and the group's rows.
+// Where a workgroup's tile lies: its group, and the group's rows and m-tiles.
 struct GroupSpan {
   int group, tile0, tiles;                   // tile0: the group's first m-tile
   int64_t row0;
   int rows;
 };
 
-// The group that holds m-tile `mt` of BM rows, from the rows of each group (held
-// on the device, or in the arguments). A count below 0 reads as 0, and one that
-// would take the running sum past M is cut there. Lanes hold two groups each;
-// every wave finds the same. Returns false where all groups have fewer tiles.
+// The groups in m-tiles of BM rows, from the rows of each group (held on the
+// device, or in the arguments), two groups a lane; every wave makes the same. A
+// count below 0 reads as 0, and one that would take the running sum past M is cut
+// there.
+struct GroupScan {
+  int64_t first[2], tend[2];                 // of lane's groups: first row, m-tiles up to its end
+  int rows[2], tiles[2];
+  int64_t total;                             // m-tiles of all groups
+};
 __device__ __forceinline__ int64_t scan64(int64_t v) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1) {
@@ -155,72 +161,143 @@ __device__ __forceinline__ int64_t scan64(int64_t v) {
   return v;
 }
 template <int BM>
-__device__ __forceinline__ bool find_group(const Int8GemmArgs& a, int64_t mt, GroupSpan* g) {
+__device__ __forceinline__ void scan_groups(const Int8GemmArgs& a, GroupScan* s) {
   if (a.split == kInt8OneGroup) {
-    *g = GroupSpan{0, 0, (int)(((int64_t)a.M + BM - 1) / BM), 0, a.M};
-    return mt < g->tiles;
+    s->total = ((int64_t)a.M + BM - 1) / BM;
+    return;
   }
   const int lane = threadIdx.x & 63;
-  int64_t rows0 = 0, tiles0 = 0;
-  bool found = false;
-  for (int base = 0; base < a.groups; base += 64) {
-    const int i = base + lane;
+  int64_t rows0 = 0;
+  s->total = 0;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    s->rows[u] = s->tiles[u] = 0;
+    s->first[u] = s->tend[u] = 0;
+    if (64 * u >= a.groups) break;           // (uniform)
+    const int i = 64 * u + lane;
     int64_t c = 0;
     if (i < a.groups) c = a.split == kInt8DeviceSizes ? a.sizes_dev[i] : (int64_t)a.sizes[i];
     c = min(max(c, (int64_t)0), (int64_t)a.M);
-    const int64_t end = rows0 + scan64(c);
-    const int64_t first = min(end - c, (int64_t)a.M), last = min(end, (int64_t)a.M);
-    const int64_t n = (last - first + BM - 1) / BM;
-    const int64_t tend = tiles0 + scan64(n);
-    const uint64_t here = __ballot(n > 0 && mt >= tend - n && mt < tend);
+    const int64_t end = rows0 + scan64(c), m = a.M;
+    s->first[u] = min(end - c, m);
+    s->rows[u] = (int)(min(end, m) - s->first[u]);
+    s->tiles[u] = (int)(((int64_t)s->rows[u] + BM - 1) / BM);
+    s->tend[u] = s->total + scan64(s->tiles[u]);
+    rows0 = __shfl(end, 63, 64);
+    s->total = __shfl(s->tend[u], 63, 64);
+  }
+}
+// The group that holds m-tile mt < total.
+template <int BM>
+__device__ __forceinline__ GroupSpan group_of(const Int8GemmArgs& a, const GroupScan& s, int64_t mt) {
+  if (a.split == kInt8OneGroup) return GroupSpan{0, 0, (int)s.total, 0, a.M};
+  GroupSpan g = {};
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint64_t here = __ballot(mt >= s.tend[u] - s.tiles[u] && mt < s.tend[u]);
     if (here) {
       const int src = __ffsll((unsigned long long)here) - 1;
-      g->group = base + src;
-      g->tile0 = (int)__shfl(tend - n, src, 64);
-      g->tiles = (int)__shfl(n, src, 64);
-      g->row0 = __shfl(first, src, 64);
-      g->rows = (int)__shfl(last - first, src, 64);
-      found = true;
+      g.group = 64 * u + src;
+      g.tiles = __builtin_amdgcn_readlane(s.tiles[u], src);
+      g.tile0 = (int)__shfl(s.tend[u], src, 64) - g.tiles;
+      g.row0 = __shfl(s.first[u], src, 64);
+      g.rows = __builtin_amdgcn_readlane(s.rows[u], src);
     }
-    rows0 = __shfl(end, 63, 64);
-    tiles0 = __shfl(tend, 63, 64);
   }
-  return found;
+  return g;
 }
 
-// A tile of 32 MI WM rows of A by 32 NI WN rows of B on WM x WN waves. Both
-// operands go straight to LDS (buffer loads with LDS as their target) one step of
-// 128 k ahead of the products, in two stages that are separate objects, so that
-// the compiler sees that a load into one never meets a read of the other. Chunk c
-// (16 bytes) of row r lies at c ^ ((r >> 1) & 7), which frees the fragment reads
-// of bank conflicts. Rows past the valid ones read as zeros by the bounds of the
-// buffer resource; past the last k, B's chunks are sent out of bounds, and what A
-// has there meets those zeros. Integers have no NaN that could survive this.
-// The MFMA takes A first, so that a lane holds one column n and 16 rows m: stores
-// of one register are whole runs of 32 columns.
+// Workgroup b of `total` runs on XCD b % 8. In rounds of 8 x CHUNK every XCD takes
+// CHUNK consecutive ids, and of what is left an eighth: ids that share rows share
+// an L2.
+template <int CHUNK>
+__device__ __forceinline__ int xcd_ids(int b, int total) {
+  const int xcd = b & 7, l = b >> 3, full = total / (8 * CHUNK), rest = total - full * 8 * CHUNK;
+  if (l < full * CHUNK) return (l / CHUNK) * 8 * CHUNK + xcd * CHUNK + l % CHUNK;
+  return full * 8 * CHUNK + xcd * (rest / 8) + min(xcd, rest % 8) + (l - full * CHUNK);
+}
+
+// silu(g) u. exp and the quotient are good to a few half steps of fp32.
+__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+
+// As vgpr_hop, for the integer sums.
+__device__ __forceinline__ int hop(int x) { return __builtin_amdgcn_mov_dpp(x, 0xE4, 0xF, 0xF, false); }
+
+// s_waitcnt immediates: vmcnt(n), as kWaitVmcnt0; and with it lgkmcnt(0).
+constexpr int wait_vmcnt(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int wait_vmcnt_lds(int n) { return 0x0070 | (n & 15) | ((n >> 4) << 14); }
+
+// The barrier alone. (__syncthreads() would wait for every load in flight first,
+// those for LDS among them.) What a wave has read of LDS before has to be in its
+// registers, and what it has loaded for the others has to have landed: the caller
+// waits for both.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
+// A tile of 64 MI rows of A by 64 NI rows of B on four waves, 2 x 2. Both operands
+// go straight to LDS (buffer loads with LDS as their target), in S stages of 128 k
+// that are separate objects, so that the compiler sees that a load into one never
+// meets a read of another. Chunk c (16 bytes) of row r lies at c ^ ((r >> 1) & 7),
+// which frees the fragment reads of bank conflicts. Rows past the valid ones read
+// as zeros by the bounds of the buffer resource; past the last k, B's chunks are
+// sent out of bounds, and what A has there meets those zeros. Integers have no NaN
+// that could survive this.
+//
+// A step of 128 k is four substeps of 32. In each, the fragments of the next
+// substep are read while the products of this one run, and the last one begins
+// with the barrier: by then every wave holds its last fragments of the stage, so
+// the loads of S steps on go into it at once (half then, half in the next
+// substep), and have S - 1 steps to land, while the first fragments of the next
+// stage are read behind the last products of this one. So neither the barrier nor
+// a fragment's latency leaves the matrix cores idle.
+// The MFMA takes B first: a lane holds one row m and runs of 4 columns n, which
+// go through LDS (16-byte chunk c of row r at c ^ (r & 15)) and leave as whole
+// cache lines.
 // With the SwiGLU, 32-row blocks of the B tile alternate between gate and up rows.
-template <int WM, int WN, int MI, int NI, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a) {
+// With parts > 1 each tile is several workgroups, each with its share of the
+// steps, that leave the sums themselves, in 32 bits, to planes of their own.
+template <int MI, int NI, int S, int EPI>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(64 * (MI + NI) * kBK * S <= 81920 ? 2 : 1)))
+void gemm_int8_kernel(Int8GemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  constexpr int W = WM * WN, BM = 32 * MI * WM, BN = 32 * NI * WN;
   constexpr bool kPair = EPI == kInt8ToSwiglu;
   static_assert(!kPair || NI % 2 == 0, "gate and up blocks come in pairs");
-  static_assert(BM % (8 * W) == 0 && BN % (8 * W) == 0 && W % 4 == 0, "whole blocks of 8 rows a wave");
+  static_assert(S == 2 || S == 4, "stages");
+  constexpr int BM = 64 * MI, BN = 64 * NI, kLoads = 2 * (MI + NI), kPerStep = (MI + NI) / MI;
+  static_assert(kPerStep * MI == MI + NI, "half of a step's loads in whole numbers per row block");
   __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kBK];
-  __shared__ __attribute__((aligned(16))) uint8_t sA1[BM * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sB0[BN * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sA1[BM * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sB1[BN * kBK];
+  __shared__ __attribute__((aligned(16))) uint8_t sA2[S > 2 ? BM * kBK : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sB2[S > 2 ? BN * kBK : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sA3[S > 2 ? BM * kBK : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sB3[S > 2 ? BN * kBK : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN, h = lane >> 5, l32 = lane & 31;
+  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, l32 = lane & 31;
   const int ntn = a.n_tiles;
-  GroupSpan g;
-  const int64_t id = blockIdx.x;
-  if (!find_group<BM>(a, id / ntn, &g)) return;
-  const int64_t local = id - (int64_t)g.tile0 * ntn;
-  const int mt = (int)(local % g.tiles), nt = (int)(local / g.tiles);
+  GroupScan scan;
+  scan_groups<BM>(a, &scan);
+  // a part's tiles are consecutive; the grid is sized for the worst split
+  const int tiles = (int)scan.total * ntn, all = tiles * a.parts;
+  if ((int)blockIdx.x >= all) return;
+  const int place = xcd_ids<MI * NI >= 16 ? 32 : 64>((int)blockIdx.x, all);
+  const int part = place / tiles, id = place - part * tiles;
+  const GroupSpan g = group_of<BM>(a, scan, id / ntn);
+  const int local = id - g.tile0 * ntn;
+  // bands of 8 m-tiles: the 32 tiles that run at once on one XCD are 8 x 4
+  const int band = local / (8 * ntn), in_band = local - band * 8 * ntn, height = min(8, g.tiles - 8 * band);
+  const int mt = 8 * band + in_band % height, nt = in_band / height;
   const int64_t row0 = g.row0 + (int64_t)mt * BM;
   const int rows = min(BM, g.rows - mt * BM);
-  const int K = a.K, nk = (K + kBK - 1) / kBK;
+  const int K = a.K, all_steps = (K + kBK - 1) / kBK;
+  const int first = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * part / a.parts));
+  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * (part + 1) / a.parts)) - first;
   const int nrows = kPair ? a.N / 2 : a.N;                 // rows of B that n-tiles cover (gate rows)
   constexpr int kTileRows = kPair ? BN / 2 : BN;
   const int n0 = nt * kTileRows, ncols = min(kTileRows, nrows - n0);
@@ -230,23 +307,28 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a)
   const __amdgpu_buffer_rsrc_t ru = make_rsrc(bg + (int64_t)(nrows + n0) * K, kPair ? (int64_t)ncols * K : 0);
   const int lch = (lane & 7) ^ (lane >> 4) ^ (4 * (wave & 1));
   const uint32_t voff = (uint32_t)(lane >> 3) * K + lch * 16;
-  auto load = [&](int kt, uint8_t* dA, uint8_t* dB) __attribute__((always_inline)) {
-    const int k0 = kt * kBK;
-    const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u;
-#pragma unroll
-    for (int it = 0; it < BM / 8 / W; ++it) {
-      const int blk = it * W + wave;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, voff, (uint32_t)(8 * blk) * K + k0, 0, 0);
-    }
-#pragma unroll
-    for (int it = 0; it < BN / 8 / W; ++it) {
-      const int blk = it * W + wave;
+  // Rows whose distance is a power of two lie on the same memory channels, so
+  // workgroups that walk along k together would meet there: they begin at other
+  // places. Those of an XCD that share rows keep step (for the L2's sake).
+  const int rot = __builtin_amdgcn_readfirstlane(nk * (int)(blockIdx.x & 7) / 8);
+  // Load p of this wave's kLoads of step kt (8 rows each: A's, then B's). Steps
+  // past the last are out of bounds for every lane: zeros, and no memory is read.
+  auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
+    const int s = kt + rot < nk ? kt + rot : kt + rot - nk;
+    const int k0 = __builtin_amdgcn_readfirstlane(kt < nk ? (first + s) * kBK : K);
+    if (p < 2 * MI) {
+      const int blk = 4 * p + wave;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, k0 < K ? voff : 0x80000000u,
+                                               (uint32_t)(8 * blk) * K + k0, 0, 0);
+    } else {
+      const int q = p - 2 * MI, blk = 4 * q + wave;
+      const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u;
       if constexpr (kPair) {
-        const int b32 = blk / 4, r0 = (b32 / 2) * 32 + (blk % 4) * 8;
-        if (b32 & 1)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, (uint32_t)r0 * K + k0, 0, 0);
+        const uint32_t so = (uint32_t)((q / 2) * 32 + 8 * wave) * K + k0;  // 32-row block q: gate and up in turn
+        if (q & 1)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
         else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, (uint32_t)r0 * K + k0, 0, 0);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
       } else {
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, (uint32_t)(8 * blk) * K + k0, 0, 0);
       }
@@ -259,169 +341,39 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_int8_kernel(Int8GemmArgs a)
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  auto frag = [&](const uint8_t* base, int r, int ks) __attribute__((always_inline)) -> v4i {
-    return *reinterpret_cast<const v4i*>(base + r * kBK + (((2 * ks + h) ^ ((r >> 1) & 7)) << 4));
-  };
-  auto compute = [&](const uint8_t* sA, const uint8_t* sB) __attribute__((always_inline)) {
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      v4i fa[MI], fb[NI];
-#pragma unroll
-      for (int i = 0; i < MI; ++i) fa[i] = frag(sA, 32 * (wm * MI + i) + l32, ks);
-#pragma unroll
-      for (int j = 0; j < NI; ++j) fb[j] = frag(sB, 32 * (wn * NI + j) + l32, ks);
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-  };
-  // The barrier says both that a stage is filled and that the other is free.
-  auto step = [&](int kt, const uint8_t* cA, const uint8_t* cB, uint8_t* nA, uint8_t* nB) __attribute__((always_inline)) {
-    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-    __syncthreads();
-    if (kt + 1 < nk) load(kt + 1, nA, nB);
-    compute(cA, cB);
-  };
-  load(0, sA0, sB0);
-  for (int kt = 0; kt < nk; kt += 2) {
-    step(kt, sA0, sB0, sA1, sB1);
-    if (kt + 1 < nk) step(kt + 1, sA1, sB1, sA0, sB0);
-  }
-  // results: column n of lane l32, rows 8 (v / 4) + 4 h + v % 4 of each 32
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int m = 32 * (wm * MI + i) + 8 * (v / 4) + 4 * h + v % 4;
-      if (m >= rows) continue;
-      const int64_t row = row0 + m;
-      const float sa = a.a_s[row];
-      if constexpr (kPair) {
-#pragma unroll
-        for (int j = 0; j < NI; j += 2) {
-          const int n = n0 + 32 * ((wn * NI + j) / 2) + l32;
-          if (n >= nrows) continue;
-          const float* const bs = a.b_s + (int64_t)g.group * a.N + n;
-          const float gate = (float)acc[i][j][v] * sa * bs[0], up = (float)acc[i][j + 1][v] * sa * bs[nrows];
-          reinterpret_cast<float*>(a.c)[row * nrows + n] = gate / (1.f + __expf(-gate)) * up;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NI; ++j) {
-          const int n = n0 + 32 * (wn * NI + j) + l32;
-          if (n >= nrows) continue;
-          const float y = (float)acc[i][j][v] * sa * a.b_s[(int64_t)g.group * a.N + n];
-          if constexpr (EPI == kInt8ToF32) reinterpret_cast<float*>(a.c)[row * a.N + n] = y;
-          else reinterpret_cast<__bf16*>(a.c)[row * a.N + n] = (__bf16)y;
-        }
-      }
-    }
-  }
-#endif
-}
-
-// As vgpr_hop, for the integer sums.
-__device__ __forceinline__ int hop(int x) { return __builtin_amdgcn_mov_dpp(x, 0xE4, 0xF, 0xF, false); }
-
-// The tile of 256 x 256 for many rows: four waves of 128 x 128, one a SIMD, so
-// that the 256 sums of a lane have their registers. The stages and their swizzle
-// are those of the kernel above; what differs is the order of things. A step of
-// 128 k is four substeps of 32. In each, the fragments of the next substep are
-// read while the products of this one run, and the last one begins with the
-// barrier: by then every wave holds its last fragments of the stage, so the loads
-// of the step after next go into it at once, and have nearly a whole step to
-// land, while the first fragments of the next stage are read behind the last
-// products of this one. So neither the barrier nor a fragment's latency leaves the
-// matrix cores idle.
-// The MFMA takes B first: a lane holds one row m and runs of 4 columns n, which
-// go through LDS (16-byte chunk c of row r at c ^ (r & 15)) and leave as whole
-// cache lines.
-template <int EPI>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void gemm_int8_big_kernel(Int8GemmArgs a) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  constexpr bool kPair = EPI == kInt8ToSwiglu;
-  constexpr int BM = 256, BN = 256;
-  __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kBK];
-  __shared__ __attribute__((aligned(16))) uint8_t sA1[BM * kBK];
-  __shared__ __attribute__((aligned(16))) uint8_t sB0[BN * kBK];
-  __shared__ __attribute__((aligned(16))) uint8_t sB1[BN * kBK];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, l32 = lane & 31;
-  const int ntn = a.n_tiles;
-  GroupSpan g;
-  const int64_t id = xcd_remap((int)blockIdx.x, (int)gridDim.x);
-  if (!find_group<BM>(a, id / ntn, &g)) return;
-  const int local = (int)(id - (int64_t)g.tile0 * ntn);
-  // bands of 8 m-tiles: the 32 tiles that run at once on one XCD are 8 x 4
-  const int band = local / (8 * ntn), in_band = local - band * 8 * ntn, height = min(8, g.tiles - 8 * band);
-  const int mt = 8 * band + in_band % height, nt = in_band / height;
-  const int64_t row0 = g.row0 + (int64_t)mt * BM;
-  const int rows = min(BM, g.rows - mt * BM);
-  const int K = a.K, nk = __builtin_amdgcn_readfirstlane((K + kBK - 1) / kBK);
-  const int nrows = kPair ? a.N / 2 : a.N;
-  constexpr int kTileRows = kPair ? BN / 2 : BN;
-  const int n0 = nt * kTileRows, ncols = min(kTileRows, nrows - n0);
-  const int8_t* const bg = a.b + (int64_t)g.group * a.N * K;
-  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.a + row0 * K, (int64_t)rows * K);
-  const __amdgpu_buffer_rsrc_t rb = make_rsrc(bg + (int64_t)n0 * K, (int64_t)ncols * K);
-  const __amdgpu_buffer_rsrc_t ru = make_rsrc(bg + (int64_t)(nrows + n0) * K, kPair ? (int64_t)ncols * K : 0);
-  const int lch = (lane & 7) ^ (lane >> 4) ^ (4 * (wave & 1));
-  const uint32_t voff = (uint32_t)(lane >> 3) * K + lch * 16;
-  // Block p of this wave's eight of A and of B of step kt. Steps past the last
-  // are out of bounds for every lane: zeros, and no memory is read.
-  auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
-    const int k0 = __builtin_amdgcn_readfirstlane(kt * kBK);
-    const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u, va = k0 < K ? voff : 0x80000000u;
-    const int blk = 4 * p + wave;
-    const uint32_t so = (uint32_t)(8 * blk) * K + k0;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, va, so, 0, 0);
-    if constexpr (kPair) {
-      const uint32_t sp = (uint32_t)((p / 2) * 32 + 8 * wave) * K + k0;    // 32-row block p: gate and up in turn
-      if (p & 1)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, sp, 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, sp, 0, 0);
-    } else {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
-    }
-  };
-  v16i acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  v4i fa[2][4], fb[2][4];
+  v4i fa[2][MI], fb[2][NI];
   const int sw = (l32 >> 1) & 7;               // of every row 32 x + l32
   auto frag = [&](const uint8_t* base, int r32, int ks) __attribute__((always_inline)) -> v4i {
     return *reinterpret_cast<const v4i*>(base + (r32 * 32 + l32) * kBK + (((2 * ks + h) ^ sw) << 4));
   };
-  // Step kt from stage (cA, cB); (nA, nB) holds step kt + 1. Half of a step's blocks
-  // are loaded in the last substep of the step two before, half in the next one.
-  auto step = [&](int kt, uint8_t* cA, uint8_t* cB, uint8_t* nA, uint8_t* nB) __attribute__((always_inline)) {
+  // Step kt from stage (cA, cB); (nA, nB) holds step kt + 1, and the loads of step
+  // kt - 1 + S, half of which are out, go to (pA, pB).
+  auto step = [&](int kt, uint8_t* cA, uint8_t* cB, uint8_t* nA, uint8_t* nB, uint8_t* pA, uint8_t* pB)
+      __attribute__((always_inline)) {
     static_for<0, 4>([&](auto ks_) __attribute__((always_inline)) {
-      constexpr int ks = decltype(ks_)::value, cur = ks & 1, nxt = cur ^ 1;
+      constexpr int ks = decltype(ks_)::value, cur = ks & 1, nxt = cur ^ 1, ns = (ks + 1) & 3;
       if constexpr (ks == 3) {
-        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-        __syncthreads();
+        __builtin_amdgcn_s_waitcnt(wait_vmcnt_lds((S - 2) * kLoads));
+        bare_barrier();
       }
-      static_for<0, 4>([&](auto i_) __attribute__((always_inline)) {
+      const uint8_t* const rA = ks == 3 ? nA : cA;
+      const uint8_t* const rB = ks == 3 ? nB : cB;
+      static_for<0, MI>([&](auto i_) __attribute__((always_inline)) {
         constexpr int i = decltype(i_)::value;
-        const uint8_t* const rA = ks == 3 ? nA : cA;
-        const uint8_t* const rB = ks == 3 ? nB : cB;
-        constexpr int ns = (ks + 1) & 3;
-        if constexpr (i < 2) {
-          fb[nxt][2 * i] = frag(rB, wn * 4 + 2 * i, ns);
-          fb[nxt][2 * i + 1] = frag(rB, wn * 4 + 2 * i + 1, ns);
-        } else {
-          fa[nxt][2 * i - 4] = frag(rA, wm * 4 + 2 * i - 4, ns);
-          fa[nxt][2 * i - 3] = frag(rA, wm * 4 + 2 * i - 3, ns);
+        // B's fragments in the first row blocks, A's in the last
+        static_for<0, MI + NI>([&](auto f_) __attribute__((always_inline)) {
+          constexpr int f = decltype(f_)::value;
+          if constexpr (f / kPerStep == i) {
+            if constexpr (f < NI) fb[nxt][f] = frag(rB, wn * NI + f, ns);
+            else fa[nxt][f - NI] = frag(rA, wm * MI + f - NI, ns);
+          }
+        });
+#pragma unroll
+        for (int q = 0; q < kPerStep; ++q) {
+          if constexpr (ks == 3) load(kt + S, cA, cB, kPerStep * i + q);
+          if constexpr (ks == 0) load(kt - 1 + S, pA, pB, MI + NI + kPerStep * i + q);
         }
-        if constexpr (ks == 3) load(kt + 2, cA, cB, i);
-        if constexpr (ks == 0) load(kt + 1, nA, nB, 4 + i);
-        static_for<0, 4>([&](auto j_) __attribute__((always_inline)) {
+        static_for<0, NI>([&](auto j_) __attribute__((always_inline)) {
           constexpr int j = decltype(j_)::value;
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
         });
@@ -429,61 +381,88 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
       });
     });
   };
+  auto fill = [&](int kt, uint8_t* dA, uint8_t* dB, int n) __attribute__((always_inline)) {
 #pragma unroll
-  for (int p = 0; p < 8; ++p) load(0, sA0, sB0, p);
-#pragma unroll
-  for (int p = 0; p < 4; ++p) load(1, sA1, sB1, p);
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    fb[0][x] = frag(sB0, wn * 4 + x, 0);
-    fa[0][x] = frag(sA0, wm * 4 + x, 0);
+    for (int p = 0; p < n; ++p) load(kt, dA, dB, p);
+  };
+  fill(0, sA0, sB0, kLoads);
+  if constexpr (S == 4) {
+    fill(1, sA1, sB1, kLoads);
+    fill(2, sA2, sB2, kLoads);
+    fill(3, sA3, sB3, MI + NI);
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads + MI + NI));          // step 0 has landed
+  } else {
+    fill(1, sA1, sB1, MI + NI);
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(MI + NI));
   }
+  bare_barrier();
+#pragma unroll
+  for (int x = 0; x < NI; ++x) fb[0][x] = frag(sB0, wn * NI + x, 0);
+#pragma unroll
+  for (int x = 0; x < MI; ++x) fa[0][x] = frag(sA0, wm * MI + x, 0);
   int kt = 0;
-  for (; kt + 1 < nk; kt += 2) {
-    step(kt, sA0, sB0, sA1, sB1);
-    step(kt + 1, sA1, sB1, sA0, sB0);
+  if constexpr (S == 4) {
+    for (; kt + 3 < nk; kt += 4) {
+      step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
+      step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+      step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
+      step(kt + 3, sA3, sB3, sA0, sB0, sA2, sB2);
+    }
+    if (kt < nk) {
+      step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
+      if (kt + 1 < nk) {
+        step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+        if (kt + 2 < nk) step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
+      }
+    }
+  } else {
+    for (; kt + 1 < nk; kt += 2) {
+      step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
+      step(kt + 1, sA1, sB1, sA0, sB0, sA0, sB0);
+    }
+    if (kt < nk) step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
   }
-  if (kt < nk) step(kt, sA0, sB0, sA1, sB1);
-  // Sums to results. Lane: row 32 i + l32 of the wave's 128, columns 32 j + 8 q +
-  // 4 h + 0 .. 3 of its 128; by 32 rows through the wave's own 16 KiB of LDS.
+  // Sums to results. Lane: row 32 i + l32 of the wave's rows, columns 32 j + 8 q +
+  // 4 h + 0 .. 3 of its columns; by 32 rows through LDS of the wave's own.
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
   __syncthreads();
-  uint8_t* const stage = (wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1);
-  constexpr int kBytes = EPI == kInt8ToBf16 ? 2 : 4, kCols = kPair ? 64 : 128, kRowBytes = kCols * kBytes;
-  constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes;
+  constexpr int kBytes = EPI == kInt8ToBf16 ? 2 : 4, kCols = (kPair ? 16 : 32) * NI, kRowBytes = kCols * kBytes;
+  constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes, kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static_assert(32 * kRowBytes <= BM * kBK && 32 * kRowBytes <= BN * kBK, "32 rows of results fit one stage of one operand");
+  uint8_t* const stage = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
   const int cn0 = n0 + wn * kCols;             // the wave's first column of C
   const int64_t ldc = nrows;
+  uint8_t* const c = reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * ldc * 4 : 0);
   const float* const bs = a.b_s + (int64_t)g.group * a.N;
-  const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(a.c) & 15) == 0;
+  const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m0 = wm * 128 + 32 * i;
+  for (int i = 0; i < MI; ++i) {
+    const int m0 = 32 * (wm * MI + i);
     if (m0 >= rows) break;
-    const float sa = a.a_s[row0 + min(m0 + l32, rows - 1)];
+    const float sa = EPI == kInt8ToSums ? 0.f : a.a_s[row0 + min(m0 + l32, rows - 1)];
 #pragma unroll
-    for (int j = 0; j < 4; j += kPair ? 2 : 1) {
+    for (int j = 0; j < NI; j += kPair ? 2 : 1) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int col = 32 * (kPair ? j / 2 : j) + 8 * q + 4 * h;
-        float y[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int n = min(cn0 + col + v, nrows - 1);
-          y[v] = (float)hop(acc[i][j][4 * q + v]) * sa * bs[n];
-          if constexpr (kPair) {
-            const float up = (float)hop(acc[i][j + 1][4 * q + v]) * sa * bs[nrows + n];
-            y[v] = y[v] / (1.f + __expf(-y[v])) * up;
-          }
-        }
-        const int chunk = col / kPer;
-        uint8_t* const at = stage + l32 * kRowBytes + ((chunk ^ (l32 & (kChunks - 1) & 15)) << 4);
-        if constexpr (kBytes == 4) {
-          *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+        uint8_t* const at = stage + l32 * kRowBytes + (((col / kPer) ^ (l32 & kMask)) << 4);
+        if constexpr (EPI == kInt8ToSums) {
+          *reinterpret_cast<v4i*>(at) = v4i{hop(acc[i][j][4 * q]), hop(acc[i][j][4 * q + 1]), hop(acc[i][j][4 * q + 2]),
+                                            hop(acc[i][j][4 * q + 3])};
         } else {
-          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+          float y[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int n = min(cn0 + col + v, nrows - 1);
+            y[v] = (float)hop(acc[i][j][4 * q + v]) * sa * bs[n];
+            if constexpr (kPair) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa * bs[nrows + n]);
+          }
+          if constexpr (kBytes == 4) {
+            *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+          } else {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+          }
         }
       }
     }
@@ -494,19 +473,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     if (whole) {
 #pragma unroll
       for (int u = 0; u < 32 * kChunks / 64; ++u) {
-        const int r = (u * 64 + lane) / kChunks, c = (u * 64 + lane) % kChunks, n = cn0 + c * kPer;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((c ^ (r & (kChunks - 1) & 15)) << 4));
-        if (m0 + r < rows && n < nrows)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(a.c) + ((row0 + m0 + r) * ldc + n) * kBytes) = w;
+        const int r = (u * 64 + lane) / kChunks, ch = (u * 64 + lane) % kChunks, n = cn0 + ch * kPer;
+        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
+        if (m0 + r < rows && n < nrows) *reinterpret_cast<uint4*>(c + ((row0 + m0 + r) * ldc + n) * kBytes) = w;
       }
     } else {
       for (int u = lane; u < 32 * kCols; u += 64) {
-        const int r = u / kCols, c = u % kCols, n = cn0 + c;
-        const uint8_t* const from = stage + r * kRowBytes + (((c / kPer) ^ (r & (kChunks - 1) & 15)) << 4) + c % kPer * kBytes;
+        const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
+        const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
         if (m0 + r < rows && n < nrows) {
           const int64_t at = (row0 + m0 + r) * ldc + n;
-          if constexpr (kBytes == 4) reinterpret_cast<float*>(a.c)[at] = *reinterpret_cast<const float*>(from);
-          else reinterpret_cast<uint16_t*>(a.c)[at] = *reinterpret_cast<const uint16_t*>(from);
+          if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
+          else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
         }
       }
     }
@@ -517,18 +495,240 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
 #endif
 }
 
-template <int WM, int WN, int MI, int NI>
-struct Shape {
-  static constexpr int kWM = WM, kWN = WN, kMI = MI, kNI = NI, kBM = 32 * MI * WM, kBN = 32 * NI * WN;
-};
-template <typename Go>
-auto by_shape(int shape, const Go& go) {
-  switch (shape) {
-    case 0: return go(Shape<1, 4, 1, 2>{});
-    case 1: return go(Shape<2, 2, 1, 2>{});
-    default: return go(Shape<2, 2, 4, 4>{});
+// The planes of a product whose steps were shared out, added up and finished: row
+// blockIdx.y, 4 columns a thread. a.planes: [parts, M, N].
+template <int EPI>
+__global__ __launch_bounds__(256) void int8_join_kernel(Int8GemmArgs a) {
+  const int row = blockIdx.y;
+  GroupScan scan;
+  scan_groups<1>(a, &scan);                    // "tiles" of one row
+  if (row >= scan.total) return;
+  const GroupSpan g = group_of<1>(a, scan, row);
+  const int cols = EPI == kInt8ToSwiglu ? a.N / 2 : a.N;
+  const int n = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (n >= cols) return;
+  const int64_t plane = (int64_t)a.M * a.N;
+  const int* const from = a.planes + (int64_t)row * a.N + n;
+  int sum[4] = {0, 0, 0, 0}, up[4] = {0, 0, 0, 0};
+  if (a.N % (EPI == kInt8ToSwiglu ? 8 : 4) == 0) {
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p) {
+      const v4i v = *reinterpret_cast<const v4i*>(from + p * plane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += v[i];
+      if constexpr (EPI == kInt8ToSwiglu) {
+        const v4i u = *reinterpret_cast<const v4i*>(from + p * plane + cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) up[i] += u[i];
+      }
+    }
+  } else {
+    for (int p = 0; p < a.parts; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < cols) {
+          sum[i] += from[p * plane + i];
+          if constexpr (EPI == kInt8ToSwiglu) up[i] += from[p * plane + cols + i];
+        }
+  }
+  const float sa = a.a_s[row];
+  const float* const bs = a.b_s + (int64_t)g.group * a.N + n;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= cols) break;
+    const int64_t at = (int64_t)row * cols + n + i;
+    const float y = (float)sum[i] * sa * bs[i];
+    if constexpr (EPI == kInt8ToSwiglu) reinterpret_cast<float*>(a.c)[at] = swiglu(y, (float)up[i] * sa * bs[cols + i]);
+    else if constexpr (EPI == kInt8ToF32) reinterpret_cast<float*>(a.c)[at] = y;
+    else reinterpret_cast<__bf16*>(a.c)[at] = (__bf16)y;
   }
 }
+
+// Few rows: the weights pass once and bound the time, so what counts is that many
+// loads are always in flight. A workgroup owns 16 NT rows of B and 16 MT of A; its
+// W waves share the steps of 128 k among them (wave w takes w, w + W, ...), each
+// with a ring of three stages of its own in LDS that only it fills and reads, two
+// steps ahead, without a barrier. The waves' sums meet in LDS at the end; sums of
+// integers are the same in any order.
+// Rows and k out of range read as zeros, as above. With the SwiGLU (NT = 2) the
+// second 16 rows of B are the up rows of the first 16's channels.
+template <int MT, int NT, int W, int EPI, bool ONCE>
+__global__ __launch_bounds__(64 * W) void gemm_int8_narrow_kernel(Int8GemmArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  constexpr bool kPair = EPI == kInt8ToSwiglu;
+  static_assert(!kPair || NT == 2, "16 gate and 16 up rows");
+  constexpr int BM = 16 * MT, TN = 16 * NT, kStage = (BM + TN) * kBK, kLoads = (BM + TN) / 8;
+  static_assert(W * kStage >= 4 * W * BM * TN, "the sums fit a stage");
+  constexpr int kAux = ONCE ? 2 : 0;                       // non-temporal
+  __shared__ __attribute__((aligned(16))) uint8_t s0[W * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s1[W * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t s2[W * kStage];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ntn = a.n_tiles, id = blockIdx.x;
+  GroupScan scan;
+  scan_groups<BM>(a, &scan);
+  if (id / ntn >= scan.total) return;
+  const GroupSpan g = group_of<BM>(a, scan, id / ntn);
+  const int local = id - g.tile0 * ntn;
+  const int mt = local % g.tiles, nt = local / g.tiles;
+  const int64_t row0 = g.row0 + (int64_t)mt * BM;
+  const int rows = min(BM, g.rows - mt * BM);
+  const int K = a.K, nk = (K + kBK - 1) / kBK;
+  const int turns = __builtin_amdgcn_readfirstlane((nk + W - 1) / W);
+  const int nrows = kPair ? a.N / 2 : a.N;
+  constexpr int kTileRows = kPair ? TN / 2 : TN;
+  const int n0 = nt * kTileRows, ncols = min(kTileRows, nrows - n0);
+  const int8_t* const bg = a.b + (int64_t)g.group * a.N * K;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(a.a + row0 * K, (int64_t)rows * K);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(bg + (int64_t)n0 * K, (int64_t)ncols * K);
+  const __amdgpu_buffer_rsrc_t ru = make_rsrc(bg + (int64_t)(nrows + n0) * K, kPair ? (int64_t)ncols * K : 0);
+  const int c_even = (lane & 7) ^ (lane >> 4);             // logical chunk in blocks of 8 rows, even ones; odd: ^ 4
+  const uint32_t v_even = (uint32_t)(lane >> 3) * K + c_even * 16, v_odd = (uint32_t)(lane >> 3) * K + (c_even ^ 4) * 16;
+  auto load = [&](int turn, uint8_t* stage) __attribute__((always_inline)) {
+    const int k0 = __builtin_amdgcn_readfirstlane(turn < turns ? (wave * turns + turn) * kBK : K);
+    uint8_t* const to = stage + wave * kStage;
+    const uint32_t be = k0 + c_even * 16 < K ? v_even : 0x80000000u, bo = k0 + (c_even ^ 4) * 16 < K ? v_odd : 0x80000000u;
+#pragma unroll
+    for (int b = 0; b < TN / 8; ++b) {
+      const uint32_t so = (uint32_t)(8 * (kPair ? b % 2 : b)) * K + k0;
+      if (kPair && b >= 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(to + b * 1024), 16, b & 1 ? bo : be, so, 0, kAux);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(to + b * 1024), 16, b & 1 ? bo : be, so, 0, kAux);
+    }
+    const uint32_t ae = k0 < K ? v_even : 0x80000000u, ao = k0 < K ? v_odd : 0x80000000u;
+#pragma unroll
+    for (int b = 0; b < BM / 8; ++b)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(to + TN * kBK + b * 1024), 16, b & 1 ? ao : ae,
+                                               (uint32_t)(8 * b) * K + k0, 0, 0);
+  };
+  v4i acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  const int r16 = lane & 15, quarter = lane >> 4;
+  auto compute = [&](const uint8_t* stage) __attribute__((always_inline)) {
+    const uint8_t* const from = stage + wave * kStage;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      v4i fa[MT], fb[NT];
+      const int at = r16 * kBK + (((4 * ks + quarter) ^ ((r16 >> 1) & 7)) << 4);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[j] = *reinterpret_cast<const v4i*>(from + 16 * j * kBK + at);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i] = *reinterpret_cast<const v4i*>(from + (TN + 16 * i) * kBK + at);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  // Turn t: the loads of turn t + 2 go out, into the stage that turn t - 1 has
+  // read; then all but the last two turns' loads have landed.
+  auto turn = [&](int t, const uint8_t* cur, uint8_t* free) __attribute__((always_inline)) {
+    load(t + 2, free);
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads));
+    compute(cur);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  load(0, s0);
+  load(1, s1);
+  int t = 0;
+  for (; t + 2 < turns; t += 3) {
+    turn(t, s0, s2);
+    turn(t + 1, s1, s0);
+    turn(t + 2, s2, s1);
+  }
+  if (t < turns) turn(t, s0, s2);
+  if (t + 1 < turns) turn(t + 1, s1, s0);
+  // sums of wave w: [w][row][column]
+  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+  __syncthreads();
+  int* const sums = reinterpret_cast<int*>(s0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) sums[(wave * BM + 16 * i + 4 * quarter + v) * TN + 16 * j + r16] = acc[i][j][v];
+  __syncthreads();
+  constexpr int kCols = kTileRows;
+  for (int u = threadIdx.x; u < BM * kCols; u += 64 * W) {
+    const int m = u / kCols, c = u % kCols, n = n0 + c;
+    if (m >= rows || n >= nrows) continue;
+    const int64_t row = row0 + m;
+    const float sa = a.a_s[row];
+    const float* const bs = a.b_s + (int64_t)g.group * a.N + n;
+    int sum = 0, sum2 = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      sum += sums[(w * BM + m) * TN + c];
+      if constexpr (kPair) sum2 += sums[(w * BM + m) * TN + 16 + c];
+    }
+    const float y = (float)sum * sa * bs[0];
+    if constexpr (kPair)
+      reinterpret_cast<float*>(a.c)[row * nrows + n] = swiglu(y, (float)sum2 * sa * bs[nrows]);
+    else if constexpr (EPI == kInt8ToF32)
+      reinterpret_cast<float*>(a.c)[row * a.N + n] = y;
+    else
+      reinterpret_cast<__bf16*>(a.c)[row * a.N + n] = (__bf16)y;
+  }
+#endif
+}
+
+// The forms of a product.
+template <int MT, int NT, int W>
+struct Narrow {
+  static constexpr int kBM = 16 * MT, kBN = 16 * NT, kThreads = 64 * W, kWaves = W;
+  static constexpr bool kPairs = NT == 2, kSums = false;
+  template <int EPI>
+  static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
+    if constexpr (EPI != kInt8ToSums && (EPI != kInt8ToSwiglu || kPairs)) {
+      if (a.once) hipLaunchKernelGGL((gemm_int8_narrow_kernel<MT, NT, W, EPI, true>), grid, dim3(kThreads), 0, s, a);
+      else hipLaunchKernelGGL((gemm_int8_narrow_kernel<MT, NT, W, EPI, false>), grid, dim3(kThreads), 0, s, a);
+    }
+  }
+};
+template <int MI, int NI, int S>
+struct Tile {
+  static constexpr int kBM = 64 * MI, kBN = 64 * NI, kThreads = 256, kWaves = 1;
+  static constexpr bool kPairs = NI % 2 == 0, kSums = true;
+  template <int EPI>
+  static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
+    if constexpr (EPI != kInt8ToSwiglu || kPairs)
+      hipLaunchKernelGGL((gemm_int8_kernel<MI, NI, S, EPI>), grid, dim3(kThreads), 0, s, a);
+  }
+};
+constexpr int kForms = 10;
+template <typename Go>
+void by_form(int form, const Go& go) {
+  switch (form) {
+    case 0: return go(Narrow<1, 1, 1>{});
+    case 1: return go(Narrow<1, 1, 4>{});
+    case 2: return go(Narrow<1, 2, 4>{});
+    case 3: return go(Narrow<2, 1, 4>{});
+    case 4: return go(Narrow<2, 2, 4>{});
+    case 5: return go(Tile<1, 1, 4>{});
+    case 6: return go(Tile<1, 2, 4>{});
+    case 7: return go(Tile<2, 2, 2>{});
+    case 8: return go(Tile<2, 2, 4>{});
+    default: return go(Tile<4, 4, 2>{});
+  }
+}
+
+// What a form takes, in us: a step of 128 k of one workgroup alone on a compute
+// unit and of one among several there, what a tile takes besides, how much more a
+// step takes where k is no multiple of 128 (each piece of a row then lies on two
+// cache lines); and the rate, in TB/s, at which it reads weights that pass once.
+struct FormCost {
+  float alone, among, tile, ragged, rate;
+};
+constexpr FormCost kCost[kForms] = {
+    {0.22f, 0.105f, 0.2f, 1.0f, 5.0f}, {0.36f, 0.35f, 0.2f, 1.5f, 5.7f}, {0.52f, 0.50f, 0.2f, 1.5f, 5.2f},
+    {0.50f, 0.50f, 0.2f, 1.5f, 3.6f},  {0.66f, 0.66f, 0.2f, 1.5f, 4.0f}, {0.29f, 0.25f, 0.5f, 1.7f, 4.5f},
+    {0.43f, 0.43f, 1.0f, 1.6f, 5.0f},  {0.81f, 0.53f, 1.0f, 1.6f, 3.4f}, {0.60f, 0.60f, 2.0f, 1.4f, 4.6f},
+    {1.45f, 1.45f, 4.0f, 1.15f, 2.5f}};
 
 }  // namespace
 
@@ -552,51 +752,90 @@ hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// The form and the number of parts that the figures above make cheapest. Checked
+// against each form forced (us; rows x n x k, form chosen first): 16 x 28672 x 4096
+// narrow 22, 64 x 128 tiles 24, 256 x 256 49; 64 x 4096 x 14336 64 x 64 tiles in 4
+// parts 18, narrow 30, whole 36; 256 x 4096 x 14336 128 x 128 in 4 parts 32, whole
+// 67; 512 x 28672 x 4096 256 x 256 69, 128 x 128 83; 2048 x 4096 x 4096 128 x 128,
+// two a compute unit, 40, 256 x 256 56. It goes by sizes alone, not by how the rows
+// fall to the groups, so that a call's workspace does not depend on it.
 Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
-  Int8Plan p;
-  const int64_t per = ((int64_t)a.M + a.groups - 1) / a.groups;        // rows of a group in the mean
-  const int64_t big = (((int64_t)a.M + 255) / 256) * (((int64_t)a.N + 255) / 256);
-  p.shape = per <= 32 ? 0 : per <= 128 || big < 128 ? 1 : 2;
-  by_shape(p.shape, [&](auto s) {
-    constexpr int BM = decltype(s)::kBM, BN = decltype(s)::kBN;
-    const int64_t cols = result == kInt8ToSwiglu ? a.N / 2 : a.N, bn = result == kInt8ToSwiglu ? BN / 2 : BN;
+  const bool pair = result == kInt8ToSwiglu;
+  const int64_t groups = std::min(a.groups, a.M), per = ((int64_t)a.M + groups - 1) / groups;
+  const int steps = (a.K + kBK - 1) / kBK;
+  const double weights = (double)groups * a.N * a.K * 1e-6;
+  Int8Plan best;
+  double best_us = 1e30;
+  for (int form = 0; form < kForms; ++form) {
+    by_form(form, [&](auto f) {
+      using Form = decltype(f);
+      const FormCost& cost = kCost[form];
+      const int64_t mtiles = groups * ((per + Form::kBM - 1) / Form::kBM);
+      for (int parts = 1; parts <= (Form::kSums ? 16 : 1); parts *= 2) {
+        const bool half = pair && parts == 1;              // the product forms the SwiGLU, not the join
+        if (half && !Form::kPairs) continue;
+        if (parts > 1 && (steps / parts < 4 || a.M > 65535 || (int64_t)parts * a.M * a.N > ((int64_t)1 << 26))) break;
+        const int64_t bn = half ? Form::kBN / 2 : Form::kBN, cols = half ? a.N / 2 : a.N;
+        const double wgs = (double)mtiles * ((cols + bn - 1) / bn) * parts;
+        const double c = std::ceil(wgs / 256);
+        const double mine = std::ceil((double)steps / (Form::kWaves * parts)) * (a.K % kBK ? cost.ragged : 1.f);
+        double us = std::max(2.5 + mine * std::max((double)cost.alone, c * cost.among) + c * cost.tile, weights / cost.rate);
+        if (parts > 1) us += 3.0 + (double)parts * a.M * a.N * 8 / 4.5e6;  // the planes, written and read
+        if (us < best_us) {
+          best_us = us;
+          best.form = form;
+          best.parts = parts;
+        }
+      }
+    });
+  }
+  by_form(best.form, [&](auto f) {
+    constexpr int BM = decltype(f)::kBM, BN = decltype(f)::kBN;
+    const bool half = pair && best.parts == 1;
+    const int64_t cols = half ? a.N / 2 : a.N, bn = half ? BN / 2 : BN;
     int64_t mtiles = 0;
     if (a.split == kInt8HostSizes) {
       for (int g = 0; g < a.groups; ++g) mtiles += ((int64_t)a.sizes[g] + BM - 1) / BM;
     } else {
-      const int64_t some = std::min<int64_t>(a.split == kInt8OneGroup ? 1 : a.groups, a.M);
+      const int64_t some = a.split == kInt8OneGroup ? 1 : groups;
       mtiles = (a.M + (BM - 1) * some) / BM;               // the most that any split can have
     }
-    p.n_tiles = (cols + bn - 1) / bn;
-    p.tiles = mtiles * p.n_tiles;
-    return 0;
+    best.n_tiles = (cols + bn - 1) / bn;
+    best.tiles = mtiles * best.n_tiles;
   });
-  return p;
+  best.workspace = best.parts > 1 ? (size_t)best.parts * a.M * a.N * 4 : 0;
+  return best;
 }
 
-hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan& p, hipStream_t stream) {
+hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan& p, void* workspace, hipStream_t stream) {
   Int8GemmArgs a = args;
   a.n_tiles = (int32_t)p.n_tiles;
+  a.parts = p.parts;
+  a.planes = reinterpret_cast<int32_t*>(workspace);
+  a.once = a.K % kBK == 0;
   if (p.tiles == 0) return hipSuccess;
-  by_shape(p.shape, [&](auto s) {
+  by_form(p.form, [&](auto s) {
     using S = decltype(s);
-    constexpr int WM = S::kWM, WN = S::kWN, MI = S::kMI, NI = S::kNI;
-    const dim3 grid((unsigned)p.tiles), block(64 * WM * WN);
-    if constexpr (S::kBM == 256) {
-      if (result == kInt8ToBf16)
-        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToBf16>), grid, block, 0, stream, a);
-      else if (result == kInt8ToF32)
-        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToF32>), grid, block, 0, stream, a);
-      else
-        hipLaunchKernelGGL((gemm_int8_big_kernel<kInt8ToSwiglu>), grid, block, 0, stream, a);
-    } else if (result == kInt8ToBf16)
-      hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, MI, NI, kInt8ToBf16>), grid, block, 0, stream, a);
-    else if (result == kInt8ToF32)
-      hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, MI, NI, kInt8ToF32>), grid, block, 0, stream, a);
-    else
-      hipLaunchKernelGGL((gemm_int8_kernel<WM, WN, MI, NI, kInt8ToSwiglu>), grid, block, 0, stream, a);
-    return 0;
+    const dim3 grid((unsigned)(p.tiles * p.parts));
+    if (p.parts > 1) {
+      Int8GemmArgs sums = a;
+      sums.c = workspace;
+      S::template launch<kInt8ToSums>(grid, stream, sums);
+    } else if (result == kInt8ToBf16) {
+      S::template launch<kInt8ToBf16>(grid, stream, a);
+    } else if (result == kInt8ToF32) {
+      S::template launch<kInt8ToF32>(grid, stream, a);
+    } else {
+      S::template launch<kInt8ToSwiglu>(grid, stream, a);
+    }
   });
+  if (p.parts > 1) {
+    const int cols = result == kInt8ToSwiglu ? a.N / 2 : a.N;
+    const dim3 grid((unsigned)((cols + 1023) / 1024), (unsigned)a.M);
+    if (result == kInt8ToBf16) hipLaunchKernelGGL(int8_join_kernel<kInt8ToBf16>, grid, dim3(256), 0, stream, a);
+    else if (result == kInt8ToF32) hipLaunchKernelGGL(int8_join_kernel<kInt8ToF32>, grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(int8_join_kernel<kInt8ToSwiglu>, grid, dim3(256), 0, stream, a);
+  }
   return hipGetLastError();
 }
 

@@ -413,18 +413,20 @@ struct Int8GemmArgs {
   int32_t M, N, K, groups, split;
   const int64_t* sizes_dev;
   int32_t sizes[kMaxGroups];
-  int32_t n_tiles;                  // set by the launch
+  int32_t n_tiles, parts, once;     // set by the launch, as is
+  int32_t* planes;                  // [parts, M, N] sums (parts > 1)
 };
-enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2 };
-// How a product runs: the tile shape, and its workgroups (at most kInt8MaxTiles:
+enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2, kInt8ToSums = 3 };
+// How a product runs: the kernel's form, and its workgroups (at most kInt8MaxTiles:
 // a launch has fewer than 2^32 threads along x).
 struct Int8Plan {
-  int32_t shape;
+  int32_t form, parts;              // parts > 1: k is shared out over workgroups
   int64_t n_tiles, tiles;
+  size_t workspace;                 // bytes of its planes
 };
 constexpr int64_t kInt8MaxTiles = ((int64_t)1 << 24) - 1;
 Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a);
-hipError_t launch_gemm_int8(int result, const Int8GemmArgs& a, const Int8Plan& p, hipStream_t stream);
+hipError_t launch_gemm_int8(int result, const Int8GemmArgs& a, const Int8Plan& p, void* workspace, hipStream_t stream);
 
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;

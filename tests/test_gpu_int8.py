@@ -131,6 +131,68 @@ def test_product(gpu_lib, m, n, k):
         _close(gpu_lib.mx_gemm_int8(a, sa, b, sb, out_dtype=dt), want, bound)
 
 
+# each kernel form once more at a size that takes it, whole and with k shared out
+# over workgroups (those need a workspace): rows per group, n, k
+FORMS = [([130], 6000, 64), ([67, 0, 133], 6000, 64), ([200], 6000, 272), ([100, 40, 60], 6000, 272), ([400], 12000, 144),
+         ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144)]
+SHARED = [([130], 100, 8192), ([130], 101, 8192), ([60, 0, 140], 1030, 4112), ([200], 2050, 4112), ([200], 2051, 4112),
+          ([130, 170, 100], 6000, 4112), ([3, 0, 0, 5], 48, 16384)]
+
+
+@pytest.mark.parametrize("sizes,n,k", FORMS + SHARED)
+def test_product_of_each_form(gpu_lib, sizes, n, k):
+    gen = torch.Generator().manual_seed(n + k)
+    G, m = len(sizes), sum(sizes)
+    a, b, sa, sb = _codes(gen, m, k), _codes(gen, G, n, k), _scales(gen, m), _scales(gen, G, n)
+    ends = np.cumsum([0] + sizes)
+    # sums of integers below 2^53: exact in 64 bits
+    want = torch.cat([(a[s:e].double() @ b[g].double().T.contiguous()) * sa[s:e].double()[:, None] * sb[g].double()
+                      for g, (s, e) in enumerate(zip(ends[:-1], ends[1:]))]).cpu().numpy()
+    nbytes = gpu_lib.gemm_int8_workspace_bytes(m, n, k, G)
+    assert (nbytes > 0) == ((sizes, n, k) in SHARED)
+    counts = torch.tensor(sizes, device="cuda")
+    for dt in (torch.bfloat16, torch.float32):
+        wbuf, ws = guarded((nbytes,), torch.uint8)
+        buf, out = guarded((m, n), dt)
+        gpu_lib.mx_grouped_gemm_int8(a, sa, b, sb, sizes, out=out, workspace=ws)
+        _close(out, want, 3.01 * ref.U * np.abs(want))
+        assert canaries_intact(buf) and canaries_intact(wbuf)
+        assert torch.equal(out, gpu_lib.mx_grouped_gemm_int8(a, sa, b, sb, counts, out_dtype=dt))
+        if G == 1:
+            assert torch.equal(out, gpu_lib.mx_gemm_int8(a, sa, b[0], sb[0], out_dtype=dt))
+    if nbytes:
+        with pytest.raises(gpu_lib.MXError):
+            gpu_lib.mx_grouped_gemm_int8(a, sa, b, sb, sizes, workspace=ws[:-1])
+
+
+def test_two_graphs_that_share_a_workspace(gpu_lib):
+    """Two products with k shared out, captured over one workspace, replayed in
+    turn with new inputs and eager calls in between."""
+    gen = torch.Generator().manual_seed(31)
+    shapes = [(130, 100, 8192), (64, 300, 8208)]
+    ws = torch.empty(max(gpu_lib.gemm_int8_workspace_bytes(*s) for s in shapes), dtype=torch.uint8, device="cuda")
+    assert all(gpu_lib.gemm_int8_workspace_bytes(*s) > 0 for s in shapes)
+    sets = [(_codes(gen, m, k), _scales(gen, m), _codes(gen, n, k), _scales(gen, n)) for m, n, k in shapes]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        gpu_lib.mx_gemm_int8(*sets[0], workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gpu_lib.mx_gemm_int8(*s, workspace=ws))
+        graphs.append(g)
+    for _ in range(4):
+        for s, g, out in zip(sets, graphs, outs):
+            s[0].copy_(_codes(gen, *s[0].shape))
+            g.replay()
+            want = gpu_lib.mx_gemm_int8(*s)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+
+
 def test_largest_sums(gpu_lib):
     """-128 times -128 summed over the longest k stays below 2^31."""
     for m, n in ((1, 3), (40, 70), (300, 300)):
@@ -217,7 +279,7 @@ def _mlp_ref(x, probs, w, sizes):
     return np.concatenate([o[0] for o in out]), np.concatenate([o[1] for o in out])
 
 
-MLPS = [([1], 32, 32), ([3, 0, 2], 64, 96), ([0, 40, 1, 33], 96, 160), ([130, 0, 257], 256, 224), ([600, 700], 128, 256),
+MLPS = [([70, 0, 60], 8192, 64), ([130], 64, 8192), ([1], 32, 32), ([3, 0, 2], 64, 96), ([0, 40, 1, 33], 96, 160), ([130, 0, 257], 256, 224), ([600, 700], 128, 256),
         ([1] * 16, 288, 64)]
 
 

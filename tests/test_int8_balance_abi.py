@@ -63,16 +63,16 @@ def test_cast_refusals(L):
 
 
 def test_product_refusals(L):
-    def one(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0):
-        return L.mx_gemm_int8(a, sa, b, sb, m, n, k, c, dt, None)
+    def one(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0, ws=None, nb=0):
+        return L.mx_gemm_int8(a, sa, b, sb, m, n, k, c, dt, ws, nb, None)
 
     sizes = (ctypes.c_int64 * 2)(2, 3)
 
-    def many(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0, sz=sizes, G=2):
-        return L.mx_grouped_gemm_int8(a, sa, b, sb, sz, G, m, n, k, c, dt, None)
+    def many(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0, sz=sizes, G=2, ws=None, nb=0):
+        return L.mx_grouped_gemm_int8(a, sa, b, sb, sz, G, m, n, k, c, dt, ws, nb, None)
 
-    def dev(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0, sz=FAKE, G=2):
-        return L.mx_grouped_gemm_int8_device_split(a, sa, b, sb, sz, G, m, n, k, c, dt, None)
+    def dev(a=FAKE, sa=FAKE, b=FAKE, sb=FAKE, m=5, n=7, k=64, c=FAKE, dt=0, sz=FAKE, G=2, ws=None, nb=0):
+        return L.mx_grouped_gemm_int8_device_split(a, sa, b, sb, sz, G, m, n, k, c, dt, ws, nb, None)
 
     for f in (one, many, dev):
         assert f(a=None) == f(sa=None) == f(b=None) == f(sb=None) == f(c=None) == f(dt=3) == EINVAL
@@ -82,6 +82,16 @@ def test_product_refusals(L):
         assert f(n=0, b=None) == OK
     assert one(m=-1) == ESHAPE and one(m=(1 << 30) + 1) == EUNSUPPORTED and one(m=0, a=None) == OK
     assert one(m=1 << 30, n=1 << 30) == EUNSUPPORTED
+    # a product that shares k out over workgroups needs its planes
+    n = ctypes.c_size_t()
+    assert L.mx_gemm_int8_sizes(16, 4096, 4096, 1, ctypes.byref(n)) == OK and n.value == 0
+    big = dict(m=64, n=4096, k=14336)
+    assert L.mx_gemm_int8_sizes(*big.values(), 1, ctypes.byref(n)) == OK and n.value % (64 * 4096 * 4) == 0 and n.value > 0
+    assert one(**big) == one(**big, nb=n.value) == EINVAL
+    assert one(**big, ws=FAKE, nb=n.value - 1) == EWORKSPACE
+    assert one(**big, ws=ctypes.c_void_p(0x100010), nb=n.value) == EALIGN
+    assert L.mx_gemm_int8_sizes(-1, 1, 16, 1, None) == L.mx_gemm_int8_sizes(1, 1, 24, 1, None) == ESHAPE
+    assert L.mx_gemm_int8_sizes(1, 1, 16, 0, None) == EINVAL and L.mx_gemm_int8_sizes(1, 1, 16, 129, None) == EUNSUPPORTED
     assert many(m=6) == many(sz=(ctypes.c_int64 * 2)(-1, 6)) == ESHAPE
     assert many(sz=None) == many(G=0) == dev(sz=None) == dev(G=0) == EINVAL
     assert many(G=129) == dev(G=129) == EUNSUPPORTED
