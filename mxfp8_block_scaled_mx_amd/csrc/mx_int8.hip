@@ -217,8 +217,8 @@ __device__ __forceinline__ int xcd_ids(int b, int total) {
   return full * 8 * CHUNK + xcd * (rest / 8) + min(xcd, rest % 8) + (l - full * CHUNK);
 }
 
-// silu(g) u. exp and the quotient are good to a few half steps of fp32.
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) u. exp and the reciprocal are good to a few half steps of fp32.
+__device__ __forceinline__ float swiglu(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
 // As vgpr_hop, for the integer sums.
 __device__ __forceinline__ int hop(int x) { return __builtin_amdgcn_mov_dpp(x, 0xE4, 0xF, 0xF, false); }
@@ -433,13 +433,33 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   const int cn0 = n0 + wn * kCols;             // the wave's first column of C
   const int64_t ldc = nrows;
   uint8_t* const c = reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * ldc * 4 : 0);
-  const float* const bs = a.b_s + (int64_t)g.group * a.N;
   const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
+  // the lane's column scales, 4 at a time (0 past the last), and its rows'
+  v4f sb[NI][4];
+  float sa[MI];
+  if constexpr (EPI != kInt8ToSums) {
+    const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_s + (int64_t)g.group * a.N + cn0, (int64_t)(nrows - cn0) * 4);
+    const __amdgpu_buffer_rsrc_t rus =
+        make_rsrc(a.b_s + (int64_t)g.group * a.N + nrows + cn0, kPair ? (int64_t)(nrows - cn0) * 4 : 0);
+    const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_s + row0, (int64_t)rows * 4);
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t at = (32 * (kPair ? j / 2 : j) + 8 * q + 4 * h) * 4;
+        const u32x4 w = kPair && (j & 1) ? __builtin_amdgcn_raw_buffer_load_b128(rus, at, 0, 0)
+                                         : __builtin_amdgcn_raw_buffer_load_b128(rbs, at, 0, 0);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sb[j][q][v] = __uint_as_float(w[v]);
+      }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+      sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (32 * (wm * MI + i) + l32) * 4, 0, 0));
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int m0 = 32 * (wm * MI + i);
     if (m0 >= rows) break;
-    const float sa = EPI == kInt8ToSums ? 0.f : a.a_s[row0 + min(m0 + l32, rows - 1)];
 #pragma unroll
     for (int j = 0; j < NI; j += kPair ? 2 : 1) {
 #pragma unroll
@@ -453,9 +473,8 @@ void gemm_int8_kernel(Int8GemmArgs a) {
           float y[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int n = min(cn0 + col + v, nrows - 1);
-            y[v] = (float)hop(acc[i][j][4 * q + v]) * sa * bs[n];
-            if constexpr (kPair) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa * bs[nrows + n]);
+            y[v] = (float)hop(acc[i][j][4 * q + v]) * sa[i] * sb[j][q][v];
+            if constexpr (kPair) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa[i] * sb[j + 1][q][v]);
           }
           if constexpr (kBytes == 4) {
             *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
