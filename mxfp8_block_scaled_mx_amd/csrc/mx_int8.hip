@@ -217,6 +217,30 @@ __device__ __forceinline__ int xcd_ids(int b, int total) {
   return full * 8 * CHUNK + xcd * (rest / 8) + min(xcd, rest % 8) + (l - full * CHUNK);
 }
 
+// A group's tile `local`, in bands of 8 m-tiles: the 32 tiles that run at once on
+// one XCD are 8 x 4.
+__device__ __forceinline__ void tile_of(int local, int ntn, int mtiles, int* mt, int* nt) {
+  const int band = local / (8 * ntn), in_band = local - band * 8 * ntn, height = min(8, mtiles - 8 * band);
+  *mt = 8 * band + in_band % height;
+  *nt = in_band / height;
+}
+
+// Tiles of 256 x 256 run 256 at a time, one a compute unit. Those of the last,
+// partial round (from id `first` on) are `parts` workgroups each, that share out
+// k, where that saves more than the sums' way through memory costs (a step takes
+// 1.45 us, a tile of sums 0.12 us to write and read, their join 8 us).
+constexpr int kTailUnits = 256;
+struct Tail {
+  int first, parts;
+};
+__host__ __device__ inline Tail tail_of(int64_t tiles, int steps) {
+  const int n = (int)(tiles % kTailUnits);
+  if (n == 0 || tiles < kTailUnits) return Tail{(int)tiles, 1};
+  const int parts = kTailUnits / n < steps / 4 ? kTailUnits / n : steps / 4;
+  if (parts < 2 || 1.45f * (steps - (steps + parts - 1) / parts) < 8.f + 0.12f * n * parts) return Tail{(int)tiles, 1};
+  return Tail{(int)tiles - n, parts};
+}
+
 // silu(g) u. exp and the reciprocal are good to a few half steps of fp32.
 __device__ __forceinline__ float swiglu(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
@@ -261,7 +285,7 @@ __device__ __forceinline__ void bare_barrier() {
 // With the SwiGLU, 32-row blocks of the B tile alternate between gate and up rows.
 // With parts > 1 each tile is several workgroups, each with its share of the
 // steps, that leave the sums themselves, in 32 bits, to planes of their own.
-template <int MI, int NI, int S, int EPI>
+template <int MI, int NI, int S, int EPI, bool TAIL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(64 * (MI + NI) * kBK * S <= 81920 ? 2 : 1)))
 void gemm_int8_kernel(Int8GemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -283,21 +307,33 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   const int ntn = a.n_tiles;
   GroupScan scan;
   scan_groups<BM>(a, &scan);
+  const int K = a.K, all_steps = (K + kBK - 1) / kBK;
   // a part's tiles are consecutive; the grid is sized for the worst split
-  const int tiles = (int)scan.total * ntn, all = tiles * a.parts;
-  if ((int)blockIdx.x >= all) return;
-  const int place = xcd_ids<MI * NI >= 16 ? 32 : 64>((int)blockIdx.x, all);
-  const int part = place / tiles, id = place - part * tiles;
+  const int tiles = (int)scan.total * ntn;
+  const Tail tail = TAIL ? tail_of(tiles, all_steps) : Tail{tiles, 1};
+  const int whole_ids = TAIL ? tail.first : tiles * a.parts;
+  int part, parts = a.parts, id, unit = -1;
+  if (!TAIL || (int)blockIdx.x < whole_ids) {
+    if ((int)blockIdx.x >= whole_ids) return;
+    const int place = xcd_ids<MI * NI >= 16 ? 32 : 64>((int)blockIdx.x, whole_ids);
+    part = place / (TAIL ? whole_ids : tiles);
+    id = place - part * tiles;
+  } else {
+    const int n = tiles - tail.first, u = (int)blockIdx.x - tail.first;
+    if (u >= n * tail.parts) return;
+    const int place = xcd_ids<32>(u, n * tail.parts);
+    part = place / n;
+    id = tail.first + place - part * n;
+    parts = tail.parts;
+    unit = parts > 1 ? place : -1;
+  }
   const GroupSpan g = group_of<BM>(a, scan, id / ntn);
-  const int local = id - g.tile0 * ntn;
-  // bands of 8 m-tiles: the 32 tiles that run at once on one XCD are 8 x 4
-  const int band = local / (8 * ntn), in_band = local - band * 8 * ntn, height = min(8, g.tiles - 8 * band);
-  const int mt = 8 * band + in_band % height, nt = in_band / height;
+  int mt, nt;
+  tile_of(id - g.tile0 * ntn, ntn, g.tiles, &mt, &nt);
   const int64_t row0 = g.row0 + (int64_t)mt * BM;
   const int rows = min(BM, g.rows - mt * BM);
-  const int K = a.K, all_steps = (K + kBK - 1) / kBK;
-  const int first = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * part / a.parts));
-  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * (part + 1) / a.parts)) - first;
+  const int first = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * part / parts));
+  const int nk = __builtin_amdgcn_readfirstlane((int)((int64_t)all_steps * (part + 1) / parts)) - first;
   const int nrows = kPair ? a.N / 2 : a.N;                 // rows of B that n-tiles cover (gate rows)
   constexpr int kTileRows = kPair ? BN / 2 : BN;
   const int n0 = nt * kTileRows, ncols = min(kTileRows, nrows - n0);
@@ -426,92 +462,118 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   // 4 h + 0 .. 3 of its columns; by 32 rows through LDS of the wave's own.
   __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
   __syncthreads();
-  constexpr int kBytes = EPI == kInt8ToBf16 ? 2 : 4, kCols = (kPair ? 16 : 32) * NI, kRowBytes = kCols * kBytes;
-  constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes, kMask = kChunks < 16 ? kChunks - 1 : 15;
-  static_assert(32 * kRowBytes <= BM * kBK && 32 * kRowBytes <= BN * kBK, "32 rows of results fit one stage of one operand");
   uint8_t* const stage = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
-  const int cn0 = n0 + wn * kCols;             // the wave's first column of C
-  const int64_t ldc = nrows;
-  uint8_t* const c = reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * ldc * 4 : 0);
-  const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
-  // the lane's column scales, 4 at a time (0 past the last), and its rows'
-  v4f sb[NI][4];
-  float sa[MI];
-  if constexpr (EPI != kInt8ToSums) {
-    const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_s + (int64_t)g.group * a.N + cn0, (int64_t)(nrows - cn0) * 4);
-    const __amdgpu_buffer_rsrc_t rus =
-        make_rsrc(a.b_s + (int64_t)g.group * a.N + nrows + cn0, kPair ? (int64_t)(nrows - cn0) * 4 : 0);
-    const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_s + row0, (int64_t)rows * 4);
+  auto finish = [&](auto epi_, uint8_t* c, int64_t ldc, int64_t crow0, int cn0, int crows, int ccols)
+      __attribute__((always_inline)) {
+    constexpr int E = decltype(epi_)::value;
+    constexpr bool kTwo = E == kInt8ToSwiglu;
+    constexpr int kBytes = E == kInt8ToBf16 ? 2 : 4, kCols = (kTwo ? 16 : 32) * NI, kRowBytes = kCols * kBytes;
+    constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes, kMask = kChunks < 16 ? kChunks - 1 : 15;
+    static_assert(32 * kRowBytes <= BM * kBK && 32 * kRowBytes <= BN * kBK, "32 rows of results fit one stage of one operand");
+    cn0 += wn * kCols;                         // the wave's first column
+    const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
+    // the lane's column scales, 4 at a time (0 past the last), and its rows'
+    v4f sb[NI][4];
+    float sa[MI];
+    if constexpr (E != kInt8ToSums) {
+      const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_s + (int64_t)g.group * a.N + cn0, (int64_t)(nrows - cn0) * 4);
+      const __amdgpu_buffer_rsrc_t rus =
+          make_rsrc(a.b_s + (int64_t)g.group * a.N + nrows + cn0, kTwo ? (int64_t)(nrows - cn0) * 4 : 0);
+      const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_s + row0, (int64_t)rows * 4);
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
+      for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t at = (32 * (kPair ? j / 2 : j) + 8 * q + 4 * h) * 4;
-        const u32x4 w = kPair && (j & 1) ? __builtin_amdgcn_raw_buffer_load_b128(rus, at, 0, 0)
-                                         : __builtin_amdgcn_raw_buffer_load_b128(rbs, at, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t at = (32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h) * 4;
+          const u32x4 w = kTwo && (j & 1) ? __builtin_amdgcn_raw_buffer_load_b128(rus, at, 0, 0)
+                                          : __builtin_amdgcn_raw_buffer_load_b128(rbs, at, 0, 0);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sb[j][q][v] = __uint_as_float(w[v]);
-      }
+          for (int v = 0; v < 4; ++v) sb[j][q][v] = __uint_as_float(w[v]);
+        }
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-      sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (32 * (wm * MI + i) + l32) * 4, 0, 0));
-  }
+      for (int i = 0; i < MI; ++i)
+        sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (32 * (wm * MI + i) + l32) * 4, 0, 0));
+    }
 #pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m0 = 32 * (wm * MI + i);
-    if (m0 >= rows) break;
+    for (int i = 0; i < MI; ++i) {
+      const int m0 = 32 * (wm * MI + i);
+      if (m0 >= crows) break;
 #pragma unroll
-    for (int j = 0; j < NI; j += kPair ? 2 : 1) {
+      for (int j = 0; j < NI; j += kTwo ? 2 : 1) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = 32 * (kPair ? j / 2 : j) + 8 * q + 4 * h;
-        uint8_t* const at = stage + l32 * kRowBytes + (((col / kPer) ^ (l32 & kMask)) << 4);
-        if constexpr (EPI == kInt8ToSums) {
-          *reinterpret_cast<v4i*>(at) = v4i{hop(acc[i][j][4 * q]), hop(acc[i][j][4 * q + 1]), hop(acc[i][j][4 * q + 2]),
-                                            hop(acc[i][j][4 * q + 3])};
-        } else {
-          float y[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            y[v] = (float)hop(acc[i][j][4 * q + v]) * sa[i] * sb[j][q][v];
-            if constexpr (kPair) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa[i] * sb[j + 1][q][v]);
-          }
-          if constexpr (kBytes == 4) {
-            *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+        for (int q = 0; q < 4; ++q) {
+          const int col = 32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h;
+          uint8_t* const at = stage + l32 * kRowBytes + (((col / kPer) ^ (l32 & kMask)) << 4);
+          if constexpr (E == kInt8ToSums) {
+            *reinterpret_cast<v4i*>(at) = v4i{hop(acc[i][j][4 * q]), hop(acc[i][j][4 * q + 1]), hop(acc[i][j][4 * q + 2]),
+                                              hop(acc[i][j][4 * q + 3])};
           } else {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+            float y[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              y[v] = (float)hop(acc[i][j][4 * q + v]) * sa[i] * sb[j][q][v];
+              if constexpr (kTwo) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa[i] * sb[j + 1][q][v]);
+            }
+            if constexpr (kBytes == 4) {
+              *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+            } else {
+              typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+              *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+            }
           }
         }
       }
-    }
-    // the wave's own LDS: its writes are done before its reads (no barrier)
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    if (whole) {
+      // the wave's own LDS: its writes are done before its reads (no barrier)
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (whole) {
 #pragma unroll
-      for (int u = 0; u < 32 * kChunks / 64; ++u) {
-        const int r = (u * 64 + lane) / kChunks, ch = (u * 64 + lane) % kChunks, n = cn0 + ch * kPer;
-        const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
-        if (m0 + r < rows && n < nrows) *reinterpret_cast<uint4*>(c + ((row0 + m0 + r) * ldc + n) * kBytes) = w;
-      }
-    } else {
-      for (int u = lane; u < 32 * kCols; u += 64) {
-        const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
-        const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
-        if (m0 + r < rows && n < nrows) {
-          const int64_t at = (row0 + m0 + r) * ldc + n;
-          if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
-          else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
+        for (int u = 0; u < 32 * kChunks / 64; ++u) {
+          const int r = (u * 64 + lane) / kChunks, ch = (u * 64 + lane) % kChunks, n = cn0 + ch * kPer;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
+          if (m0 + r < crows && n < ccols) *reinterpret_cast<uint4*>(c + ((crow0 + m0 + r) * ldc + n) * kBytes) = w;
+        }
+      } else {
+        for (int u = lane; u < 32 * kCols; u += 64) {
+          const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
+          const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
+          if (m0 + r < crows && n < ccols) {
+            const int64_t at = (crow0 + m0 + r) * ldc + n;
+            if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
+            else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
+          }
         }
       }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
+  };
+  if (TAIL && unit >= 0)                       // a tile of sums, rows past the valid ones left out
+    finish(std::integral_constant<int, kInt8ToSums>{}, reinterpret_cast<uint8_t*>(a.planes + (int64_t)unit * BM * BN), BN, 0,
+           0, rows, BN);
+  else
+    finish(std::integral_constant<int, EPI>{},
+           reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * nrows * 4 : 0), nrows, row0, n0,
+           rows, nrows);
 #endif
+}
+
+// Four sums of a row from column n on as results (bs: their column scales).
+template <int EPI>
+__device__ __forceinline__ void finish_four(const Int8GemmArgs& a, int64_t row, int n, int cols, v4i sum, v4i up,
+                                            const float* bs) {
+  const float sa = a.a_s[row];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= cols) break;
+    const int64_t at = row * cols + n + i;
+    const float y = (float)sum[i] * sa * bs[i];
+    if constexpr (EPI == kInt8ToSwiglu) reinterpret_cast<float*>(a.c)[at] = swiglu(y, (float)up[i] * sa * bs[cols + i]);
+    else if constexpr (EPI == kInt8ToF32) reinterpret_cast<float*>(a.c)[at] = y;
+    else reinterpret_cast<__bf16*>(a.c)[at] = (__bf16)y;
+  }
 }
 
 // The planes of a product whose steps were shared out, added up and finished: row
@@ -550,16 +612,43 @@ __global__ __launch_bounds__(256) void int8_join_kernel(Int8GemmArgs a) {
           if constexpr (EPI == kInt8ToSwiglu) up[i] += from[p * plane + cols + i];
         }
   }
-  const float sa = a.a_s[row];
-  const float* const bs = a.b_s + (int64_t)g.group * a.N + n;
+  finish_four<EPI>(a, row, n, cols, v4i{sum[0], sum[1], sum[2], sum[3]}, v4i{up[0], up[1], up[2], up[3]},
+                   a.b_s + (int64_t)g.group * a.N + n);
+}
+
+// The tail's tiles of sums added up and finished: 16 rows of tail tile blockIdx.x /
+// 16, 4 columns a thread.
+template <int EPI>
+__global__ __launch_bounds__(256) void int8_tail_join_kernel(Int8GemmArgs a) {
+  constexpr bool kPair = EPI == kInt8ToSwiglu;
+  GroupScan scan;
+  scan_groups<256>(a, &scan);
+  const int ntn = a.n_tiles, tiles = (int)scan.total * ntn;
+  const Tail tail = tail_of(tiles, (a.K + kBK - 1) / kBK);
+  const int t = blockIdx.x >> 4, n = tiles - tail.first;
+  if (t >= n || tail.parts < 2) return;
+  const int id = tail.first + t;
+  const GroupSpan g = group_of<256>(a, scan, id / ntn);
+  int mt, nt;
+  tile_of(id - g.tile0 * ntn, ntn, g.tiles, &mt, &nt);
+  const int cols = kPair ? a.N / 2 : a.N, c = (threadIdx.x & 63) * 4;
+  if (kPair && c >= 128) return;
+  const int col = (kPair ? 128 : 256) * nt + c, from = kPair ? 64 * (c / 32) + c % 32 : c;
+  if (col >= cols) return;
+  const float* const bs = a.b_s + (int64_t)g.group * a.N + col;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= cols) break;
-    const int64_t at = (int64_t)row * cols + n + i;
-    const float y = (float)sum[i] * sa * bs[i];
-    if constexpr (EPI == kInt8ToSwiglu) reinterpret_cast<float*>(a.c)[at] = swiglu(y, (float)up[i] * sa * bs[cols + i]);
-    else if constexpr (EPI == kInt8ToF32) reinterpret_cast<float*>(a.c)[at] = y;
-    else reinterpret_cast<__bf16*>(a.c)[at] = (__bf16)y;
+  for (int r = 0; r < 4; ++r) {
+    const int m = (blockIdx.x & 15) * 16 + 4 * r + (threadIdx.x >> 6);
+    if (mt * 256 + m >= g.rows) break;
+    v4i sum = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int p = 0; p < tail.parts; ++p) {
+      const int* const at = a.planes + ((int64_t)(p * n + t) * 256 + m) * 256 + from;
+      sum += *reinterpret_cast<const v4i*>(at);
+      if constexpr (kPair) up += *reinterpret_cast<const v4i*>(at + 32);
+    }
+    const int64_t row = g.row0 + (int64_t)mt * 256 + m;
+    finish_four<EPI>(a, row, col, cols, sum, up, bs);
   }
 }
 
@@ -715,8 +804,16 @@ struct Tile {
   static constexpr bool kPairs = NI % 2 == 0, kSums = true;
   template <int EPI>
   static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
-    if constexpr (EPI != kInt8ToSwiglu || kPairs)
-      hipLaunchKernelGGL((gemm_int8_kernel<MI, NI, S, EPI>), grid, dim3(kThreads), 0, s, a);
+    if constexpr (EPI != kInt8ToSwiglu || kPairs) {
+      if constexpr (MI * NI >= 16 && EPI != kInt8ToSums) {
+        if (a.tail) {
+          hipLaunchKernelGGL((gemm_int8_kernel<MI, NI, S, EPI, true>), grid, dim3(kThreads), 0, s, a);
+          hipLaunchKernelGGL(int8_tail_join_kernel<EPI>, dim3(16 * kTailUnits / 2), dim3(256), 0, s, a);
+          return;
+        }
+      }
+      hipLaunchKernelGGL((gemm_int8_kernel<MI, NI, S, EPI, false>), grid, dim3(kThreads), 0, s, a);
+    }
   }
 };
 constexpr int kForms = 10;
@@ -796,9 +893,17 @@ Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
         if (parts > 1 && (steps / parts < 4 || a.M > 65535 || (int64_t)parts * a.M * a.N > ((int64_t)1 << 26))) break;
         const int64_t bn = half ? Form::kBN / 2 : Form::kBN, cols = half ? a.N / 2 : a.N;
         const double wgs = (double)mtiles * ((cols + bn - 1) / bn) * parts;
-        const double c = std::ceil(wgs / 256);
+        double c = std::ceil(wgs / 256), more = 0;
+        if (form == kForms - 1 && parts == 1) {   // (the last round's tiles may share out k too)
+          const Tail tail = tail_of((int64_t)wgs, steps);
+          if (tail.parts > 1) {
+            c = tail.first / 256 + 1.0 / tail.parts;
+            more = 8 + 0.12 * (wgs - tail.first) * tail.parts;
+          }
+        }
         const double mine = std::ceil((double)steps / (Form::kWaves * parts)) * (a.K % kBK ? cost.ragged : 1.f);
         double us = std::max(2.5 + mine * std::max((double)cost.alone, c * cost.among) + c * cost.tile, weights / cost.rate);
+        us += more;
         if (parts > 1) us += 3.0 + (double)parts * a.M * a.N * 8 / 4.5e6;  // the planes, written and read
         if (us < best_us) {
           best_us = us;
@@ -823,6 +928,16 @@ Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
     best.tiles = mtiles * best.n_tiles;
   });
   best.workspace = best.parts > 1 ? (size_t)best.parts * a.M * a.N * 4 : 0;
+  best.tail = 0;
+  if (best.form == kForms - 1 && best.parts == 1) {
+    // a tail: of these tiles, or with groups of any that their rows can make
+    best.tail = (int64_t)a.M * a.N > ((int64_t)1 << 24) && tail_of(kTailUnits + 1, steps).parts > 1;
+    if (a.split != kInt8DeviceSizes) best.tail = best.tail && tail_of(best.tiles, steps).parts > 1;
+    if (best.tail) {
+      best.tiles = (best.tiles + kTailUnits - 1) / kTailUnits * kTailUnits;
+      best.workspace = (size_t)kTailUnits * 256 * 256 * 4;
+    }
+  }
   return best;
 }
 
@@ -830,6 +945,7 @@ hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan
   Int8GemmArgs a = args;
   a.n_tiles = (int32_t)p.n_tiles;
   a.parts = p.parts;
+  a.tail = p.tail;
   a.planes = reinterpret_cast<int32_t*>(workspace);
   a.once = a.K % kBK == 0;
   if (p.tiles == 0) return hipSuccess;

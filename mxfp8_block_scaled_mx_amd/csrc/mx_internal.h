@@ -413,14 +413,15 @@ struct Int8GemmArgs {
   int32_t M, N, K, groups, split;
   const int64_t* sizes_dev;
   int32_t sizes[kMaxGroups];
-  int32_t n_tiles, parts, once;     // set by the launch, as is
-  int32_t* planes;                  // [parts, M, N] sums (parts > 1)
+  int32_t n_tiles, parts, tail, once;   // set by the launch, as is
+  int32_t* planes;                  // sums: [parts, M, N] (parts > 1), or tiles of the tail's
 };
 enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2, kInt8ToSums = 3 };
 // How a product runs: the kernel's form, and its workgroups (at most kInt8MaxTiles:
 // a launch has fewer than 2^32 threads along x).
 struct Int8Plan {
   int32_t form, parts;              // parts > 1: k is shared out over workgroups
+  int32_t tail;                     // or may be for the tiles of the last round
   int64_t n_tiles, tiles;
   size_t workspace;                 // bytes of its planes
 };

@@ -137,9 +137,11 @@ FORMS = [([130], 6000, 64), ([67, 0, 133], 6000, 64), ([200], 6000, 272), ([100,
          ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144)]
 SHARED = [([130], 100, 8192), ([130], 101, 8192), ([60, 0, 140], 1030, 4112), ([200], 2050, 4112), ([200], 2051, 4112),
           ([130, 170, 100], 6000, 4112), ([3, 0, 0, 5], 48, 16384)]
+# ... and for the tiles of the last round alone
+TAILS = [([4000], 4300, 4096), ([1000, 0, 3100], 4301, 2064), ([4100], 4096, 4096)]
 
 
-@pytest.mark.parametrize("sizes,n,k", FORMS + SHARED)
+@pytest.mark.parametrize("sizes,n,k", FORMS + SHARED + TAILS)
 def test_product_of_each_form(gpu_lib, sizes, n, k):
     gen = torch.Generator().manual_seed(n + k)
     G, m = len(sizes), sum(sizes)
@@ -149,7 +151,7 @@ def test_product_of_each_form(gpu_lib, sizes, n, k):
     want = torch.cat([(a[s:e].double() @ b[g].double().T.contiguous()) * sa[s:e].double()[:, None] * sb[g].double()
                       for g, (s, e) in enumerate(zip(ends[:-1], ends[1:]))]).cpu().numpy()
     nbytes = gpu_lib.gemm_int8_workspace_bytes(m, n, k, G)
-    assert (nbytes > 0) == ((sizes, n, k) in SHARED)
+    assert (nbytes > 0) == ((sizes, n, k) in SHARED + TAILS)
     counts = torch.tensor(sizes, device="cuda")
     for dt in (torch.bfloat16, torch.float32):
         wbuf, ws = guarded((nbytes,), torch.uint8)
@@ -162,7 +164,7 @@ def test_product_of_each_form(gpu_lib, sizes, n, k):
             assert torch.equal(out, gpu_lib.mx_gemm_int8(a, sa, b[0], sb[0], out_dtype=dt))
     if nbytes:
         with pytest.raises(gpu_lib.MXError):
-            gpu_lib.mx_grouped_gemm_int8(a, sa, b, sb, sizes, workspace=ws[:-1])
+            gpu_lib.mx_grouped_gemm_int8(a, sa, b, sb, counts, workspace=ws[:-1])
 
 
 def test_two_graphs_that_share_a_workspace(gpu_lib):
@@ -279,8 +281,8 @@ def _mlp_ref(x, probs, w, sizes):
     return np.concatenate([o[0] for o in out]), np.concatenate([o[1] for o in out])
 
 
-MLPS = [([70, 0, 60], 8192, 64), ([130], 64, 8192), ([1], 32, 32), ([3, 0, 2], 64, 96), ([0, 40, 1, 33], 96, 160), ([130, 0, 257], 256, 224), ([600, 700], 128, 256),
-        ([1] * 16, 288, 64)]
+MLPS = [([70, 0, 60], 8192, 64), ([130], 64, 8192), ([1], 32, 32), ([3, 0, 2], 64, 96), ([0, 40, 1, 33], 96, 160),
+        ([130, 0, 257], 256, 224), ([600, 700], 128, 256), ([1] * 16, 288, 64), ([2300], 4096, 3712), ([1500, 0, 2600], 4096, 2176)]
 
 
 @pytest.mark.parametrize("sizes,H,F", MLPS)
