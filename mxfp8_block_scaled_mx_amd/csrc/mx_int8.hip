@@ -148,59 +148,68 @@ struct GroupSpan {
 // count below 0 reads as 0, and one that would take the running sum past M is cut
 // there.
 struct GroupScan {
-  int64_t first[2], tend[2];                 // of lane's groups: first row, m-tiles up to its end
-  int rows[2], tiles[2];
-  int64_t total;                             // m-tiles of all groups
+  int first[2], rows[2], tend[2], tiles[2];  // of lane's groups: first row, rows, m-tiles up to its end, its own
+  int total;                                 // m-tiles of all groups
 };
-__device__ __forceinline__ int64_t scan64(int64_t v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int64_t o = __shfl_up(v, m, 64);
-    if ((int)(threadIdx.x & 63) >= m) v += o;
-  }
-  return v;
+// Sums over the lanes up to each lane, cut at `most` (no sum of two below 2^31
+// passes 2^32, and cutting every partial sum cuts the whole): within rows of 16
+// lanes, then each row's last on to the next, then lane 31's to the upper half.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t add_from(uint32_t v, uint32_t most) {
+  const uint32_t s = v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  return s < most ? s : most;
+}
+__device__ __forceinline__ uint32_t scan_cut(uint32_t v, uint32_t most) {
+  v = add_from<0x111, 0xF>(v, most);           // row_shr 1, 2, 4, 8
+  v = add_from<0x112, 0xF>(v, most);
+  v = add_from<0x114, 0xF>(v, most);
+  v = add_from<0x118, 0xF>(v, most);
+  v = add_from<0x142, 0xA>(v, most);           // row_bcast 15 into rows 1 and 3
+  return add_from<0x143, 0xC>(v, most);        // row_bcast 31 into rows 2 and 3
 }
 template <int BM>
 __device__ __forceinline__ void scan_groups(const Int8GemmArgs& a, GroupScan* s) {
   if (a.split == kInt8OneGroup) {
-    s->total = ((int64_t)a.M + BM - 1) / BM;
+    s->total = (int)(((int64_t)a.M + BM - 1) / BM);
     return;
   }
   const int lane = threadIdx.x & 63;
-  int64_t rows0 = 0;
-  s->total = 0;
+  const uint32_t M = (uint32_t)a.M;
+  uint32_t rows0 = 0, tiles0 = 0;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    s->rows[u] = s->tiles[u] = 0;
-    s->first[u] = s->tend[u] = 0;
-    if (64 * u >= a.groups) break;           // (uniform)
+    s->rows[u] = s->tiles[u] = s->first[u] = s->tend[u] = 0;
+    if (64 * u >= a.groups) break;             // (uniform)
     const int i = 64 * u + lane;
     int64_t c = 0;
     if (i < a.groups) c = a.split == kInt8DeviceSizes ? a.sizes_dev[i] : (int64_t)a.sizes[i];
-    c = min(max(c, (int64_t)0), (int64_t)a.M);
-    const int64_t end = rows0 + scan64(c), m = a.M;
-    s->first[u] = min(end - c, m);
-    s->rows[u] = (int)(min(end, m) - s->first[u]);
-    s->tiles[u] = (int)(((int64_t)s->rows[u] + BM - 1) / BM);
-    s->tend[u] = s->total + scan64(s->tiles[u]);
-    rows0 = __shfl(end, 63, 64);
-    s->total = __shfl(s->tend[u], 63, 64);
+    const uint32_t mine = (uint32_t)min(max(c, (int64_t)0), (int64_t)M);
+    const uint32_t upto = scan_cut(mine, M), end = min(rows0 + upto, M);
+    // the rows before: what the lane below has come to
+    const uint32_t below = (uint32_t)__shfl_up((int)end, 1, 64), from = lane == 0 ? rows0 : below;
+    s->first[u] = (int)from;
+    s->rows[u] = (int)(end - from);
+    s->tiles[u] = (int)((end - from + BM - 1) / BM);
+    s->tend[u] = (int)(tiles0 + scan_cut((uint32_t)s->tiles[u], 0x7FFFFFFFu));
+    rows0 = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    tiles0 = (uint32_t)__builtin_amdgcn_readlane(s->tend[u], 63);
   }
+  s->total = (int)tiles0;
 }
 // The group that holds m-tile mt < total.
 template <int BM>
-__device__ __forceinline__ GroupSpan group_of(const Int8GemmArgs& a, const GroupScan& s, int64_t mt) {
-  if (a.split == kInt8OneGroup) return GroupSpan{0, 0, (int)s.total, 0, a.M};
+__device__ __forceinline__ GroupSpan group_of(const Int8GemmArgs& a, const GroupScan& s, int mt) {
+  if (a.split == kInt8OneGroup) return GroupSpan{0, 0, s.total, 0, a.M};
   GroupSpan g = {};
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint64_t here = __ballot(mt >= s.tend[u] - s.tiles[u] && mt < s.tend[u]);
     if (here) {
-      const int src = __ffsll((unsigned long long)here) - 1;
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)here) - 1);
       g.group = 64 * u + src;
       g.tiles = __builtin_amdgcn_readlane(s.tiles[u], src);
-      g.tile0 = (int)__shfl(s.tend[u], src, 64) - g.tiles;
-      g.row0 = __shfl(s.first[u], src, 64);
+      g.tile0 = __builtin_amdgcn_readlane(s.tend[u], src) - g.tiles;
+      g.row0 = __builtin_amdgcn_readlane(s.first[u], src);
       g.rows = __builtin_amdgcn_readlane(s.rows[u], src);
     }
   }
@@ -309,7 +318,7 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   scan_groups<BM>(a, &scan);
   const int K = a.K, all_steps = (K + kBK - 1) / kBK;
   // a part's tiles are consecutive; the grid is sized for the worst split
-  const int tiles = (int)scan.total * ntn;
+  const int tiles = scan.total * ntn;
   const Tail tail = TAIL ? tail_of(tiles, all_steps) : Tail{tiles, 1};
   const int whole_ids = TAIL ? tail.first : tiles * a.parts;
   int part, parts = a.parts, id, unit = -1;
@@ -623,7 +632,7 @@ __global__ __launch_bounds__(256) void int8_tail_join_kernel(Int8GemmArgs a) {
   constexpr bool kPair = EPI == kInt8ToSwiglu;
   GroupScan scan;
   scan_groups<256>(a, &scan);
-  const int ntn = a.n_tiles, tiles = (int)scan.total * ntn;
+  const int ntn = a.n_tiles, tiles = scan.total * ntn;
   const Tail tail = tail_of(tiles, (a.K + kBK - 1) / kBK);
   const int t = blockIdx.x >> 4, n = tiles - tail.first;
   if (t >= n || tail.parts < 2) return;
