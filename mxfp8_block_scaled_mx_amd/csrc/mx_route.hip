@@ -246,6 +246,14 @@ __global__ __launch_bounds__(256) void route_bwd_kernel(RouteBwdArgs a) {
 // gradient, and that of the means P themselves, is
 //     dz_te = p_te / n (A_e - sum_j p_tj A_j),   A_e = dloss E c_e / (k n) + dP_e.
 
+// Part i of n items (below 2^27) in whole multiples of `step`: [first, last). In
+// 32 bits, since a division of 64 takes as long as a row of a token.
+__device__ __forceinline__ void part_of(uint32_t n, uint32_t parts, uint32_t i, uint32_t step, int64_t* first, int64_t* last) {
+  const uint32_t size = (n + parts * step - 1) / (parts * step) * step;
+  *first = min(i * size, n);
+  *last = min((i + 1) * size, n);
+}
+
 // The tokens [begin, end) of sequence s; offsets outside 0 .. tokens, or that
 // fall, are cut so that no token outside the arrays is named.
 struct Span {
@@ -255,6 +263,53 @@ __device__ __forceinline__ Span span_of(const int32_t* segments, int s, int64_t 
   if (segments == nullptr) return Span{0, tokens};
   const int64_t b = min(max((int64_t)segments[s], (int64_t)0), tokens);
   return Span{b, min(max((int64_t)segments[s + 1], b), tokens)};
+}
+
+// A lane's V values of a row as loaded. The loads are unconditional, from clamped
+// addresses, so that those of several rows are in flight together: one under a
+// condition is waited for where its branch joins again.
+template <int V, bool F32, bool VEC>
+__device__ __forceinline__ void load_raw(const void* p, int64_t row, int e0, int E, uint32_t (&w)[V]) {
+  if constexpr (V == 4 && VEC) {
+    const int64_t at = row + min(e0, E - 4);
+    if constexpr (F32) {
+      const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + at);
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[V - 1] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(p) + at);
+      w[0] = v.x; w[1] = v.y;                 // two to a word: unpacked by value_of
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int64_t at = row + min(e0 + i, E - 1);
+      w[i] = F32 ? reinterpret_cast<const uint32_t*>(p)[at] : (uint32_t) reinterpret_cast<const uint16_t*>(p)[at] << 16;
+    }
+  }
+}
+template <int V, bool F32, bool VEC>
+__device__ __forceinline__ float value_of(const uint32_t (&w)[V], int i) {
+  if constexpr (V == 4 && VEC && !F32) return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  else return __uint_as_float(w[i]);
+}
+// Its logits, shut ones -inf, with the lane's biases (0 without).
+template <int V, bool F32, bool VEC>
+__device__ __forceinline__ void open_logits(const uint32_t (&w)[V], const float (&bias)[V], int e0, int E, float (&z)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float x = value_of<V, F32, VEC>(w, v);
+    z[v] = e0 + v < E && x + bias[v] > kShut ? x : kShut;
+  }
+}
+
+// e^x for x <= 0, good to two half steps: 2^t with t = x log2(e) rounded, times 1 + r
+// ln 2 with r what the rounding left out (the hardware's 2^t alone would be off by
+// |x| half steps more).
+__device__ __forceinline__ float exp_below(float x) {
+  x = fmaxf(x, -200.f);                                   // (0 from there on; the products below stay finite)
+  constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
+  const float t = x * kLog2e, r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t)), e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * kLn2, e);
 }
 
 // The row's softmax over the open experts (0 for shut ones, and for all where
@@ -268,11 +323,11 @@ __device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) 
   float sum = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    p[v] = z[v] > kShut ? expf(z[v] - zm) : 0.f;
+    p[v] = z[v] > kShut ? exp_below(z[v] - zm) : 0.f;
     sum += p[v];
   }
   sum = group_sum<G>(sum);
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] *= inv;
 }
@@ -299,31 +354,49 @@ __device__ __forceinline__ void balance_results(const BalanceArgs& a, int s, int
 // results where a sequence is one part, else to the workspace. The sums are kept
 // in 64 bits: in 32 they would stand still past 2^24 tokens, and the few adds a
 // token hide behind its loads.
-template <int G, int V, bool F32>
+template <int G, int V, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs a) {
-  constexpr int N = 256 / G;                              // tokens at a time
+  constexpr int N = 256 / G, U = 4;                       // tokens at a time, and rows of a lane in flight
   __shared__ double probs[N][G * V];
   __shared__ double prob[G * V];
   __shared__ int count[G * V];
-  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y, tid = threadIdx.x;
+  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y, tid = threadIdx.x, E = a.experts;
   const Span sp = span_of(a.segments, s, a.tokens);
   const int64_t n = sp.end - sp.begin, parts = gridDim.x;
-  const int64_t t0 = sp.begin + n * blockIdx.x / parts, t1 = sp.begin + n * (blockIdx.x + 1) / parts;
+  int64_t t0, t1;
+  part_of((uint32_t)n, gridDim.x, blockIdx.x, N, &t0, &t1);
+  t0 += sp.begin;
+  t1 += sp.begin;
+  double acc[V];
+  float bias[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    acc[v] = 0.0;
+    bias[v] = a.bias != nullptr ? a.bias[min(e0 + v, E - 1)] : 0.f;
+  }
   if (tid < G * V) count[tid] = 0;
   __syncthreads();
-  for (int64_t i = t0 * a.topk + tid; i < t1 * a.topk; i += 256) {
-    const int e = a.topk_idx[i];
-    if (e >= 0 && e < a.experts) atomicAdd(&count[e], 1); // integers: any order gives the same sum
-  }
-  double acc[V];
+  if (t0 < t1) {
+    int64_t i = t0 * a.topk + tid;
+    for (int64_t t = t0 + tid / G; t - tid / G < t1; t += U * N) {
+      uint32_t w[U][V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) acc[v] = 0.0;
-  for (int64_t t = t0 + tid / G; t < t1; t += N) {
-    float z[V], key[V], p[V];
-    load_row<V, F32>(a.logits, a.bias, t, a.experts, e0, a.vec, z, key);
-    row_softmax<G, V>(z, p);
+      for (int u = 0; u < U; ++u) load_raw<V, F32, VEC>(a.logits, min(t + u * N, t1 - 1) * E, e0, E, w[u]);
+      // the choices of these rows, while they travel (integers: any order gives the same sum)
+      for (const int64_t end = min(t - tid / G + U * N, t1) * a.topk; i < end; i += 256) {
+        const int e = a.topk_idx[i];
+        if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+      }
 #pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] += (double)p[v];
+      for (int u = 0; u < U; ++u) {
+        if (t - tid / G + u * N >= t1) break;             // (uniform)
+        float z[V], p[V];
+        open_logits<V, F32, VEC>(w[u], bias, e0, E, z);
+        row_softmax<G, V>(z, p);
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += t + u * N < t1 ? (double)p[v] : 0.0;
+      }
+    }
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) probs[tid / G][e0 + v] = acc[v];
@@ -386,70 +459,73 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a) {
 // A is made once a workgroup, in 64 bits, less its mean over the experts: since
 // the p of a row sum to 1 the gradient does not see the shift, and the
 // difference A_e - sum p A loses fewer bits.
-template <int G, int V, bool F32>
+template <int G, int V, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
-  constexpr int N = 256 / G;
-  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y;
+  constexpr int N = 256 / G, U = 4;
+  const int gl = (threadIdx.x & 63) % G, e0 = gl * V, s = blockIdx.y, E = a.experts, mine = threadIdx.x / G;
   const bool gap = s >= a.sequences;
   Span sp;
-  int64_t n, skip = 0, skip_at = 0;                       // the gap: token u, or past skip_at, u + skip
+  int64_t n, skip = 0, skip_at = a.tokens;                // the gap: token u, or from skip_at on u + skip
   if (gap) {
     const int64_t first = min(max((int64_t)a.segments[0], (int64_t)0), a.tokens);
     const int64_t last = min(max((int64_t)a.segments[a.sequences], first), a.tokens);
     sp = Span{0, first + a.tokens - last};
     skip_at = first;
     skip = last - first;
-    n = sp.end;
   } else {
     sp = span_of(a.segments, s, a.tokens);
-    n = sp.end - sp.begin;
-    skip_at = a.tokens;
   }
-  const int64_t u0 = sp.begin + n * blockIdx.x / gridDim.x, u1 = sp.begin + n * (blockIdx.x + 1) / gridDim.x;
+  n = sp.end - sp.begin;
+  int64_t u0, u1;
+  part_of((uint32_t)n, gridDim.x, blockIdx.x, N, &u0, &u1);
+  u0 += sp.begin;
+  u1 += sp.begin;
   if (u0 >= u1) return;
-  float A[V];
+  const void* const add = a.add != nullptr ? a.add : a.logits;           // (read and not used without)
+  uint32_t w[U][V], d[U][V];
+  auto fetch = [&](int64_t u) __attribute__((always_inline)) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = 0.f;
-  if (!gap) {
-    double w[V], sum = 0.0;
-    const double f = a.dloss != nullptr ? (double)a.dloss[s] * a.experts / ((double)a.topk * (double)n) : 0.0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      w[v] = 0.0;
-      if (e0 + v < a.experts) {
-        const int64_t at = (int64_t)s * a.experts + e0 + v;
-        if (a.dloss != nullptr) w[v] = f * (double)a.counts[at];
-        if (a.dmean_prob != nullptr) w[v] += (double)a.dmean_prob[at];
-      }
-      sum += w[v];
+    for (int i = 0; i < U; ++i) {
+      const int64_t uc = min(u + mine + i * N, u1 - 1), row = (uc < skip_at ? uc : uc + skip) * E;
+      load_raw<V, F32, VEC>(a.logits, row, e0, E, w[i]);
+      load_raw<V, F32, VEC>(add, row, e0, E, d[i]);
     }
-    const double mean = (double)(group_sum<G>((float)sum) / (float)a.experts);
+  };
+  fetch(u0);
+  float A[V], bias[V];
+  double c[V], sum = 0.0;
+  const int sc = gap ? 0 : s;
+  const double per = 1.0 / ((double)a.topk * (double)n), per_token = per * a.topk;
+  const double f = a.dloss != nullptr ? (double)a.dloss[sc] * E * per : 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = e0 + v < a.experts ? (float)((w[v] - mean) / (double)n) : 0.f;
+  for (int v = 0; v < V; ++v) {
+    const int64_t at = (int64_t)sc * E + min(e0 + v, E - 1);
+    bias[v] = a.bias != nullptr ? a.bias[min(e0 + v, E - 1)] : 0.f;
+    c[v] = a.dloss != nullptr ? f * (double)a.counts[at] : 0.0;
+    if (a.dmean_prob != nullptr) c[v] += (double)a.dmean_prob[at];
+    if (e0 + v < E) sum += c[v];
   }
-  // whole passes of N tokens, so that every lane takes part in the reductions
-  for (int64_t u = u0; u < u1; u += N) {
-    const int64_t mine = u + threadIdx.x / G;
-    const bool live = mine < u1;
-    const int64_t uc = live ? mine : u1 - 1;
-    const int64_t t = uc < skip_at ? uc : uc + skip;
-    float z[V], key[V], p[V], base[V];
-    if (!gap) {
-      load_row<V, F32>(a.logits, a.bias, t, a.experts, e0, a.vec, z, key);
-    }
+  const double mean = (double)(group_sum<G>((float)sum) / (float)E);
 #pragma unroll
-    for (int v = 0; v < V; ++v) base[v] = 0.f;
-    if (a.add != nullptr && e0 < a.experts) load_values<V, F32>(a.add, t * a.experts + e0, a.experts - e0, a.vec, base);
-    if (!gap) {
+  for (int v = 0; v < V; ++v) A[v] = e0 + v < E && !gap ? (float)((c[v] - mean) * per_token) : 0.f;
+  for (int64_t u = u0; u < u1; u += U * N) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int64_t uc = u + mine + i * N, t = uc < skip_at ? uc : uc + skip;
+      if (u + i * N >= u1) break;                         // (uniform)
+      float z[V], p[V], out[V];
+      open_logits<V, F32, VEC>(w[i], bias, e0, E, z);
       row_softmax<G, V>(z, p);
       float dot = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) dot += p[v] * A[v];
       dot = group_sum<G>(dot);
 #pragma unroll
-      for (int v = 0; v < V; ++v) base[v] += p[v] * (A[v] - dot);
+      for (int v = 0; v < V; ++v)                         // in a gap A and so the sum is 0, whatever its logits are
+        out[v] = (a.add != nullptr ? value_of<V, F32, VEC>(d[i], v) : 0.f) + (gap ? 0.f : p[v] * (A[v] - dot));
+      if (uc < u1 && e0 < E) store_values<V, F32>(a.dlogits, t * E + e0, E - e0, VEC, out);
     }
-    if (live && e0 < a.experts) store_values<V, F32>(a.dlogits, t * a.experts + e0, a.experts - e0, a.vec, base);
+    if (u + U * N < u1) fetch(u + U * N);
   }
 }
 
@@ -471,6 +547,12 @@ void by_shape(int32_t experts, const Go& go) {
     go(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
   else
     go(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
+}
+
+template <typename Go>
+void by_type(int32_t f32, bool vec, const Go& go) {
+  if (f32) vec ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  else vec ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 }  // namespace
@@ -519,10 +601,11 @@ hipError_t launch_balance(const BalanceArgs& args, hipStream_t stream) {
   by_shape(a.experts, [&](auto g_, auto v_) {
     constexpr int G = decltype(g_)::value, V = decltype(v_)::value;
     const dim3 grid((unsigned)a.parts, (unsigned)a.sequences);
-    if (a.f32)
-      hipLaunchKernelGGL((balance_kernel<G, V, true>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((balance_kernel<G, V, false>), grid, dim3(256), 0, stream, a);
+    const auto go = [&](auto f32_, auto vec_) {
+      constexpr bool F32 = decltype(f32_)::value, VEC = decltype(vec_)::value;
+      hipLaunchKernelGGL((balance_kernel<G, V, F32, VEC>), grid, dim3(256), 0, stream, a);
+    };
+    by_type(a.f32, V == 4 && a.vec, go);
   });
   if (a.parts > 1)
     hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)a.sequences), dim3(1024), 0, stream, a);
@@ -536,12 +619,13 @@ hipError_t launch_balance_bwd(const BalanceBwdArgs& args, hipStream_t stream) {
   const int rows = a.sequences + (a.segments != nullptr ? 1 : 0);
   by_shape(a.experts, [&](auto g_, auto v_) {
     constexpr int G = decltype(g_)::value, V = decltype(v_)::value, per = 256 / G;
-    const int64_t parts = std::max<int64_t>(1, std::min((a.tokens + per - 1) / per, (int64_t)((2048 + rows - 1) / rows)));
+    const int64_t parts = std::max<int64_t>(1, std::min((a.tokens + per - 1) / per, (int64_t)((1024 + rows - 1) / rows)));
     const dim3 grid((unsigned)parts, (unsigned)rows);
-    if (a.f32)
-      hipLaunchKernelGGL((balance_bwd_kernel<G, V, true>), grid, dim3(256), 0, stream, a);
-    else
-      hipLaunchKernelGGL((balance_bwd_kernel<G, V, false>), grid, dim3(256), 0, stream, a);
+    const auto go = [&](auto f32_, auto vec_) {
+      constexpr bool F32 = decltype(f32_)::value, VEC = decltype(vec_)::value;
+      hipLaunchKernelGGL((balance_bwd_kernel<G, V, F32, VEC>), grid, dim3(256), 0, stream, a);
+    };
+    by_type(a.f32, V == 4 && a.vec, go);
   });
   return hipGetLastError();
 }

@@ -135,6 +135,30 @@ def test_autograd(gpu_lib):
     assert not gpu_lib.MoEBalance.apply(z, idx)[0].requires_grad
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_far_logits(gpu_lib, dtype):
+    """Masks of the type's lowest value are open experts of probability 0; rows of
+    nothing but them are even; logits far apart."""
+    z = torch.randn((40, 20), device="cuda").to(dtype)
+    z[3, 5:] = torch.finfo(dtype).min
+    z[4] = torch.finfo(dtype).min
+    z[5, ::2], z[5, 1::2] = torch.finfo(dtype).min, torch.finfo(dtype).max
+    z[6] = (torch.arange(20, device="cuda") * -9.7).to(dtype)
+    z[7] = z[6] + 1e4
+    idx = gpu_lib.mx_moe_route(z, 3)[0]
+    loss, counts, mean = gpu_lib.mx_moe_balance(z, idx)
+    zn = f64(z)
+    rl, rc, rm, bl, bm = ref.balance(zn, None, idx.cpu().numpy(), None, 20)
+    assert np.array_equal(counts.cpu().numpy(), rc)
+    assert np.all(np.abs(f64(mean) - rm) <= bm) and np.all(np.abs(f64(loss) - rl) <= bl)
+    w = torch.randn((1, 20), device="cuda")
+    dz = gpu_lib.mx_moe_balance_bwd(z, counts, 3, dloss=torch.ones(1, device="cuda"), dmean_prob=w)
+    want, bound = ref.balance_bwd(zn, None, rc, 3, np.ones(1), f64(w), None, None)
+    if dtype == torch.bfloat16:
+        bound = bound + decode_ref.BF16_HALF * (np.abs(want) + bound)
+    assert np.all(np.abs(f64(dz) - want) <= bound + 1e-37)
+
+
 def test_choices_outside_and_repeated(gpu_lib):
     z = torch.randn((70, 12), device="cuda")
     idx = torch.randint(0, 12, (70, 4), device="cuda", dtype=torch.int32)
