@@ -2226,7 +2226,7 @@ mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_rows, int6
   g_err[0] = 0;
   const char* who = "mx_quantize_int8";
   if (x_dtype != MX_BF16 && x_dtype != MX_F32) return fail(MX_EINVAL, "%s: bad dtype %d", who, (int)x_dtype);
-  if (x_rows < 0 || rows < 0 || (!row_index && rows != x_rows) || cols <= 0 || cols % 16)
+  if (x_rows < 0 || rows < 0 || (!row_index && rows != x_rows && rows > 0) || cols <= 0 || cols % 16)
     return fail(MX_ESHAPE, "%s: need rows >= 0 (those of x without an index) and cols a positive multiple of 16", who);
   const int64_t per = x_dtype == MX_F32 ? 4 : 8;             // values of 16 bytes
   if (ldx % per || (x_rows > 1 && ldx < cols))

@@ -884,12 +884,13 @@ hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream) {
 // 67; 512 x 28672 x 4096 256 x 256 69, 128 x 128 83; 2048 x 4096 x 4096 128 x 128,
 // two a compute unit, 40, 256 x 256 56. It goes by sizes alone, not by how the rows
 // fall to the groups, so that a call's workspace does not depend on it.
-Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
-  const bool pair = result == kInt8ToSwiglu;
+struct Int8Choice {
+  int32_t form, parts;
+};
+void choose_int8(bool pair, const Int8GemmArgs& a, Int8Choice* chosen) {
   const int64_t groups = std::min(a.groups, a.M), per = ((int64_t)a.M + groups - 1) / groups;
   const int steps = (a.K + kBK - 1) / kBK;
   const double weights = (double)groups * a.N * a.K * 1e-6;
-  Int8Plan best;
   double best_us = 1e30;
   for (int form = 0; form < kForms; ++form) {
     by_form(form, [&](auto f) {
@@ -916,12 +917,38 @@ Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
         if (parts > 1) us += 3.0 + (double)parts * a.M * a.N * 8 / 4.5e6;  // the planes, written and read
         if (us < best_us) {
           best_us = us;
-          best.form = form;
-          best.parts = parts;
+          chosen->form = form;
+          chosen->parts = parts;
         }
       }
     });
   }
+}
+
+// Weighing the forms takes about a microsecond, a third of a small call's time on
+// the host: the last choices of a thread are kept by their sizes.
+Int8Choice choice_int8(bool pair, const Int8GemmArgs& a) {
+  struct Entry {
+    int32_t M = -1, N, K, groups, pair;
+    Int8Choice choice;
+  };
+  static thread_local Entry kept[64];
+  Entry& e = kept[((uint32_t)a.M * 2654435761u ^ (uint32_t)a.N * 40503u ^ (uint32_t)a.K * 97u ^ (uint32_t)a.groups * 7u ^ pair) >> 3 & 63];
+  if (e.M != a.M || e.N != a.N || e.K != a.K || e.groups != a.groups || e.pair != pair) {
+    choose_int8(pair, a, &e.choice);
+    e.M = a.M; e.N = a.N; e.K = a.K; e.groups = a.groups; e.pair = pair;
+  }
+  return e.choice;
+}
+
+Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
+  const bool pair = result == kInt8ToSwiglu;
+  const int64_t groups = std::min(a.groups, a.M);
+  const int steps = (a.K + kBK - 1) / kBK;
+  const Int8Choice choice = choice_int8(pair, a);
+  Int8Plan best;
+  best.form = choice.form;
+  best.parts = choice.parts;
   by_form(best.form, [&](auto f) {
     constexpr int BM = decltype(f)::kBM, BN = decltype(f)::kBN;
     const bool half = pair && best.parts == 1;

@@ -100,6 +100,7 @@ def test_cast_of_non_finite_rows_indices_outside_and_3d(gpu_lib):
     assert q.shape == (3, 5, 32) and s.shape == (3, 5)
     _check_cast(q.view(15, 32), s.view(15), w.view(15, 32))
     assert gpu_lib.mx_quantize_int8(x[:0])[0].shape == (0, 64)
+    assert gpu_lib.mx_quantize_int8(x, row_index=idx[:0], row_weight=x[:0, 0].contiguous())[1].shape == (0,)
 
 
 def _codes(gen, *shape):
