@@ -272,7 +272,7 @@ __device__ __forceinline__ void bare_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// A tile of 64 MI rows of A by 64 NI rows of B on four waves, 2 x 2. Both operands
+// A tile of 64 TI rows of A by 64 NI rows of B on four waves, 2 x 2. Both operands
 // go straight to LDS (buffer loads with LDS as their target), in S stages of 128 k
 // that are separate objects, so that the compiler sees that a load into one never
 // meets a read of another. Chunk c (16 bytes) of row r lies at c ^ ((r >> 1) & 7),
@@ -294,15 +294,14 @@ __device__ __forceinline__ void bare_barrier() {
 // With the SwiGLU, 32-row blocks of the B tile alternate between gate and up rows.
 // With parts > 1 each tile is several workgroups, each with its share of the
 // steps, that leave the sums themselves, in 32 bits, to planes of their own.
-template <int MI, int NI, int S, int EPI, bool TAIL>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(64 * (MI + NI) * kBK * S <= 81920 ? 2 : 1)))
+template <int TI, int NI, int S, int EPI, bool TAIL>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(64 * (TI + NI) * kBK * S <= 81920 ? 2 : 1)))
 void gemm_int8_kernel(Int8GemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPair = EPI == kInt8ToSwiglu;
   static_assert(!kPair || NI % 2 == 0, "gate and up blocks come in pairs");
   static_assert(S == 2 || S == 4, "stages");
-  constexpr int BM = 64 * MI, BN = 64 * NI, kLoads = 2 * (MI + NI), kPerStep = (MI + NI) / MI;
-  static_assert(kPerStep * MI == MI + NI, "half of a step's loads in whole numbers per row block");
+  constexpr int BM = 64 * TI, BN = 64 * NI;
   __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sB0[BN * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sA1[BM * kBK];
@@ -324,7 +323,7 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   int part, parts = a.parts, id, unit = -1;
   if (!TAIL || (int)blockIdx.x < whole_ids) {
     if ((int)blockIdx.x >= whole_ids) return;
-    const int place = xcd_ids<MI * NI >= 16 ? 32 : 64>((int)blockIdx.x, whole_ids);
+    const int place = xcd_ids<TI * NI >= 16 ? 32 : 64>((int)blockIdx.x, whole_ids);
     part = place / (TAIL ? whole_ids : tiles);
     id = place - part * tiles;
   } else {
@@ -356,216 +355,230 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   // workgroups that walk along k together would meet there: they begin at other
   // places. Those of an XCD that share rows keep step (for the L2's sake).
   const int rot = __builtin_amdgcn_readfirstlane(nk * (int)(blockIdx.x & 7) / 8);
-  // Load p of this wave's kLoads of step kt (8 rows each: A's, then B's). Steps
-  // past the last are out of bounds for every lane: zeros, and no memory is read.
-  auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
-    const int s = kt + rot < nk ? kt + rot : kt + rot - nk;
-    const int k0 = __builtin_amdgcn_readfirstlane(kt < nk ? (first + s) * kBK : K);
-    if (p < 2 * MI) {
-      const int blk = 4 * p + wave;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, k0 < K ? voff : 0x80000000u,
-                                               (uint32_t)(8 * blk) * K + k0, 0, 0);
-    } else {
-      const int q = p - 2 * MI, blk = 4 * q + wave;
-      const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u;
-      if constexpr (kPair) {
-        const uint32_t so = (uint32_t)((q / 2) * 32 + 8 * wave) * K + k0;  // 32-row block q: gate and up in turn
-        if (q & 1)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
-        else
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
+  auto run = [&](auto mi_) __attribute__((always_inline)) {
+    constexpr int MI = decltype(mi_)::value, kLoads = 2 * (MI + NI), kPerStep = (MI + NI) / MI;
+    static_assert(kPerStep * MI == MI + NI, "half of a step's loads in whole numbers per row block");
+    // Load p of this wave's kLoads of step kt (8 rows each: A's, then B's). Steps
+    // past the last are out of bounds for every lane: zeros, and no memory is read.
+    auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
+      const int s = kt + rot < nk ? kt + rot : kt + rot - nk;
+      const int k0 = __builtin_amdgcn_readfirstlane(kt < nk ? (first + s) * kBK : K);
+      if (p < 2 * MI) {
+        const int blk = 4 * p + wave;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(dA + blk * 1024), 16, k0 < K ? voff : 0x80000000u,
+                                                 (uint32_t)(8 * blk) * K + k0, 0, 0);
       } else {
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, (uint32_t)(8 * blk) * K + k0, 0, 0);
-      }
-    }
-  };
-  v16i acc[MI][NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-  v4i fa[2][MI], fb[2][NI];
-  const int sw = (l32 >> 1) & 7;               // of every row 32 x + l32
-  auto frag = [&](const uint8_t* base, int r32, int ks) __attribute__((always_inline)) -> v4i {
-    return *reinterpret_cast<const v4i*>(base + (r32 * 32 + l32) * kBK + (((2 * ks + h) ^ sw) << 4));
-  };
-  // Step kt from stage (cA, cB); (nA, nB) holds step kt + 1, and the loads of step
-  // kt - 1 + S, half of which are out, go to (pA, pB).
-  auto step = [&](int kt, uint8_t* cA, uint8_t* cB, uint8_t* nA, uint8_t* nB, uint8_t* pA, uint8_t* pB)
-      __attribute__((always_inline)) {
-    static_for<0, 4>([&](auto ks_) __attribute__((always_inline)) {
-      constexpr int ks = decltype(ks_)::value, cur = ks & 1, nxt = cur ^ 1, ns = (ks + 1) & 3;
-      if constexpr (ks == 3) {
-        __builtin_amdgcn_s_waitcnt(wait_vmcnt_lds((S - 2) * kLoads));
-        bare_barrier();
-      }
-      const uint8_t* const rA = ks == 3 ? nA : cA;
-      const uint8_t* const rB = ks == 3 ? nB : cB;
-      static_for<0, MI>([&](auto i_) __attribute__((always_inline)) {
-        constexpr int i = decltype(i_)::value;
-        // B's fragments in the first row blocks, A's in the last
-        static_for<0, MI + NI>([&](auto f_) __attribute__((always_inline)) {
-          constexpr int f = decltype(f_)::value;
-          if constexpr (f / kPerStep == i) {
-            if constexpr (f < NI) fb[nxt][f] = frag(rB, wn * NI + f, ns);
-            else fa[nxt][f - NI] = frag(rA, wm * MI + f - NI, ns);
-          }
-        });
-#pragma unroll
-        for (int q = 0; q < kPerStep; ++q) {
-          if constexpr (ks == 3) load(kt + S, cA, cB, kPerStep * i + q);
-          if constexpr (ks == 0) load(kt - 1 + S, pA, pB, MI + NI + kPerStep * i + q);
+        const int q = p - 2 * MI, blk = 4 * q + wave;
+        const uint32_t vb = k0 + lch * 16 < K ? voff : 0x80000000u;
+        if constexpr (kPair) {
+          const uint32_t so = (uint32_t)((q / 2) * 32 + 8 * wave) * K + k0;  // 32-row block q: gate and up in turn
+          if (q & 1)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ru, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
+          else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, so, 0, 0);
+        } else {
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(dB + blk * 1024), 16, vb, (uint32_t)(8 * blk) * K + k0, 0, 0);
         }
-        static_for<0, NI>([&](auto j_) __attribute__((always_inline)) {
-          constexpr int j = decltype(j_)::value;
-          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-    });
-  };
-  auto fill = [&](int kt, uint8_t* dA, uint8_t* dB, int n) __attribute__((always_inline)) {
-#pragma unroll
-    for (int p = 0; p < n; ++p) load(kt, dA, dB, p);
-  };
-  fill(0, sA0, sB0, kLoads);
-  if constexpr (S == 4) {
-    fill(1, sA1, sB1, kLoads);
-    fill(2, sA2, sB2, kLoads);
-    fill(3, sA3, sB3, MI + NI);
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads + MI + NI));          // step 0 has landed
-  } else {
-    fill(1, sA1, sB1, MI + NI);
-    __builtin_amdgcn_s_waitcnt(wait_vmcnt(MI + NI));
-  }
-  bare_barrier();
-#pragma unroll
-  for (int x = 0; x < NI; ++x) fb[0][x] = frag(sB0, wn * NI + x, 0);
-#pragma unroll
-  for (int x = 0; x < MI; ++x) fa[0][x] = frag(sA0, wm * MI + x, 0);
-  int kt = 0;
-  if constexpr (S == 4) {
-    for (; kt + 3 < nk; kt += 4) {
-      step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
-      step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
-      step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
-      step(kt + 3, sA3, sB3, sA0, sB0, sA2, sB2);
-    }
-    if (kt < nk) {
-      step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
-      if (kt + 1 < nk) {
-        step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
-        if (kt + 2 < nk) step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
       }
-    }
-  } else {
-    for (; kt + 1 < nk; kt += 2) {
-      step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
-      step(kt + 1, sA1, sB1, sA0, sB0, sA0, sB0);
-    }
-    if (kt < nk) step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
-  }
-  // Sums to results. Lane: row 32 i + l32 of the wave's rows, columns 32 j + 8 q +
-  // 4 h + 0 .. 3 of its columns; by 32 rows through LDS of the wave's own.
-  __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
-  __syncthreads();
-  uint8_t* const stage = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
-  auto finish = [&](auto epi_, uint8_t* c, int64_t ldc, int64_t crow0, int cn0, int crows, int ccols)
-      __attribute__((always_inline)) {
-    constexpr int E = decltype(epi_)::value;
-    constexpr bool kTwo = E == kInt8ToSwiglu;
-    constexpr int kBytes = E == kInt8ToBf16 ? 2 : 4, kCols = (kTwo ? 16 : 32) * NI, kRowBytes = kCols * kBytes;
-    constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes, kMask = kChunks < 16 ? kChunks - 1 : 15;
-    static_assert(32 * kRowBytes <= BM * kBK && 32 * kRowBytes <= BN * kBK, "32 rows of results fit one stage of one operand");
-    cn0 += wn * kCols;                         // the wave's first column
-    const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
-    // the lane's column scales, 4 at a time (0 past the last), and its rows'
-    v4f sb[NI][4];
-    float sa[MI];
-    if constexpr (E != kInt8ToSums) {
-      const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_s + (int64_t)g.group * a.N + cn0, (int64_t)(nrows - cn0) * 4);
-      const __amdgpu_buffer_rsrc_t rus =
-          make_rsrc(a.b_s + (int64_t)g.group * a.N + nrows + cn0, kTwo ? (int64_t)(nrows - cn0) * 4 : 0);
-      const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_s + row0, (int64_t)rows * 4);
-#pragma unroll
+    };
+    v16i acc[MI][NI];
+  #pragma unroll
+    for (int i = 0; i < MI; ++i)
+  #pragma unroll
       for (int j = 0; j < NI; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t at = (32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h) * 4;
-          const u32x4 w = kTwo && (j & 1) ? __builtin_amdgcn_raw_buffer_load_b128(rus, at, 0, 0)
-                                          : __builtin_amdgcn_raw_buffer_load_b128(rbs, at, 0, 0);
-#pragma unroll
-          for (int v = 0; v < 4; ++v) sb[j][q][v] = __uint_as_float(w[v]);
+  #pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+    v4i fa[2][MI], fb[2][NI];
+    const int sw = (l32 >> 1) & 7;               // of every row 32 x + l32
+    auto frag = [&](const uint8_t* base, int r32, int ks) __attribute__((always_inline)) -> v4i {
+      return *reinterpret_cast<const v4i*>(base + (r32 * 32 + l32) * kBK + (((2 * ks + h) ^ sw) << 4));
+    };
+    // Step kt from stage (cA, cB); (nA, nB) holds step kt + 1, and the loads of step
+    // kt - 1 + S, half of which are out, go to (pA, pB).
+    auto step = [&](int kt, uint8_t* cA, uint8_t* cB, uint8_t* nA, uint8_t* nB, uint8_t* pA, uint8_t* pB)
+        __attribute__((always_inline)) {
+      static_for<0, 4>([&](auto ks_) __attribute__((always_inline)) {
+        constexpr int ks = decltype(ks_)::value, cur = ks & 1, nxt = cur ^ 1, ns = (ks + 1) & 3;
+        if constexpr (ks == 3) {
+          __builtin_amdgcn_s_waitcnt(wait_vmcnt_lds((S - 2) * kLoads));
+          bare_barrier();
         }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-        sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (32 * (wm * MI + i) + l32) * 4, 0, 0));
-    }
-#pragma unroll
-    for (int i = 0; i < MI; ++i) {
-      const int m0 = 32 * (wm * MI + i);
-      if (m0 >= crows) break;
-#pragma unroll
-      for (int j = 0; j < NI; j += kTwo ? 2 : 1) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = 32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h;
-          uint8_t* const at = stage + l32 * kRowBytes + (((col / kPer) ^ (l32 & kMask)) << 4);
-          if constexpr (E == kInt8ToSums) {
-            *reinterpret_cast<v4i*>(at) = v4i{hop(acc[i][j][4 * q]), hop(acc[i][j][4 * q + 1]), hop(acc[i][j][4 * q + 2]),
-                                              hop(acc[i][j][4 * q + 3])};
-          } else {
-            float y[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              y[v] = (float)hop(acc[i][j][4 * q + v]) * sa[i] * sb[j][q][v];
-              if constexpr (kTwo) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa[i] * sb[j + 1][q][v]);
+        const uint8_t* const rA = ks == 3 ? nA : cA;
+        const uint8_t* const rB = ks == 3 ? nB : cB;
+        static_for<0, MI>([&](auto i_) __attribute__((always_inline)) {
+          constexpr int i = decltype(i_)::value;
+          // B's fragments in the first row blocks, A's in the last
+          static_for<0, MI + NI>([&](auto f_) __attribute__((always_inline)) {
+            constexpr int f = decltype(f_)::value;
+            if constexpr (f / kPerStep == i) {
+              if constexpr (f < NI) fb[nxt][f] = frag(rB, wn * NI + f, ns);
+              else fa[nxt][f - NI] = frag(rA, wm * MI + f - NI, ns);
             }
-            if constexpr (kBytes == 4) {
-              *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+          });
+  #pragma unroll
+          for (int q = 0; q < kPerStep; ++q) {
+            if constexpr (ks == 3) load(kt + S, cA, cB, kPerStep * i + q);
+            if constexpr (ks == 0) load(kt - 1 + S, pA, pB, MI + NI + kPerStep * i + q);
+          }
+          static_for<0, NI>([&](auto j_) __attribute__((always_inline)) {
+            constexpr int j = decltype(j_)::value;
+            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
+          });
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    };
+    auto fill = [&](int kt, uint8_t* dA, uint8_t* dB, int n) __attribute__((always_inline)) {
+  #pragma unroll
+      for (int p = 0; p < n; ++p) load(kt, dA, dB, p);
+    };
+    fill(0, sA0, sB0, kLoads);
+    if constexpr (S == 4) {
+      fill(1, sA1, sB1, kLoads);
+      fill(2, sA2, sB2, kLoads);
+      fill(3, sA3, sB3, MI + NI);
+      __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads + MI + NI));          // step 0 has landed
+    } else {
+      fill(1, sA1, sB1, MI + NI);
+      __builtin_amdgcn_s_waitcnt(wait_vmcnt(MI + NI));
+    }
+    bare_barrier();
+  #pragma unroll
+    for (int x = 0; x < NI; ++x) fb[0][x] = frag(sB0, wn * NI + x, 0);
+  #pragma unroll
+    for (int x = 0; x < MI; ++x) fa[0][x] = frag(sA0, wm * MI + x, 0);
+    int kt = 0;
+    if constexpr (S == 4) {
+      for (; kt + 3 < nk; kt += 4) {
+        step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
+        step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+        step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
+        step(kt + 3, sA3, sB3, sA0, sB0, sA2, sB2);
+      }
+      if (kt < nk) {
+        step(kt, sA0, sB0, sA1, sB1, sA3, sB3);
+        if (kt + 1 < nk) {
+          step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+          if (kt + 2 < nk) step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
+        }
+      }
+    } else {
+      for (; kt + 1 < nk; kt += 2) {
+        step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
+        step(kt + 1, sA1, sB1, sA0, sB0, sA0, sB0);
+      }
+      if (kt < nk) step(kt, sA0, sB0, sA1, sB1, sA1, sB1);
+    }
+    // Sums to results. Lane: row 32 i + l32 of the wave's rows, columns 32 j + 8 q +
+    // 4 h + 0 .. 3 of its columns; by 32 rows through LDS of the wave's own.
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    uint8_t* const stage = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
+    auto finish = [&](auto epi_, uint8_t* c, int64_t ldc, int64_t crow0, int cn0, int crows, int ccols)
+        __attribute__((always_inline)) {
+      constexpr int E = decltype(epi_)::value;
+      constexpr bool kTwo = E == kInt8ToSwiglu;
+      constexpr int kBytes = E == kInt8ToBf16 ? 2 : 4, kCols = (kTwo ? 16 : 32) * NI, kRowBytes = kCols * kBytes;
+      constexpr int kChunks = kRowBytes / 16, kPer = 16 / kBytes, kMask = kChunks < 16 ? kChunks - 1 : 15;
+      static_assert(32 * kRowBytes <= BM * kBK && 32 * kRowBytes <= BN * kBK, "32 rows of results fit one stage of one operand");
+      cn0 += wn * kCols;                         // the wave's first column
+      const bool whole = ldc % kPer == 0 && (reinterpret_cast<uintptr_t>(c) & 15) == 0;
+      // the lane's column scales, 4 at a time (0 past the last), and its rows'
+      v4f sb[NI][4];
+      float sa[MI];
+      if constexpr (E != kInt8ToSums) {
+        const __amdgpu_buffer_rsrc_t rbs = make_rsrc(a.b_s + (int64_t)g.group * a.N + cn0, (int64_t)(nrows - cn0) * 4);
+        const __amdgpu_buffer_rsrc_t rus =
+            make_rsrc(a.b_s + (int64_t)g.group * a.N + nrows + cn0, kTwo ? (int64_t)(nrows - cn0) * 4 : 0);
+        const __amdgpu_buffer_rsrc_t ras = make_rsrc(a.a_s + row0, (int64_t)rows * 4);
+  #pragma unroll
+        for (int j = 0; j < NI; ++j)
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t at = (32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h) * 4;
+            const u32x4 w = kTwo && (j & 1) ? __builtin_amdgcn_raw_buffer_load_b128(rus, at, 0, 0)
+                                            : __builtin_amdgcn_raw_buffer_load_b128(rbs, at, 0, 0);
+  #pragma unroll
+            for (int v = 0; v < 4; ++v) sb[j][q][v] = __uint_as_float(w[v]);
+          }
+  #pragma unroll
+        for (int i = 0; i < MI; ++i)
+          sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (32 * (wm * MI + i) + l32) * 4, 0, 0));
+      }
+  #pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int m0 = 32 * (wm * MI + i);
+        if (m0 >= crows) break;
+  #pragma unroll
+        for (int j = 0; j < NI; j += kTwo ? 2 : 1) {
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int col = 32 * (kTwo ? j / 2 : j) + 8 * q + 4 * h;
+            uint8_t* const at = stage + l32 * kRowBytes + (((col / kPer) ^ (l32 & kMask)) << 4);
+            if constexpr (E == kInt8ToSums) {
+              *reinterpret_cast<v4i*>(at) = v4i{hop(acc[i][j][4 * q]), hop(acc[i][j][4 * q + 1]), hop(acc[i][j][4 * q + 2]),
+                                                hop(acc[i][j][4 * q + 3])};
             } else {
-              typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-              *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+              float y[4];
+  #pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                y[v] = (float)hop(acc[i][j][4 * q + v]) * sa[i] * sb[j][q][v];
+                if constexpr (kTwo) y[v] = swiglu(y[v], (float)hop(acc[i][j + 1][4 * q + v]) * sa[i] * sb[j + 1][q][v]);
+              }
+              if constexpr (kBytes == 4) {
+                *reinterpret_cast<v4f*>(at) = v4f{y[0], y[1], y[2], y[3]};
+              } else {
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                *reinterpret_cast<bf16x4*>(at + 8 * h) = bf16x4{(__bf16)y[0], (__bf16)y[1], (__bf16)y[2], (__bf16)y[3]};
+              }
             }
           }
         }
-      }
-      // the wave's own LDS: its writes are done before its reads (no barrier)
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (whole) {
-#pragma unroll
-        for (int u = 0; u < 32 * kChunks / 64; ++u) {
-          const int r = (u * 64 + lane) / kChunks, ch = (u * 64 + lane) % kChunks, n = cn0 + ch * kPer;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
-          if (m0 + r < crows && n < ccols) *reinterpret_cast<uint4*>(c + ((crow0 + m0 + r) * ldc + n) * kBytes) = w;
-        }
-      } else {
-        for (int u = lane; u < 32 * kCols; u += 64) {
-          const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
-          const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
-          if (m0 + r < crows && n < ccols) {
-            const int64_t at = (crow0 + m0 + r) * ldc + n;
-            if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
-            else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
+        // the wave's own LDS: its writes are done before its reads (no barrier)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        if (whole) {
+  #pragma unroll
+          for (int u = 0; u < 32 * kChunks / 64; ++u) {
+            const int r = (u * 64 + lane) / kChunks, ch = (u * 64 + lane) % kChunks, n = cn0 + ch * kPer;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * kRowBytes + ((ch ^ (r & kMask)) << 4));
+            if (m0 + r < crows && n < ccols) *reinterpret_cast<uint4*>(c + ((crow0 + m0 + r) * ldc + n) * kBytes) = w;
+          }
+        } else {
+          for (int u = lane; u < 32 * kCols; u += 64) {
+            const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
+            const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
+            if (m0 + r < crows && n < ccols) {
+              const int64_t at = (crow0 + m0 + r) * ldc + n;
+              if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
+              else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
+            }
           }
         }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
       }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
+    };
+    if (TAIL && unit >= 0)                       // a tile of sums, rows past the valid ones left out
+      finish(std::integral_constant<int, kInt8ToSums>{}, reinterpret_cast<uint8_t*>(a.planes + (int64_t)unit * BM * BN), BN, 0,
+             0, rows, BN);
+    else
+      finish(std::integral_constant<int, EPI>{},
+             reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * nrows * 4 : 0), nrows, row0, n0,
+             rows, nrows);
   };
-  if (TAIL && unit >= 0)                       // a tile of sums, rows past the valid ones left out
-    finish(std::integral_constant<int, kInt8ToSums>{}, reinterpret_cast<uint8_t*>(a.planes + (int64_t)unit * BM * BN), BN, 0,
-           0, rows, BN);
-  else
-    finish(std::integral_constant<int, EPI>{},
-           reinterpret_cast<uint8_t*>(a.c) + (EPI == kInt8ToSums ? (int64_t)part * a.M * nrows * 4 : 0), nrows, row0, n0,
-           rows, nrows);
+  if constexpr (TI == 4) {
+    // The last tile of a group that needs at most half its rows has half the work
+    // (8192 rows of 8 groups by 28672 x 4096: 991 -> 974 us; MLP of 4096 tokens, two
+    // choices of 8 experts of 4096 x 14336: 1558 -> 1528 us).
+    if (rows <= BM / 2) {
+      run(std::integral_constant<int, 2>{});
+      return;
+    }
+  }
+  run(std::integral_constant<int, TI>{});
 #endif
 }
 

@@ -135,11 +135,11 @@ def test_product(gpu_lib, m, n, k):
 # each kernel form once more at a size that takes it, whole and with k shared out
 # over workgroups (those need a workspace): rows per group, n, k
 FORMS = [([130], 6000, 64), ([67, 0, 133], 6000, 64), ([200], 6000, 272), ([100, 40, 60], 6000, 272), ([400], 12000, 144),
-         ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144)]
+         ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144), ([896, 1409], 16000, 512)]
 SHARED = [([130], 100, 8192), ([130], 101, 8192), ([60, 0, 140], 1030, 4112), ([200], 2050, 4112), ([200], 2051, 4112),
           ([130, 170, 100], 6000, 4112), ([3, 0, 0, 5], 48, 16384)]
 # ... and for the tiles of the last round alone
-TAILS = [([4000], 4300, 4096), ([1000, 0, 3100], 4301, 2064), ([4100], 4096, 4096)]
+TAILS = [([4000], 4300, 4096), ([1000, 0, 3100], 4301, 2064), ([4100], 4096, 4096), ([1920, 2177], 6000, 4096)]
 
 
 @pytest.mark.parametrize("sizes,n,k", FORMS + SHARED + TAILS)
