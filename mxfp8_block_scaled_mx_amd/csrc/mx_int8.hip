@@ -305,9 +305,9 @@ __device__ __forceinline__ void bare_barrier() {
 // library product of the same format reaches 2.4. The matrix cores are busy 73% of
 // the cycles, no read of LDS meets a bank conflict, and the clock falls to 1.66 GHz
 // under this load (all zeros, which draw less power, take 281 us): power bounds it.
-// 8192 rows of 8 unlike groups by 28672 x 4096: 950 us, 2.0 POP/s, 8% of it rows that
-// tiles have too many and the rest a tile's start and end, 16 us of 60. With a second
-// barrier a step, or a fragment's wait behind the barrier, 20 to 40 us more.
+// 8192 rows of 8 unlike groups by 28672 x 4096: 950 us, 2.0 POP/s (the library on one
+// group: 2.1). Some 6% of it are rows that tiles have too many; k is shorter, so each
+// tile's first loads and its results, which nothing hides, weigh more.
 template <int TI, int NI, int S, int EPI, bool TAIL>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(64 * (TI + NI) * kBK * S <= 81920 ? 2 : 1)))
 void gemm_int8_kernel(Int8GemmArgs a) {
