@@ -302,8 +302,8 @@ __device__ __forceinline__ void bare_barrier() {
 // steps, that leave the sums themselves, in 32 bits, to planes of their own.
 //
 // 256 x 256 tiles, 8191 x 4096 x 14336: 375 to 385 us, 2.5 to 2.6 POP/s, where a large
-// library product of the same format reaches 2.4. The matrix cores are busy 73% of
-// the cycles, no read of LDS meets a bank conflict, and the clock falls to 1.66 GHz
+// library product of the same format reaches 2.4. The matrix cores are busy 69 to 73%
+// of the cycles, no read of LDS meets a bank conflict, and the clock falls to 1.7 GHz
 // under this load (all zeros, which draw less power, take 281 us): power bounds it.
 // 8192 rows of 8 unlike groups by 28672 x 4096: 950 us, 2.0 POP/s (the library on one
 // group: 2.1). Some 6% of it are rows that tiles have too many; k is shorter, so each
