@@ -314,7 +314,7 @@ void gemm_int8_kernel(Int8GemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPair = EPI == kInt8ToSwiglu;
   static_assert(!kPair || NI % 2 == 0, "gate and up blocks come in pairs");
-  static_assert(S == 2 || S == 4, "stages");
+  static_assert(S >= 2 && S <= 4, "stages");
   constexpr int BM = 64 * TI, BN = 64 * NI;
   __shared__ __attribute__((aligned(16))) uint8_t sA0[BM * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sB0[BN * kBK];
@@ -322,8 +322,8 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t sB1[BN * kBK];
   __shared__ __attribute__((aligned(16))) uint8_t sA2[S > 2 ? BM * kBK : 16];
   __shared__ __attribute__((aligned(16))) uint8_t sB2[S > 2 ? BN * kBK : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t sA3[S > 2 ? BM * kBK : 16];
-  __shared__ __attribute__((aligned(16))) uint8_t sB3[S > 2 ? BN * kBK : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sA3[S > 3 ? BM * kBK : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t sB3[S > 3 ? BN * kBK : 16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1, h = lane >> 5, l32 = lane & 31;
   const int ntn = a.n_tiles;
@@ -370,8 +370,7 @@ void gemm_int8_kernel(Int8GemmArgs a) {
   // places. Those of an XCD that share rows keep step (for the L2's sake).
   const int rot = __builtin_amdgcn_readfirstlane(nk * (int)(blockIdx.x & 7) / 8);
   auto run = [&](auto mi_) __attribute__((always_inline)) {
-    constexpr int MI = decltype(mi_)::value, kLoads = 2 * (MI + NI), kPerStep = (MI + NI) / MI;
-    static_assert(kPerStep * MI == MI + NI, "half of a step's loads in whole numbers per row block");
+    constexpr int MI = decltype(mi_)::value, kLoads = 2 * (MI + NI);
     // Load p of this wave's kLoads of step kt (8 rows each: A's, then B's). Steps
     // past the last are out of bounds for every lane: zeros, and no memory is read.
     auto load = [&](int kt, uint8_t* dA, uint8_t* dB, int p) __attribute__((always_inline)) {
@@ -421,19 +420,21 @@ void gemm_int8_kernel(Int8GemmArgs a) {
         const uint8_t* const rB = ks == 3 ? nB : cB;
         static_for<0, MI>([&](auto i_) __attribute__((always_inline)) {
           constexpr int i = decltype(i_)::value;
-          // B's fragments in the first row blocks, A's in the last
+          // half a step's loads, and fragments of which B's come first, dealt out to the row blocks
           static_for<0, MI + NI>([&](auto f_) __attribute__((always_inline)) {
             constexpr int f = decltype(f_)::value;
-            if constexpr (f / kPerStep == i) {
+            if constexpr (f * MI / (MI + NI) == i) {
               if constexpr (f < NI) fb[nxt][f] = frag(rB, wn * NI + f, ns);
               else fa[nxt][f - NI] = frag(rA, wm * MI + f - NI, ns);
             }
           });
-  #pragma unroll
-          for (int q = 0; q < kPerStep; ++q) {
-            if constexpr (ks == 3) load(kt + S, cA, cB, kPerStep * i + q);
-            if constexpr (ks == 0) load(kt - 1 + S, pA, pB, MI + NI + kPerStep * i + q);
-          }
+          static_for<0, MI + NI>([&](auto f_) __attribute__((always_inline)) {
+            constexpr int f = decltype(f_)::value;
+            if constexpr (f * MI / (MI + NI) == i) {
+              if constexpr (ks == 3) load(kt + S, cA, cB, f);
+              if constexpr (ks == 0) load(kt - 1 + S, pA, pB, MI + NI + f);
+            }
+          });
           static_for<0, NI>([&](auto j_) __attribute__((always_inline)) {
             constexpr int j = decltype(j_)::value;
             acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[cur][j], fa[cur][i], acc[i][j], 0, 0, 0);
@@ -447,15 +448,10 @@ void gemm_int8_kernel(Int8GemmArgs a) {
       for (int p = 0; p < n; ++p) load(kt, dA, dB, p);
     };
     fill(0, sA0, sB0, kLoads);
-    if constexpr (S == 4) {
-      fill(1, sA1, sB1, kLoads);
-      fill(2, sA2, sB2, kLoads);
-      fill(3, sA3, sB3, MI + NI);
-      __builtin_amdgcn_s_waitcnt(wait_vmcnt(2 * kLoads + MI + NI));          // step 0 has landed
-    } else {
-      fill(1, sA1, sB1, MI + NI);
-      __builtin_amdgcn_s_waitcnt(wait_vmcnt(MI + NI));
-    }
+    if constexpr (S > 2) fill(1, sA1, sB1, kLoads);
+    if constexpr (S > 3) fill(2, sA2, sB2, kLoads);
+    fill(S - 1, S == 2 ? sA1 : S == 3 ? sA2 : sA3, S == 2 ? sB1 : S == 3 ? sB2 : sB3, MI + NI);
+    __builtin_amdgcn_s_waitcnt(wait_vmcnt((S - 2) * kLoads + MI + NI));      // step 0 has landed
     bare_barrier();
   #pragma unroll
     for (int x = 0; x < NI; ++x) fb[0][x] = frag(sB0, wn * NI + x, 0);
@@ -475,6 +471,16 @@ void gemm_int8_kernel(Int8GemmArgs a) {
           step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
           if (kt + 2 < nk) step(kt + 2, sA2, sB2, sA3, sB3, sA1, sB1);
         }
+      }
+    } else if constexpr (S == 3) {
+      for (; kt + 2 < nk; kt += 3) {
+        step(kt, sA0, sB0, sA1, sB1, sA2, sB2);
+        step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
+        step(kt + 2, sA2, sB2, sA0, sB0, sA1, sB1);
+      }
+      if (kt < nk) {
+        step(kt, sA0, sB0, sA1, sB1, sA2, sB2);
+        if (kt + 1 < nk) step(kt + 1, sA1, sB1, sA2, sB2, sA0, sB0);
       }
     } else {
       for (; kt + 1 < nk; kt += 2) {
@@ -560,15 +566,22 @@ void gemm_int8_kernel(Int8GemmArgs a) {
             if (m0 + r < crows && n < ccols) *reinterpret_cast<uint4*>(c + ((crow0 + m0 + r) * ldc + n) * kBytes) = w;
           }
         } else {
-          for (int u = lane; u < 32 * kCols; u += 64) {
-            const int r = u / kCols, cc = u % kCols, n = cn0 + cc;
-            const uint8_t* const from = stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) + cc % kPer * kBytes;
-            if (m0 + r < crows && n < ccols) {
-              const int64_t at = (crow0 + m0 + r) * ldc + n;
-              if constexpr (kBytes == 4) reinterpret_cast<uint32_t*>(c)[at] = *reinterpret_cast<const uint32_t*>(from);
-              else reinterpret_cast<uint16_t*>(c)[at] = *reinterpret_cast<const uint16_t*>(from);
+          // Rows that no 16-byte stores fit: two bf16 at once where they are even, single
+          // values where not; eight reads of LDS in flight (4100 x 4500 x 528: 80 us one by
+          // one, 45 by twos; 4100 x 4501 x 528 57).
+          const auto narrow = [&](auto word) __attribute__((always_inline)) {
+            using Word = decltype(word);
+            constexpr int kPlaces = kRowBytes / (int)sizeof(Word), kValues = (int)sizeof(Word) / kBytes;
+#pragma unroll 8
+            for (int u = 0; u < 32 * kPlaces / 64; ++u) {
+              const int r = (u * 64 + lane) / kPlaces, cc = (u * 64 + lane) % kPlaces * kValues, n = cn0 + cc;
+              const Word w = *reinterpret_cast<const Word*>(stage + r * kRowBytes + (((cc / kPer) ^ (r & kMask)) << 4) +
+                                                            cc % kPer * kBytes);
+              if (m0 + r < crows && n < ccols) *reinterpret_cast<Word*>(c + ((crow0 + m0 + r) * ldc + n) * kBytes) = w;
             }
-          }
+          };
+          if (kBytes == 4 || (ldc % 2 == 0 && (reinterpret_cast<uintptr_t>(c) & 3) == 0)) narrow(uint32_t{});
+          else if constexpr (kBytes == 2) narrow(uint16_t{});
         }
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -860,7 +873,7 @@ struct Tile {
     }
   }
 };
-constexpr int kForms = 10;
+constexpr int kForms = 11;
 template <typename Go>
 void by_form(int form, const Go& go) {
   switch (form) {
@@ -873,6 +886,7 @@ void by_form(int form, const Go& go) {
     case 6: return go(Tile<1, 2, 4>{});
     case 7: return go(Tile<2, 2, 2>{});
     case 8: return go(Tile<2, 2, 4>{});
+    case 9: return go(Tile<4, 2, 3>{});
     default: return go(Tile<4, 4, 2>{});
   }
 }
@@ -888,7 +902,7 @@ constexpr FormCost kCost[kForms] = {
     {0.22f, 0.105f, 0.2f, 1.0f, 5.0f}, {0.36f, 0.35f, 0.2f, 1.5f, 5.7f}, {0.52f, 0.50f, 0.2f, 1.5f, 5.2f},
     {0.50f, 0.50f, 0.2f, 1.5f, 3.6f},  {0.66f, 0.66f, 0.2f, 1.5f, 4.0f}, {0.29f, 0.25f, 0.5f, 1.7f, 4.5f},
     {0.43f, 0.43f, 1.0f, 1.6f, 5.0f},  {0.81f, 0.53f, 1.0f, 1.6f, 3.4f}, {0.60f, 0.60f, 2.0f, 1.4f, 4.6f},
-    {1.45f, 1.45f, 4.0f, 1.15f, 2.5f}};
+    {0.80f, 0.88f, 5.0f, 1.4f, 3.2f},  {1.45f, 1.45f, 4.0f, 1.15f, 2.5f}};
 
 }  // namespace
 
@@ -920,8 +934,9 @@ hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream) {
 // against each form forced (us; rows x n x k, form chosen first): 16 x 28672 x 4096
 // narrow 22, 64 x 128 tiles 24, 256 x 256 49; 64 x 4096 x 14336 64 x 64 tiles in 4
 // parts 18, narrow 30, whole 36; 256 x 4096 x 14336 128 x 128 in 4 parts 32, whole
-// 67; 512 x 28672 x 4096 256 x 256 69, 128 x 128 83; 2048 x 4096 x 4096 128 x 128,
-// two a compute unit, 40, 256 x 256 56. It goes by sizes alone, not by how the rows
+// 67; 256 x 28672 x 4096 256 x 128 39, 128 x 128 51, 256 x 256 54; 512 x 14336 x 4096
+// 256 x 128 34, 128 x 128 46, 256 x 256 51; 512 x 28672 x 4096 256 x 256 64, 256 x 128
+// 69, 128 x 128 90; 2048 x 4096 x 4096 128 x 128, two a compute unit, 40, 256 x 256 56. It goes by sizes alone, not by how the rows
 // fall to the groups, so that a call's workspace does not depend on it.
 struct Int8Choice {
   int32_t form, parts;

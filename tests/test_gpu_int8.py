@@ -135,9 +135,11 @@ def test_product(gpu_lib, m, n, k):
 # each kernel form once more at a size that takes it, whole and with k shared out
 # over workgroups (those need a workspace): rows per group, n, k
 FORMS = [([130], 6000, 64), ([67, 0, 133], 6000, 64), ([200], 6000, 272), ([100, 40, 60], 6000, 272), ([400], 12000, 144),
-         ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144), ([896, 1409], 16000, 512)]
+         ([12], 11500, 144), ([24], 11000, 272), ([1, 300, 99], 12000, 144), ([896, 1409], 16000, 512), ([1000], 4501, 272),
+         ([400, 0, 600], 4500, 400), ([400, 0, 600], 4500, 528), ([1000], 4501, 1040), ([400, 0, 600], 4500, 1168),
+         ([400, 0, 600], 4500, 1296)]
 SHARED = [([130], 100, 8192), ([130], 101, 8192), ([60, 0, 140], 1030, 4112), ([200], 2050, 4112), ([200], 2051, 4112),
-          ([130, 170, 100], 6000, 4112), ([3, 0, 0, 5], 48, 16384)]
+          ([130, 170, 100], 6000, 4112), ([3, 0, 0, 5], 48, 16384), ([200], 4500, 8192), ([200], 5120, 13824)]
 # ... and for the tiles of the last round alone
 TAILS = [([4000], 4300, 4096), ([1000, 0, 3100], 4301, 2064), ([4100], 4096, 4096), ([1920, 2177], 6000, 4096)]
 
@@ -283,7 +285,8 @@ def _mlp_ref(x, probs, w, sizes):
 
 
 MLPS = [([70, 0, 60], 8192, 64), ([130], 64, 8192), ([1], 32, 32), ([3, 0, 2], 64, 96), ([0, 40, 1, 33], 96, 160),
-        ([130, 0, 257], 256, 224), ([600, 700], 128, 256), ([1] * 16, 288, 64), ([2300], 4096, 3712), ([1500, 0, 2600], 4096, 2176)]
+        ([130, 0, 257], 256, 224), ([600, 700], 128, 256), ([1] * 16, 288, 64), ([2300], 4096, 3712), ([1500, 0, 2600], 4096, 2176),
+        ([400, 0, 600], 288, 2272), ([400, 0, 600], 1056, 2272)]
 
 
 @pytest.mark.parametrize("sizes,H,F", MLPS)
