@@ -862,7 +862,8 @@ MX_API mx_status mx_moe_route_bwd(const void* logits, mx_dtype logits_dtype, con
  *   workspace     mx_moe_balance_sizes bytes (0 for short calls; then it may be
  *                 NULL), 256-byte aligned.
  * Sums are kept in 64 bits, in one order for a given shape, so results repeat
- * bit for bit. Logits of +inf are outside the contract.
+ * bit for bit. A logit of +inf whose expert is open makes its token's p NaN, and
+ * with it the loss and the means of its sequence and the token's gradient.
  *
  * mx_moe_balance_bwd -- gradient for the logits:
  *     A_e = dloss num_experts counts_e / (topk n) + dmean_prob_e

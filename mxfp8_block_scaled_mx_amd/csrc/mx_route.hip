@@ -313,7 +313,8 @@ __device__ __forceinline__ float exp_below(float x) {
 }
 
 // The row's softmax over the open experts (0 for shut ones, and for all where
-// none is open).
+// none is open; NaN for all where one is +inf: that expert's inf - inf counts as 0
+// in exp_below and so do the others, so the sum, at least 1 otherwise, is 0).
 template <int G, int V>
 __device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) {
   float zm = z[0];
@@ -327,7 +328,7 @@ __device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) 
     sum += p[v];
   }
   sum = group_sum<G>(sum);
-  const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+  const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : zm > kShut ? __builtin_nanf("") : 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] *= inv;
 }
