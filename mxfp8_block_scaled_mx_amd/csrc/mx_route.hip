@@ -29,7 +29,8 @@ constexpr float kShut = -__builtin_inff();
 
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(v), __float_as_int(v), CTRL, 0xF, 0xF, false));
+  // (with the bound control the move folds into the operation that takes it)
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 // The lane's value combined with that of lane ^ 1, ^ 2, then of the mirrored
 // half row and row (the four, and then eight, lanes agree by then), then of
@@ -302,7 +303,7 @@ __device__ __forceinline__ void open_logits(const uint32_t (&w)[V], const float 
   }
 }
 
-// e^x for x <= 0, good to two half steps: 2^t with t = x log2(e) rounded, times 1 + r
+// e^x for x <= 0 (0 for NaN), good to two half steps: 2^t with t = x log2(e) rounded, times 1 + r
 // ln 2 with r what the rounding left out (the hardware's 2^t alone would be off by
 // |x| half steps more).
 __device__ __forceinline__ float exp_below(float x) {
@@ -312,23 +313,31 @@ __device__ __forceinline__ float exp_below(float x) {
   return fmaf(e, r * kLn2, e);
 }
 
-// The row's softmax over the open experts (0 for shut ones, and for all where
-// none is open; NaN for all where one is +inf: that expert's inf - inf counts as 0
-// in exp_below and so do the others, so the sum, at least 1 otherwise, is 0).
+// The row's softmax over the open experts before it is divided by its sum: e^(z -
+// max), 0 for shut experts (-inf less the maximum, or less -inf, which is NaN).
 template <int G, int V>
-__device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) {
+__device__ __forceinline__ float row_exps(const float (&z)[V], float (&e)[V]) {
   float zm = z[0];
 #pragma unroll
   for (int v = 1; v < V; ++v) zm = fmaxf(zm, z[v]);
   zm = group_max<G>(zm);
+#pragma unroll
+  for (int v = 0; v < V; ++v) e[v] = exp_below(z[v] - zm);
+  return zm;
+}
+// 1 over the sum, which is at least 1 where an expert is open. Where none is: 0.
+// Where one is +inf: NaN (its inf - inf counts as 0 in exp_below, and so do the
+// others, so the sum is 0).
+__device__ __forceinline__ float over_sum(float sum, float zm) {
+  return sum > 0.f ? __builtin_amdgcn_rcpf(sum) : zm > kShut ? __builtin_nanf("") : 0.f;
+}
+template <int G, int V>
+__device__ __forceinline__ void row_softmax(const float (&z)[V], float (&p)[V]) {
+  const float zm = row_exps<G, V>(z, p);
   float sum = 0.f;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    p[v] = z[v] > kShut ? exp_below(z[v] - zm) : 0.f;
-    sum += p[v];
-  }
-  sum = group_sum<G>(sum);
-  const float inv = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : zm > kShut ? __builtin_nanf("") : 0.f;
+  for (int v = 0; v < V; ++v) sum += p[v];
+  const float inv = over_sum(group_sum<G>(sum), zm);
 #pragma unroll
   for (int v = 0; v < V; ++v) p[v] *= inv;
 }
@@ -463,9 +472,13 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a) {
 // Part blockIdx.x of sequence blockIdx.y; the last blockIdx.y of a call with
 // offsets takes the tokens before the first sequence and behind the last, whose
 // gradient is `add` alone.
-// A is made once a workgroup, in 64 bits, less its mean over the experts: since
-// the p of a row sum to 1 the gradient does not see the shift, and the
-// difference A_e - sum p A loses fewer bits.
+// A is made once a workgroup, in 64 bits, less the point between its least and its
+// largest value that is nearest to 0: since the p of a row sum to 1 the gradient
+// does not see the shift, equal A become 0, and no A gets larger than it was. (A
+// less its mean does where few experts outweigh the rest: with the gradient of sum
+// log P and one expert of P = 4e-14 the others' gradients were off by 400 times
+// their size.) sum p A is made twice, the second time from A less the first: what
+// is left of its error is relative to the differences, not to A.
 // 16383 bf16 tokens of 128 experts with another gradient to add: 10.4 us in 13
 // sequences of unlike lengths, 8.2 as one, for 12.6 MB that memory passes in 2.1;
 // 65536 tokens 17.5 (50 MB: 8.5). Bound by latency, as the forward; at 65536 also by
@@ -504,7 +517,8 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
   };
   fetch(u0);
   float A[V], bias[V];
-  double c[V], sum = 0.0;
+  double c[V];
+  float least = __builtin_inff(), most = -__builtin_inff();
   const int sc = gap ? 0 : s;
   const double per = 1.0 / ((double)a.topk * (double)n), per_token = per * a.topk;
   const double f = a.dloss != nullptr ? (double)a.dloss[sc] * E * per : 0.0;
@@ -514,26 +528,43 @@ __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
     bias[v] = a.bias != nullptr ? a.bias[min(e0 + v, E - 1)] : 0.f;
     c[v] = a.dloss != nullptr ? f * (double)a.counts[at] : 0.0;
     if (a.dmean_prob != nullptr) c[v] += (double)a.dmean_prob[at];
-    if (e0 + v < E) sum += c[v];
+    if (e0 + v < E) {
+      least = fminf(least, (float)c[v]);
+      most = fmaxf(most, (float)c[v]);
+    }
   }
-  const double mean = (double)(group_sum<G>((float)sum) / (float)E);
+  const double shift = (double)fmaxf(-group_max<G>(-least), fminf(group_max<G>(most), 0.f));
 #pragma unroll
-  for (int v = 0; v < V; ++v) A[v] = e0 + v < E && !gap ? (float)((c[v] - mean) * per_token) : 0.f;
+  for (int v = 0; v < V; ++v) A[v] = e0 + v < E ? (float)((c[v] - shift) * per_token) : 0.f;
   for (int64_t u = u0; u < u1; u += U * N) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int64_t uc = u + mine + i * N, t = uc < skip_at ? uc : uc + skip;
       if (u + i * N >= u1) break;                         // (uniform)
-      float z[V], p[V], out[V];
-      open_logits<V, F32, VEC>(w[i], bias, e0, E, z);
-      row_softmax<G, V>(z, p);
-      float dot = 0.f;
+      float out[V];
 #pragma unroll
-      for (int v = 0; v < V; ++v) dot += p[v] * A[v];
-      dot = group_sum<G>(dot);
+      for (int v = 0; v < V; ++v) out[v] = a.add != nullptr ? value_of<V, F32, VEC>(d[i], v) : 0.f;
+      if (!gap) {
+        float z[V], p[V], b[V];
+        open_logits<V, F32, VEC>(w[i], bias, e0, E, z);
+        const float zm = row_exps<G, V>(z, p);
+        float sum = 0.f, dot = 0.f, rest = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)                         // in a gap A and so the sum is 0, whatever its logits are
-        out[v] = (a.add != nullptr ? value_of<V, F32, VEC>(d[i], v) : 0.f) + (gap ? 0.f : p[v] * (A[v] - dot));
+        for (int v = 0; v < V; ++v) {
+          sum += p[v];
+          dot = fmaf(p[v], A[v], dot);
+        }
+        const float inv = over_sum(group_sum<G>(sum), zm);
+        dot = group_sum<G>(dot) * inv;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          b[v] = A[v] - dot;
+          rest = fmaf(p[v], b[v], rest);
+        }
+        rest = group_sum<G>(rest) * inv;
+#pragma unroll
+        for (int v = 0; v < V; ++v) out[v] += p[v] * inv * (b[v] - rest);
+      }
       if (uc < u1 && e0 < E) store_values<V, F32>(a.dlogits, t * E + e0, E - e0, VEC, out);
     }
     if (u + U * N < u1) fetch(u + U * N);

@@ -1,8 +1,12 @@
 """Values at the border of what the balance loss (mx_moe_balance,
-mx_moe_balance_bwd) takes: what is not finite shows, and only where it belongs."""
+mx_moe_balance_bwd) takes: what is not finite shows, and only where it belongs;
+gradients of the means that are far apart, or that share a large part."""
 import numpy as np
 import pytest
 import torch
+
+from tests import balance_ref as ref
+from tests import decode_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +49,54 @@ def test_infinite_logits_show(gpu_lib, T, E, dtype):
         shut = z.clone()
         shut[:, 0] = float("inf")
         assert all(torch.equal(x, y) for x, y in zip(run(shut, b), run(z, b)))
+
+
+def _gradient(z, dm, segments):
+    """dlogits of the means' gradients dm in 64 bits, and its bound, with the p and
+    their relative bounds r of balance_ref. a = A - c, rounded once, with c the point
+    between the least and the largest A that is nearest to 0: the softmax does not
+    see it, equal A become 0, and |a| <= |A|. With b = a - dot the sum over p b has
+    p's errors, b's and a product's rounding and at most 9 additions, so whatever
+    dot's error was, what is left of it is relative to sum p |b|; a difference and
+    a product round after that."""
+    u = ref.U
+    p, r = ref.probs(z, None)
+    dz, bound = np.zeros_like(z), np.zeros_like(z)
+    for s, (b, e) in enumerate(ref.spans(segments, len(z))):
+        A = dm[s] / max(1, e - b)
+        a = (A - np.clip(0, A.min(), A.max()))[None]
+        pp, rr = p[b:e], r[b:e]
+        diff = a - (pp * a).sum(1, keepdims=True)
+        off = (pp * (u * np.abs(a) + (rr + 11 * u) * np.abs(diff))).sum(1, keepdims=True)
+        dz[b:e] = pp * diff
+        bound[b:e] = 1.01 * pp * ((rr + 3 * u) * np.abs(diff) + u * np.abs(a) + off)
+    return dz, bound
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E", [5, 8, 60, 128])
+@pytest.mark.parametrize("kind", ["rare", "rare and positive", "rare with offset", "offset", "negative offset"])
+def test_gradients_of_means_far_apart(gpu_lib, E, kind, dtype):
+    """The gradient of sum log mean_prob, where one expert's mean is next to
+    nothing and its gradient that much larger than the others'; and gradients that
+    share a part a thousand times what differs."""
+    T, o = 300, [0, 170, 300]
+    gen = torch.Generator().manual_seed(E)
+    z = torch.randn((T, E), generator=gen)
+    if "rare" in kind:
+        z[:170, 3] -= 22.0
+    z = z.to(dtype).cuda()
+    seg = torch.tensor(o, dtype=torch.int32, device="cuda")
+    mean = gpu_lib.mx_moe_balance(z, gpu_lib.mx_moe_route(z, 2)[0], segments=seg)[2]
+    if "rare" in kind:
+        assert mean[0, 3] < 1e-8
+        dm = 1 / (E * mean) if "positive" in kind else -1 / (E * mean)
+        if "offset" in kind:
+            dm = dm + 1000.0
+    else:
+        dm = torch.randn((2, E), generator=gen).cuda() + (1000.0 if kind == "offset" else -1000.0)
+    dz = gpu_lib.mx_moe_balance_bwd(z, None, 2, dmean_prob=dm, segments=seg)
+    want, bound = _gradient(decode_ref.f64(z), decode_ref.f64(dm), o)
+    if dtype == torch.bfloat16:
+        bound = bound + decode_ref.BF16_HALF * (np.abs(want) + bound)
+    assert np.all(np.abs(decode_ref.f64(dz) - want) <= bound + 1e-37)
