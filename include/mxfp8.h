@@ -932,6 +932,19 @@ MX_API mx_status mx_moe_balance_bwd(const void* logits, mx_dtype logits_dtype, c
  * 16-byte, others by element), MX_EWORKSPACE, MX_EUNSUPPORTED (groups > MX_MAX_GROUPS, m or n >
  * 2^30, k > 131071, too many tiles), MX_EHIP.
  *
+ * mx_gemm_int8_plan -- how a product of these sizes runs, for tests and
+ * measurements (one call with groups 1 and no sizes as mx_gemm_int8; group_sizes
+ * on the host as mx_grouped_gemm_int8, NULL with more groups as _device_split;
+ * swiglu: the MLP's first product, n counts gate and up rows). Which sizes run how
+ * may change; the result does not depend on it. No device is touched.
+ *   tile_rows, tile_cols  of a workgroup, rows of A by rows of B; 0 for an empty
+ *                product, then so is the rest.
+ *   waves, stages  of a workgroup, and its stages of 128 k in LDS.
+ *   k_parts        workgroups that share out a tile's k (sums in the workspace).
+ *   last_round     1 if those of the last, partial round of tiles may (device
+ *                  sizes) or do (host sizes).
+ *   nontemporal    1 if weights are loaded nontemporally.
+ *
  * grouped_mlp_fwd_int8 -- the MoE MLP (article item 3) for inference on int8
  * weights: for expert e and its rows, w the row's routing weight,
  *     [g | u] = W1_e Q(x);  A = silu(g) u (fp32);  y = w W2_e Q(A)
@@ -953,6 +966,11 @@ MX_API mx_status mx_quantize_int8(const void* x, mx_dtype x_dtype, int64_t x_row
                                   const int32_t* row_index, int64_t rows, const float* row_weight, int8_t* q,
                                   float* s, void* stream);
 MX_API mx_status mx_gemm_int8_sizes(int64_t m, int64_t n, int64_t k, int32_t groups, size_t* workspace);
+typedef struct mx_int8_plan {
+  int32_t tile_rows, tile_cols, waves, stages, k_parts, last_round, nontemporal;
+} mx_int8_plan;
+MX_API mx_status mx_gemm_int8_plan(int64_t m, int64_t n, int64_t k, int32_t groups, const int64_t* group_sizes,
+                                   int32_t swiglu, mx_int8_plan* plan);
 MX_API mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m,
                               int64_t n, int64_t k, void* c, mx_dtype c_dtype, void* workspace,
                               size_t workspace_bytes, void* stream);

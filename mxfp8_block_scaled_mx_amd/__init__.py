@@ -21,6 +21,7 @@ calls return has no history, also where an input requires a gradient.
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import functools
 import os
@@ -35,7 +36,7 @@ __all__ = [
     "mx_gemv_fp4", "mx_gemv_nvfp4", "gemv_workspace_bytes", "grouped_mlp_decode", "mlp_decode_workspace_bytes",
     "mx_moe_route", "mx_moe_route_bwd", "MoERoute", "mx_moe_balance", "mx_moe_balance_bwd", "MoEBalance",
     "moe_balance_workspace_bytes", "mx_quantize_int8", "mx_gemm_int8", "mx_grouped_gemm_int8", "grouped_mlp_fwd_int8",
-    "gemm_int8_workspace_bytes", "mlp_int8_workspace_bytes",
+    "gemm_int8_workspace_bytes", "gemm_int8_plan", "mlp_int8_workspace_bytes",
 ]
 
 FWD_STAGES = ("quantize_x", "quantize_w1", "quantize_w2", "gemm1_swiglu", "gemm2")
@@ -190,6 +191,8 @@ def load() -> ctypes.CDLL:
     L.mx_quantize_int8.argtypes = [vp, i32, i64, i64, i64, vp, i64, vp, vp, vp, vp]
     L.mx_gemm_int8_sizes.restype = ctypes.c_int
     L.mx_gemm_int8_sizes.argtypes = [i64, i64, i64, i32, ctypes.POINTER(sz)]
+    L.mx_gemm_int8_plan.restype = ctypes.c_int
+    L.mx_gemm_int8_plan.argtypes = [i64, i64, i64, i32, p64, i32, ctypes.POINTER(ctypes.c_int32 * 7)]
     L.mx_gemm_int8.restype = ctypes.c_int
     L.mx_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, i32, vp, sz, vp]
     L.mx_grouped_gemm_int8.restype = ctypes.c_int
@@ -1345,6 +1348,21 @@ def gemm_int8_workspace_bytes(m: int, n: int, k: int, groups: int = 1) -> int:
     nbytes = ctypes.c_size_t()
     _check(load().mx_gemm_int8_sizes(m, n, k, _i32(groups), ctypes.byref(nbytes)))
     return nbytes.value
+
+
+Int8Plan = collections.namedtuple("Int8Plan", "tile_rows tile_cols waves stages k_parts last_round nontemporal")
+
+
+def gemm_int8_plan(m: int, n: int, k: int, groups: int = 1, group_sizes=None, swiglu: bool = False) -> Int8Plan:
+    """How an 8-bit integer product of these sizes runs (mx_gemm_int8_plan), for
+    tests and measurements: group_sizes a list, or None for mx_gemm_int8 and for
+    sizes on the device; swiglu: the MLP's first product, n its gate and up rows."""
+    if group_sizes is not None and len(group_sizes) != groups:
+        raise ValueError(f"gemm_int8_plan: group_sizes must be {groups} counts")
+    sizes = None if group_sizes is None else (ctypes.c_int64 * max(1, groups))(*group_sizes)
+    plan = (ctypes.c_int32 * 7)()
+    _check(load().mx_gemm_int8_plan(m, n, k, _i32(groups), sizes, int(swiglu), ctypes.byref(plan)))
+    return Int8Plan(*plan)
 
 
 def _int8_scratch(who, workspace, nbytes, dev, stream):

@@ -2258,6 +2258,25 @@ mx_status mx_gemm_int8_sizes(int64_t m, int64_t n, int64_t k, int32_t groups, si
   return MX_OK;
 }
 
+mx_status mx_gemm_int8_plan(int64_t m, int64_t n, int64_t k, int32_t groups, const int64_t* group_sizes,
+                            int32_t swiglu, mx_int8_plan* plan) {
+  g_err[0] = 0;
+  const char* who = "mx_gemm_int8_plan";
+  if (!plan) return fail(MX_EINVAL, "%s: null plan", who);
+  static const int64_t unread = 0;
+  mx::Int8GemmArgs g{};
+  mx::Int8Plan p;
+  mx_status st = int8_groups(who, group_sizes ? group_sizes : &unread, !group_sizes, groups, m, &g);
+  if (st != MX_OK) return st;
+  if (groups == 1 && !group_sizes) g.split = mx::kInt8OneGroup;
+  if (swiglu && n % 2) return fail(MX_ESHAPE, "%s: gate and up rows come in pairs", who);
+  if ((st = int8_shape(who, swiglu ? mx::kInt8ToSwiglu : mx::kInt8ToBf16, n, k, &g, &p)) != MX_OK) return st;
+  mx::Int8Run r{};
+  if (p.tiles > 0) r = mx::describe_gemm_int8(g, p);
+  *plan = mx_int8_plan{r.tile_rows, r.tile_cols, r.waves, r.stages, r.k_parts, r.last_round, r.nontemporal};
+  return MX_OK;
+}
+
 mx_status mx_gemm_int8(const int8_t* a, const float* a_s, const int8_t* b, const float* b_s, int64_t m, int64_t n,
                        int64_t k, void* c, mx_dtype c_dtype, void* workspace, size_t workspace_bytes, void* stream) {
   g_err[0] = 0;

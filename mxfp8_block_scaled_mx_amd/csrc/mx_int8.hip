@@ -845,7 +845,7 @@ __global__ __launch_bounds__(64 * W) void gemm_int8_narrow_kernel(Int8GemmArgs a
 // The forms of a product.
 template <int MT, int NT, int W>
 struct Narrow {
-  static constexpr int kBM = 16 * MT, kBN = 16 * NT, kThreads = 64 * W, kWaves = W;
+  static constexpr int kBM = 16 * MT, kBN = 16 * NT, kThreads = 64 * W, kWaves = W, kStages = 3;
   static constexpr bool kPairs = NT == 2, kSums = false;
   template <int EPI>
   static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
@@ -857,7 +857,7 @@ struct Narrow {
 };
 template <int MI, int NI, int S>
 struct Tile {
-  static constexpr int kBM = 64 * MI, kBN = 64 * NI, kThreads = 256, kWaves = 1;
+  static constexpr int kBM = 64 * MI, kBN = 64 * NI, kThreads = 256, kWaves = 1, kStages = S;
   static constexpr bool kPairs = NI % 2 == 0, kSums = true;
   template <int EPI>
   static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
@@ -1031,13 +1031,29 @@ Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a) {
   return best;
 }
 
+// The narrow forms load weights nontemporally where rows of k begin on cache lines
+// (with k no multiple of 128 two steps share a line, and two rows do). This goes by
+// k alone: where a group has several m-tiles its weights are read as often, past
+// the caches too.
+bool nontemporal_int8(const Int8GemmArgs& a) { return a.K % kBK == 0; }
+
+Int8Run describe_gemm_int8(const Int8GemmArgs& a, const Int8Plan& p) {
+  Int8Run r{};
+  by_form(p.form, [&](auto f) {
+    using Form = decltype(f);
+    r = Int8Run{Form::kBM, Form::kBN, Form::kThreads / 64, Form::kStages, p.parts, p.tail,
+                !Form::kSums && nontemporal_int8(a)};
+  });
+  return r;
+}
+
 hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan& p, void* workspace, hipStream_t stream) {
   Int8GemmArgs a = args;
   a.n_tiles = (int32_t)p.n_tiles;
   a.parts = p.parts;
   a.tail = p.tail;
   a.planes = reinterpret_cast<int32_t*>(workspace);
-  a.once = a.K % kBK == 0;
+  a.once = nontemporal_int8(a);
   if (p.tiles == 0) return hipSuccess;
   by_form(p.form, [&](auto s) {
     using S = decltype(s);

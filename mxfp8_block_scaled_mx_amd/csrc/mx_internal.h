@@ -413,7 +413,7 @@ struct Int8GemmArgs {
   int32_t M, N, K, groups, split;
   const int64_t* sizes_dev;
   int32_t sizes[kMaxGroups];
-  int32_t n_tiles, parts, tail, once;   // set by the launch, as is
+  int32_t n_tiles, parts, tail, once;   // set by the launch (once: nontemporal weights, narrow forms), as is
   int32_t* planes;                  // sums: [parts, M, N] (parts > 1), or tiles of the tail's
 };
 enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2, kInt8ToSums = 3 };
@@ -427,6 +427,11 @@ struct Int8Plan {
 };
 constexpr int64_t kInt8MaxTiles = ((int64_t)1 << 24) - 1;
 Int8Plan plan_gemm_int8(int result, const Int8GemmArgs& a);
+// The same in the terms of the kernels: mx_int8_plan's fields, in order.
+struct Int8Run {
+  int32_t tile_rows, tile_cols, waves, stages, k_parts, last_round, nontemporal;
+};
+Int8Run describe_gemm_int8(const Int8GemmArgs& a, const Int8Plan& p);
 hipError_t launch_gemm_int8(int result, const Int8GemmArgs& a, const Int8Plan& p, void* workspace, hipStream_t stream);
 
 constexpr int kTileM = 256;
