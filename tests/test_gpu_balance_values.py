@@ -1,6 +1,7 @@
 """Values at the border of what the balance loss (mx_moe_balance,
 mx_moe_balance_bwd) takes: what is not finite shows, and only where it belongs;
-gradients of the means that are far apart, or that share a large part."""
+gradients of the means that are far apart, or that share a large part; the
+exponential over its range."""
 import numpy as np
 import pytest
 import torch
@@ -100,3 +101,20 @@ def test_gradients_of_means_far_apart(gpu_lib, E, kind, dtype):
     if dtype == torch.bfloat16:
         bound = bound + decode_ref.BF16_HALF * (np.abs(want) + bound)
     assert np.all(np.abs(decode_ref.f64(dz) - want) <= bound + 1e-37)
+
+
+def test_probabilities_over_the_range(gpu_lib):
+    """Tokens of their own sequences with logits 0 and -x: the mean is p = e / (1 +
+    e) itself. e = exp(-x) is good to three half steps (the difference to the
+    maximum is exact), 1 + e rounds once, the reciprocal is good to two and the
+    product to one: 7 for p, and e's again by its share of the sum. Results below
+    2^-126 may be 0."""
+    S = 60000
+    x = torch.linspace(0, 120, S, dtype=torch.float32)
+    z = torch.stack([torch.zeros(S), -x], 1).cuda()
+    seg = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    mean = decode_ref.f64(gpu_lib.mx_moe_balance(z, gpu_lib.mx_moe_route(z, 1)[0], segments=seg)[2])
+    e = np.exp(-x.double().numpy())
+    p = e / (1 + e)
+    assert np.all(np.abs(mean[:, 1] - p) <= 1.001 * (7 + 3 * p) * ref.U * p + 2.0 ** -126)
+    assert np.all(np.abs(mean[:, 0] - (1 - p)) <= 1.001 * (4 + 3 * p) * ref.U)
