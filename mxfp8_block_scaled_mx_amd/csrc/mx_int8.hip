@@ -73,10 +73,10 @@ __device__ __forceinline__ uint2 eight_codes(const Eight<F32>& w, float top, flo
 
 // L lanes a row (a wave, or the workgroup's four), C pieces of 8 values a lane in
 // registers as they were read, so that memory is passed over once; C == 0: any
-// number of pieces, read twice. Bound by memory: 16384 x 4096 bf16 in 35 us, 5.75
-// TB/s read and written (33 us gathered from 8192 rows), 8192 x 14336 fp32 in 107 us,
-// 5.5 TB/s, where a copy reaches 5.95. With a branch per value for those beside a
-// half 38, 34 and 112 us.
+// number of pieces, read twice. Bound by memory, inputs that no cache holds: 16384 x
+// 4096 bf16 in 36 us, 5.6 TB/s read and written (32 us gathered from 8192 rows), 8192 x
+// 14336 bf16 in 67.5, 5.2, fp32 in 107, 5.5, where a copy reaches 5.95. With a branch
+// per value for those beside a half 38, 34 (gathered), 79 and 112 us.
 template <bool F32, int L, int C>
 __global__ __launch_bounds__(256) void quantize_int8_kernel(QuantInt8Args a) {
   __shared__ uint32_t tops[4];
@@ -306,10 +306,10 @@ __device__ __forceinline__ void bare_barrier() {
 // steps, that leave the sums themselves, in 32 bits, to planes of their own.
 //
 // 256 x 256 tiles, 8191 x 4096 x 14336: 375 to 385 us, 2.5 to 2.6 POP/s, where a large
-// library product of the same format reaches 2.4. The matrix cores are busy 69 to 73%
+// library product of the same format reaches 2.4. The matrix cores are busy 68 to 73%
 // of the cycles, no read of LDS meets a bank conflict, and the clock falls to 1.7 GHz
 // under this load (all zeros, which draw less power, take 281 us): power bounds it.
-// 8192 rows of 8 unlike groups by 28672 x 4096: 950 us, 2.0 POP/s (the library on one
+// 8192 rows of 8 unlike groups by 28672 x 4096: 920 us, 2.1 POP/s (the library on one
 // group: 2.1). Some 6% of it are rows that tiles have too many; k is shorter, so each
 // tile's first loads and its results, which nothing hides, weigh more.
 template <int TI, int NI, int S, int EPI, bool TAIL>
@@ -707,28 +707,28 @@ __global__ __launch_bounds__(256) void int8_tail_join_kernel(Int8GemmArgs a) {
   }
 }
 
-// Few rows: the weights pass once and bound the time, so what counts is that many
-// loads are always in flight. A workgroup owns 16 NT rows of B and 16 MT of A; its
+// Few rows: the weights pass once (where a group has one m-tile) and bound the
+// time, so what counts is that many loads are always in flight. A workgroup owns 16 NT rows of B and 16 MT of A; its
 // W waves share the steps of 128 k among them, each a run of its own, with a ring of
 // three stages of its own in LDS that only it fills and reads, two steps ahead,
 // without a barrier. The waves' sums meet in LDS at the end; sums of
 // integers are the same in any order.
 // Rows and k out of range read as zeros, as above. With the SwiGLU (NT = 2) the
 // second 16 rows of B are the up rows of the first 16's channels.
-// Bound by reading: 16 x 28672 x 4096 in 22 us, 117 MB at 5.3 TB/s of the 6.9 that
+// Bound by reading: 16 x 28672 x 4096 in 22.5 us, 117 MB at 5.2 TB/s of the 6.9 that
 // reading alone reaches (the ramp of a launch and of the first loads is 3 us of it);
-// 16 x 4096 x 14336 12.8, 1 x 999 x 544 2.7 (a launch is 2.2). Steps dealt out in
+// 16 x 4096 x 14336 12.9, 1 x 999 x 544 2.7 (a launch is 2.2). Steps dealt out in
 // turn, not in runs, 23.8 for the first; weights by ordinary instead of nontemporal
 // loads 25.8 then. XCDs that start at 8 places of k, as the tiles' do, take 15.4
 // instead of 12.9 for the second.
-template <int MT, int NT, int W, int EPI, bool ONCE>
+template <int MT, int NT, int W, int EPI, bool NONTEMPORAL>
 __global__ __launch_bounds__(64 * W) void gemm_int8_narrow_kernel(Int8GemmArgs a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr bool kPair = EPI == kInt8ToSwiglu;
   static_assert(!kPair || NT == 2, "16 gate and 16 up rows");
   constexpr int BM = 16 * MT, TN = 16 * NT, kStage = (BM + TN) * kBK, kLoads = (BM + TN) / 8;
   static_assert(W * kStage >= 4 * W * BM * TN, "the sums fit a stage");
-  constexpr int kAux = ONCE ? 2 : 0;                       // non-temporal
+  constexpr int kAux = NONTEMPORAL ? 2 : 0;
   __shared__ __attribute__((aligned(16))) uint8_t s0[W * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t s1[W * kStage];
   __shared__ __attribute__((aligned(16))) uint8_t s2[W * kStage];
@@ -854,7 +854,7 @@ struct Narrow {
   template <int EPI>
   static void launch(dim3 grid, hipStream_t s, const Int8GemmArgs& a) {
     if constexpr (EPI != kInt8ToSums && (EPI != kInt8ToSwiglu || kPairs)) {
-      if (a.once) hipLaunchKernelGGL((gemm_int8_narrow_kernel<MT, NT, W, EPI, true>), grid, dim3(kThreads), 0, s, a);
+      if (a.nontemporal) hipLaunchKernelGGL((gemm_int8_narrow_kernel<MT, NT, W, EPI, true>), grid, dim3(kThreads), 0, s, a);
       else hipLaunchKernelGGL((gemm_int8_narrow_kernel<MT, NT, W, EPI, false>), grid, dim3(kThreads), 0, s, a);
     }
   }
@@ -922,7 +922,7 @@ hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream) {
     // A row on a wave while its values take 4 pieces, so that no barrier stands
     // between its loads and its stores; longer ones on the workgroup (16384 x 4096
     // bf16 35 us, on a wave 39; 33 rows 4.0 and 7.6; 16384 x 2048 on a wave 19.6, on
-    // the workgroup 22.9).
+    // the workgroup 22.9: two inputs in turn).
     if (a.cols <= 64 * 8) go(f32, integral_constant<int, 64>{}, integral_constant<int, 1>{});
     else if (a.cols <= 64 * 8 * 4) go(f32, integral_constant<int, 64>{}, integral_constant<int, 4>{});
     else if (a.cols <= 256 * 8 * 2) go(f32, integral_constant<int, 256>{}, integral_constant<int, 2>{});
@@ -935,13 +935,27 @@ hipError_t launch_quantize_int8(const QuantInt8Args& a, hipStream_t stream) {
 }
 
 // The form and the number of parts that the figures above make cheapest. Checked
-// against each form forced (us; rows x n x k, form chosen first): 16 x 28672 x 4096
-// narrow 22, 64 x 128 tiles 24, 256 x 256 49; 64 x 4096 x 14336 64 x 64 tiles in 4
-// parts 18, narrow 30, whole 36; 256 x 4096 x 14336 128 x 128 in 4 parts 32, whole
-// 67; 256 x 28672 x 4096 256 x 128 39, 128 x 128 51, 256 x 256 54; 512 x 14336 x 4096
-// 256 x 128 34, 128 x 128 46, 256 x 256 51; 512 x 28672 x 4096 256 x 256 64, 256 x 128
-// 69, 128 x 128 90; 2048 x 4096 x 4096 128 x 128, two a compute unit, 40, 256 x 256 56. It goes by sizes alone, not by how the rows
-// fall to the groups, so that a call's workspace does not depend on it.
+// against forms forced, on one group (us; rows x n x k, the form chosen first, /p: k
+// shared out by p):
+//   16 x 28672 x 4096   16 x 32 22.7, 16 x 16 22.6, 64 x 128 23.9, 256 x 256 40
+//   30 x 4096 x 4096    32 x 16 6.8, 32 x 32 8.2, 16 x 32 8.3, 16 x 16 9.1, 64 x 64 11.3
+//   30 x 4096 x 4112    32 x 16 8.8, 16 x 32 9.6, 32 x 32 10.6, 64 x 64/2 12.0
+//   30 x 5000 x 2048    32 x 32 6.1, 32 x 16 6.9, 64 x 64 7.2, 16 x 16 7.8
+//   20 x 8192 x 2048    32 x 32 6.1, 32 x 16 6.8, 64 x 64 7.9, 16 x 32 8.5
+//   32 x 4096 x 14336   64 x 128/8 17.6, 32 x 16 17.0, 32 x 32 21.2, 64 x 64/2 23.2
+//   32 x 14336 x 4096   64 x 64 14.5, 32 x 32 16.3, 64 x 128 18.5, 32 x 16 19.1
+//   64 x 4096 x 14336   64 x 64/4 18.9, 32 x 32 24.7, 64 x 64 38
+//   256 x 4096 x 14336  128 x 128/4 32, 256 x 128/4 37, 128 x 128 71
+//   256 x 28672 x 4096  256 x 128 39, 128 x 128 50, 256 x 256 54
+//   512 x 14336 x 4096  256 x 128 36, 128 x 128 47, 256 x 256 53
+//   512 x 28672 x 4096  256 x 256 62, 256 x 128 69, 128 x 128 90
+//   2048 x 4096 x 4096  256 x 128 37, 128 x 128 (two a compute unit) 40, 256 x 256 53
+//   1024 x 4096 x 14336 128 x 128 73, 256 x 128/2 72, 256 x 256/4 77, 256 x 128 91
+// It goes by sizes alone, as if the rows fell evenly to the groups, so that a call's
+// workspace does not depend on how they do. For groups of few rows that is its weak
+// side: 8 groups by 28672 x 4096 with 8 rows each take 162 us in 16 x 16 (16 x 32
+// 147), with 5 to 30 rows 254 in 16 x 16 (64 x 64 163, and 32 x 32 203), with 128 in
+// one group 174 (64 x 128 31).
 struct Int8Choice {
   int32_t form, parts;
 };
@@ -1057,7 +1071,7 @@ hipError_t launch_gemm_int8(int result, const Int8GemmArgs& args, const Int8Plan
   a.parts = p.parts;
   a.tail = p.tail;
   a.planes = reinterpret_cast<int32_t*>(workspace);
-  a.once = nontemporal_int8(a);
+  a.nontemporal = nontemporal_int8(a);
   if (p.tiles == 0) return hipSuccess;
   by_form(p.form, [&](auto s) {
     using S = decltype(s);

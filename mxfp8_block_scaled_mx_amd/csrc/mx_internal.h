@@ -413,7 +413,7 @@ struct Int8GemmArgs {
   int32_t M, N, K, groups, split;
   const int64_t* sizes_dev;
   int32_t sizes[kMaxGroups];
-  int32_t n_tiles, parts, tail, once;   // set by the launch (once: nontemporal weights, narrow forms), as is
+  int32_t n_tiles, parts, tail, nontemporal;   // set by the launch, as is
   int32_t* planes;                  // sums: [parts, M, N] (parts > 1), or tiles of the tail's
 };
 enum Int8Result : int { kInt8ToBf16 = 0, kInt8ToF32 = 1, kInt8ToSwiglu = 2, kInt8ToSums = 3 };

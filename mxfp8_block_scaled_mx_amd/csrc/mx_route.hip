@@ -367,11 +367,12 @@ __device__ __forceinline__ void balance_results(const BalanceArgs& a, int s, int
 // results where a sequence is one part, else to the workspace. The sums are kept
 // in 64 bits: in 32 they would stand still past 2^24 tokens, and the few adds a
 // token hide behind its loads.
-// 16383 bf16 tokens of 128 experts, 8 choices, in 13 sequences of unlike lengths: 8.5
+// 16383 bf16 tokens of 128 experts, 8 choices, in 13 sequences of unlike lengths: 7.6
 // us of which 2 are the launch, for 4.7 MB that memory passes in 1: what bounds it is
 // the chain of offsets, rows, two reductions a row and the sum over the workgroup, and
-// the longest sequence's parts. 33 tokens: 4.8 us. As one sequence, with the join: 128
-// parts of 128 tokens 14.8 us, 256 of 64 13.6, 512 of 32 18.
+// the longest sequence's parts. 33 tokens: 4.6 us. As one sequence, with the join: 256
+// parts of 64 tokens 13.2 us; 128 of 128 took 1.2 more, 512 of 32 4.4 more. 65536
+// tokens in 512 parts: 25.1.
 template <int G, int V, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs a) {
   constexpr int N = 256 / G, U = 4;                       // tokens at a time, and rows of a lane in flight
@@ -482,10 +483,11 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(BalanceArgs a) {
 // log P and one expert of P = 4e-14 the others' gradients were off by 400 times
 // their size.) sum p A is made twice, the second time from A less the first: what
 // is left of its error is relative to the differences, not to A.
-// 16383 bf16 tokens of 128 experts with another gradient to add: 10.4 us in 13
-// sequences of unlike lengths, 8.2 as one, for 12.6 MB that memory passes in 2.1;
-// 65536 tokens 17.5 (50 MB: 8.5). Bound by latency, as the forward; at 65536 also by
-// 6 us of instructions (about 100 a row of two tokens, four cycles each).
+// 16383 bf16 tokens of 128 experts with another gradient to add: 10.2 us in 13
+// sequences of unlike lengths, 7.5 as one, for 12.6 MB that memory passes in 2.1;
+// 65536 tokens 17.1 (50 MB: 8.5), 15.3 without one to add. Bound by latency, as the
+// forward; at 65536 also by 9 us of instructions (about 180 a row of two tokens, four
+// cycles each), of which the second sum p A is 1.
 template <int G, int V, bool F32, bool VEC>
 __global__ __launch_bounds__(256) void balance_bwd_kernel(BalanceBwdArgs a) {
   constexpr int N = 256 / G, U = 4;
@@ -665,7 +667,7 @@ hipError_t launch_balance_bwd(const BalanceBwdArgs& args, hipStream_t stream) {
   by_shape(a.experts, [&](auto g_, auto v_) {
     constexpr int G = decltype(g_)::value, V = decltype(v_)::value, per = 256 / G;
     // four workgroups a compute unit: 16383 tokens of 128 experts in 13 sequences of
-    // unlike lengths 10.4 us, three 11.0; of like lengths 9.5 and 8.3
+    // unlike lengths 10.2 us, three 0.6 more; of like lengths three take 1.2 less
     const int64_t parts = std::max<int64_t>(1, std::min((a.tokens + per - 1) / per, (int64_t)((1024 + rows - 1) / rows)));
     const dim3 grid((unsigned)parts, (unsigned)rows);
     const auto go = [&](auto f32_, auto vec_) {
