@@ -708,11 +708,11 @@ __global__ __launch_bounds__(256) void int8_tail_join_kernel(Int8GemmArgs a) {
 }
 
 // Few rows: the weights pass once (where a group has one m-tile) and bound the
-// time, so what counts is that many loads are always in flight. A workgroup owns 16 NT rows of B and 16 MT of A; its
-// W waves share the steps of 128 k among them, each a run of its own, with a ring of
-// three stages of its own in LDS that only it fills and reads, two steps ahead,
-// without a barrier. The waves' sums meet in LDS at the end; sums of
-// integers are the same in any order.
+// time, so what counts is that many loads are always in flight. A workgroup owns 16
+// NT rows of B and 16 MT of A; its W waves share the steps of 128 k among them, each
+// a run of its own, with a ring of three stages of its own in LDS that only it fills
+// and reads, two steps ahead, without a barrier. The waves' sums meet in LDS at the
+// end; sums of integers are the same in any order.
 // Rows and k out of range read as zeros, as above. With the SwiGLU (NT = 2) the
 // second 16 rows of B are the up rows of the first 16's channels.
 // Bound by reading: 16 x 28672 x 4096 in 22.5 us, 117 MB at 5.2 TB/s of the 6.9 that
